@@ -89,6 +89,10 @@ typedef void *ttt_stream; /* a cudaStream_t */
                                loss and its gradient use them (the query is
                                used as given) */
 
+#define TTT_F_RMS 16u       /* ttt_join_*: RMSNorm instead of LayerNorm         */
+#define TTT_F_GATE_SIGMOID 32u /* ttt_join_*: act(gate) = sigmoid(gate) instead of
+                               SiLU, gate sigmoid(gate)                     */
+
 #define TTT_ABI_VERSION 1
 
 /* ABI version of the loaded library (TTT_ABI_VERSION at build time). */
@@ -449,6 +453,114 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
                                      float *W_end, int S, int H, int nseg, int d,
                                      long long seq_stride, long long seg_stride, unsigned flags,
                                      ttt_stream stream);
+
+/*
+ * Gated delta rule forward: the linear fast weight of ttt_linear_fwd without
+ * LayerNorm, taken online (b = 1: one gradient step per token, "The Dual-Loop
+ * Structure"), with a forget gate: the weight decays by exp(g_t) before the
+ * token's step.
+ *   Wd  = exp(g_t) W,   rho_t = v_t - k_t Wd,
+ *   W   = Wd + eta_t k_t^T rho_t,   z_t = q_scale * q_t W.
+ * With g = 0 and q_scale = 1 this is ttt_linear_fwd with b = 1 and no flags.
+ * Arguments:
+ *   Q, K      [B][Hk][T][dk], dtype dt: head h of the H value heads reads query
+ *             and key head h / (H / Hk) (H a multiple of Hk)
+ *   V         [B][H][T][dv], dtype dt
+ *   eta       [B][H][T] fp32, the step sizes
+ *   g         [B][H][T] fp32, log decays (0: keep, -inf: forget), or NULL: none
+ *   W0        [H][dk][dv] (or [N][H][dk][dv] with TTT_F_W0_PER_SEQ) fp32, or
+ *             NULL: zero
+ *   Z         [B][H][T][dv] output: fp32, or bf16 with TTT_F_Z_BF16
+ *   W_out     [N][H][dk][dv] fp32 output, the weight after the last token, or NULL
+ *   seq_start NULL: the B rows are the N = B sequences. Else packed sequences:
+ *             B = 1 and a device array of n_seq + 1 int32 offsets along T;
+ *             sequence n holds the tokens seq_start[n] .. seq_start[n+1] - 1
+ *             (none: its W_out is its start weight), N = n_seq. Offsets must
+ *             not decrease and lie in [0, T]; the host cannot see them, so the
+ *             kernels clamp them. Rows of Z outside every sequence are left as
+ *             they were.
+ * workspace: device memory of at least ttt_delta_workspace_bytes(...) bytes,
+ *   256-byte aligned, owned by the caller, clobbered. Calls that share one must
+ *   not overlap on the GPU (two captured graphs that may run at the same time
+ *   need one each). n_seq is 0 without seq_start.
+ * Supported: any T >= 1, dk and dv in {64, 128}, TTT_BF16 or TTT_FP32.
+ *   Deterministic. The weight, the sums over tokens and the decays are held
+ *   in fp32 (their products on the tensor cores take an fp32 operand as two
+ *   fp16 terms under a power-of-two scale, 22 significant bits); with
+ *   TTT_F_Z_BF16 the products that only Z depends on take one term.
+ * flags: TTT_F_W0_PER_SEQ, TTT_F_Z_BF16.
+ */
+TTT_API size_t ttt_delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,
+                                         ttt_dtype dt);
+TTT_API ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, const float *eta,
+                                 const float *g, const float *W0, void *Z, float *W_out,
+                                 const int *seq_start, int n_seq, float q_scale, int B, int Hk,
+                                 int H, int T, int dk, int dv, ttt_dtype dt, unsigned flags,
+                                 void *workspace, size_t workspace_bytes, ttt_stream stream);
+
+/*
+ * Gated delta rule decode: n tokens per row, the states in a pool, updated in
+ * place, exactly as n calls with one token. Q, K [B][Hk][n][dk], V [B][H][n][dv],
+ * eta, g [B][H][n] (g NULL: no decay), Z [B][H][n][dv].
+ *   W           [n_slots][H][dk][dv] fp32, the pool
+ *   state_index [B] int32 on the device: row b continues state state_index[b];
+ *               NULL: row b continues state b (B <= n_slots). A row whose index
+ *               is outside 0 .. n_slots - 1 is padding: nothing of it is read
+ *               beyond the index, and its Z is left as it was. The indices
+ *               of the other rows must be distinct: two rows of one call that
+ *               name one state race on it.
+ * Arguments otherwise as ttt_delta_fwd. No workspace. flags: TTT_F_Z_BF16.
+ */
+TTT_API ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V, const float *eta,
+                                    const float *g, float *W, void *Z, const int *state_index,
+                                    int n_slots, float q_scale, int B, int Hk, int H, int n, int dk,
+                                    int dv, ttt_dtype dt, unsigned flags, ttt_stream stream);
+
+/*
+ * The join between two blocks: what stands between the read-out of one layer
+ * and the input of the next. Per token, D = H d channels:
+ *   y = scale * act(gate) * (Norm(z) post_gamma + post_beta)   (Norm per head)
+ *   r = x + y,   h = Norm(r) pre_gamma + pre_beta              (Norm over D)
+ *   X, gate, R, Hn  [B][T][D], dtype dt
+ *   Z               [B][H][T][d] as the forwards write it: fp32, or bf16 with
+ *                   TTT_F_Z_BF16. One head (H = 1, d = D) is a norm over the row.
+ *   scale, post_gamma, post_beta, pre_gamma, pre_beta  [D] fp32 (head-major, so
+ *                   that [H][d] is the same array)
+ * NULL: gate (no gate), scale (1), gammas (1), betas (0), Hn (no second norm).
+ * Z NULL: h = Norm(x) pre_gamma + pre_beta alone (the norm in front of the first
+ * block); R, gate, scale, post_gamma and post_beta must be NULL too, Hn not.
+ * R may be X. Norm is LayerNorm with the population variance, or with
+ * TTT_F_RMS RMSNorm x / sqrt(mean(x^2) + eps); eps > 0. act is SiLU, or with
+ * TTT_F_GATE_SIGMOID the sigmoid. h is the norm of r as stored. Sums in fp32.
+ * Supported: H = 1 with d a multiple of 8, or d in {16, 32, 64, 128, 256}; D <= 4096.
+ * flags: TTT_F_Z_BF16, TTT_F_RMS, TTT_F_GATE_SIGMOID.
+ */
+TTT_API ttt_status ttt_join_fwd(const void *X, const void *Z, const void *gate, const float *scale,
+                                const float *post_gamma, const float *post_beta,
+                                const float *pre_gamma, const float *pre_beta, void *R, void *Hn,
+                                float eps, int B, int H, int T, int d, ttt_dtype dt,
+                                unsigned flags, ttt_stream stream);
+
+/*
+ * Backward of ttt_join_fwd, from the stored R (without Z: X). Inputs dR and dH
+ * [B][T][D] fp32, the gradients of R and Hn (either may be NULL: zero, not both);
+ * outputs fp32, overwritten: dX [B][T][D], dZ [B][H][T][d] (as the backwards of
+ * the layers take it), dGate [B][T][D] (with gate), and the parameters' [D]
+ * gradients, each NULL where it is not wanted. post_beta is read, pre_beta is
+ * not needed. dX may be dR.
+ * workspace: at least ttt_join_bwd_workspace_bytes(...) bytes, 256-byte
+ *   aligned, clobbered; calls that share one must not overlap on the GPU.
+ * Deterministic. Shapes and flags as ttt_join_fwd.
+ */
+TTT_API size_t ttt_join_bwd_workspace_bytes(int B, int H, int T, int d);
+TTT_API ttt_status ttt_join_bwd(const void *R, const void *Z, const void *gate, const float *scale,
+                                const float *post_gamma, const float *post_beta,
+                                const float *pre_gamma, const float *dR, const float *dH,
+                                float *dX, float *dZ, float *dGate, float *dscale,
+                                float *dpost_gamma, float *dpost_beta, float *dpre_gamma,
+                                float *dpre_beta, float eps, int B, int H, int T, int d,
+                                ttt_dtype dt, unsigned flags, void *workspace,
+                                size_t workspace_bytes, ttt_stream stream);
 
 /*
  * Synchronises `stream`, then returns TTT_OK, TTT_ERR_DEVICE_TIMEOUT if a

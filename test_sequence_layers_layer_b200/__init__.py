@@ -30,6 +30,8 @@ TTT_F_LN = 1
 TTT_F_W0_PER_SEQ = 2
 TTT_F_Z_BF16 = 4
 TTT_F_L2_KEYS = 8
+TTT_F_RMS = 16
+TTT_F_GATE_SIGMOID = 32
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -92,6 +94,21 @@ def lib() -> ctypes.CDLL:
         L.ttt_affine_prefix.restype = _I
         L.ttt_affine_prefix.argtypes = ([_P] * 5 + [_I] * 4 + [ctypes.c_longlong] * 2
                                         + [ctypes.c_uint, _P])
+        L.ttt_delta_workspace_bytes.restype = ctypes.c_size_t
+        L.ttt_delta_workspace_bytes.argtypes = [_I] * 8
+        L.ttt_delta_fwd.restype = _I
+        L.ttt_delta_fwd.argtypes = ([_P] * 9 + [_I, ctypes.c_float] + [_I] * 7
+                                    + [ctypes.c_uint, _P, ctypes.c_size_t, _P])
+        L.ttt_delta_decode.restype = _I
+        L.ttt_delta_decode.argtypes = ([_P] * 8 + [_I, ctypes.c_float] + [_I] * 7
+                                       + [ctypes.c_uint, _P])
+        L.ttt_join_fwd.restype = _I
+        L.ttt_join_fwd.argtypes = [_P] * 10 + [ctypes.c_float] + [_I] * 5 + [ctypes.c_uint, _P]
+        L.ttt_join_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.ttt_join_bwd_workspace_bytes.argtypes = [_I] * 4
+        L.ttt_join_bwd.restype = _I
+        L.ttt_join_bwd.argtypes = ([_P] * 17 + [ctypes.c_float] + [_I] * 5
+                                   + [ctypes.c_uint, _P, ctypes.c_size_t, _P])
         L.ttt_device_status.restype = _I
         L.ttt_device_status.argtypes = [_P]
         L.ttt_launch_count.restype = ctypes.c_ulonglong
@@ -319,6 +336,49 @@ def ttt_affine_prefix(M, N, W0, W_in, W_end, S, H, nseg, d, seq_stride, seg_stri
     rc = lib().ttt_affine_prefix(_ptr(M), _ptr(N), _ptr(W0), _ptr(W_in), _ptr(W_end), S, H, nseg,
                                  d, seq_stride, seg_stride, flags, _stream(stream))
     return _check("ttt_affine_prefix", rc) if check else rc
+
+
+def ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt) -> int:
+    return int(lib().ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt))
+
+
+def ttt_delta_fwd(Q, K, V, eta, g, W0, Z, W_out, seq_start, n_seq, q_scale, B, Hk, H, T, dk, dv,
+                  dt, flags, workspace, workspace_bytes, stream=None, check=True):
+    rc = lib().ttt_delta_fwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(eta), _ptr(g), _ptr(W0), _ptr(Z),
+                             _ptr(W_out), _ptr(seq_start), n_seq, q_scale, B, Hk, H, T, dk, dv,
+                             dt, flags, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check("ttt_delta_fwd", rc) if check else rc
+
+
+def ttt_delta_decode(Q, K, V, eta, g, W, Z, state_index, n_slots, q_scale, B, Hk, H, n, dk, dv,
+                     dt, flags, stream=None, check=True):
+    rc = lib().ttt_delta_decode(_ptr(Q), _ptr(K), _ptr(V), _ptr(eta), _ptr(g), _ptr(W), _ptr(Z),
+                                _ptr(state_index), n_slots, q_scale, B, Hk, H, n, dk, dv, dt,
+                                flags, _stream(stream))
+    return _check("ttt_delta_decode", rc) if check else rc
+
+
+def ttt_join_fwd(X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn, eps, B, H,
+                 T, d, dt, flags, stream=None, check=True):
+    rc = lib().ttt_join_fwd(*[_ptr(x) for x in (X, Z, gate, scale, post_gamma, post_beta,
+                                                pre_gamma, pre_beta, R, Hn)],
+                            eps, B, H, T, d, dt, flags, _stream(stream))
+    return _check("ttt_join_fwd", rc) if check else rc
+
+
+def ttt_join_bwd_workspace_bytes(B, H, T, d) -> int:
+    return int(lib().ttt_join_bwd_workspace_bytes(B, H, T, d))
+
+
+def ttt_join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, dX, dZ, dGate,
+                 dscale, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, eps, B, H, T, d, dt,
+                 flags, workspace, workspace_bytes, stream=None, check=True):
+    rc = lib().ttt_join_bwd(*[_ptr(x) for x in (R, Z, gate, scale, post_gamma, post_beta,
+                                                pre_gamma, dR, dH, dX, dZ, dGate, dscale,
+                                                dpost_gamma, dpost_beta, dpre_gamma, dpre_beta)],
+                            eps, B, H, T, d, dt, flags, _ptr(workspace), workspace_bytes,
+                            _stream(stream))
+    return _check("ttt_join_bwd", rc) if check else rc
 
 
 def ttt_device_status(stream=None) -> int:
@@ -604,3 +664,228 @@ def affine_prefix(M, N, W0, W_in, W_end=None, *, S, H, nseg, seq_stride, seg_str
     d = M.shape[-1]
     ttt_affine_prefix(M, N, W0, W_in, W_end, S, H, nseg, d, seq_stride, seg_stride,
                       TTT_F_W0_PER_SEQ if w0_per_seq else 0, stream)
+
+
+# The calls below read their shapes off the tensors, check every tensor
+# (device, type, shape, contiguous) and run on the tensors' own device, on
+# `stream` or that device's current stream; what they allocate belongs to the
+# stream that uses it.
+
+def _tensors(fn, device, **want):
+    """want: name=(tensor or None, dtypes, shape). Raises ValueError on the first that is off."""
+    for name, (t, dtypes, shape) in want.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+
+
+class _On:
+    """The device and the stream of a call; empty() allocates for that stream."""
+
+    def __init__(self, fn, first, stream):
+        import torch
+        if not first.is_cuda:
+            raise ValueError(f"{fn}: tensors must be on a CUDA device, got {first.device}")
+        self.device = first.device
+        self._guard = torch.cuda.device(first.device)
+        if isinstance(stream, int):
+            # 0 is the legacy default stream, which torch knows as its default stream
+            stream = torch.cuda.ExternalStream(stream, device=first.device) if stream else \
+                torch.cuda.default_stream(first.device)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {first.device}")
+        self._stream = stream
+
+    def __enter__(self):
+        import torch
+        self._guard.__enter__()
+        if self._stream is None:
+            self._stream = torch.cuda.current_stream()
+        self._other = self._stream != torch.cuda.current_stream()
+        self.handle = self._stream.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        import torch
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self._other:
+            # memory the current stream may still be using: the call waits for
+            # that, and the block is not handed out again before the call is done
+            self._stream.wait_stream(torch.cuda.current_stream())
+            t.record_stream(self._stream)
+        return t
+
+    def workspace(self, fn, given, need):
+        import torch
+        if given is None:
+            return self.empty(max(need, 256), torch.uint8) if need else None
+        if given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"{fn}: workspace must be contiguous and on {self.device}")
+        return given
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _delta_shapes(fn, dev, Q, K, V, eta, g, W0, w0_per_seq, seq_start):
+    """Checks the inputs of the gated delta rule; returns B, Hk, H, T, dk, dv, n_seq, N."""
+    import torch
+    if Q.dim() != 4 or V.dim() != 4:
+        raise ValueError(f"{fn}: Q, K, V must be [B, heads, T, d]")
+    B, Hk, T, dk = Q.shape
+    H, dv = V.shape[1], V.shape[3]
+    n_seq = 0
+    if seq_start is not None:
+        if seq_start.dim() != 1 or seq_start.numel() < 2:
+            raise ValueError(f"{fn}: seq_start must hold n_seq + 1 >= 2 offsets")
+        if B != 1:
+            raise ValueError(f"{fn}: packed sequences need B = 1, got {B}")
+        n_seq = seq_start.numel() - 1
+    N = n_seq or B
+    f32, same = (torch.float32,), (Q.dtype,)
+    _dtype_code(Q)
+    _tensors(fn, dev, Q=(Q, same, (B, Hk, T, dk)), K=(K, same, (B, Hk, T, dk)),
+             V=(V, same, (B, H, T, dv)), eta=(eta, f32, (B, H, T)), g=(g, f32, (B, H, T)),
+             W0=(W0, f32, (N, H, dk, dv) if w0_per_seq else (H, dk, dv)),
+             seq_start=(seq_start, (torch.int32,), (n_seq + 1,)))
+    return B, Hk, H, T, dk, dv, n_seq, N
+
+
+def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None, q_scale=1.0,
+              z_bf16=False, want_w=True, Z=None, workspace=None, stream=None):
+    """Gated delta rule forward (ttt_delta_fwd). Q, K [B, Hk, T, dk], V [B, H, T, dv] (bf16 or
+    fp32), eta and g (log decays; None: no decay) [B, H, T] fp32, W0 [H, dk, dv] or, with
+    w0_per_seq, [N, H, dk, dv] (None: zero). seq_start: int32 offsets of N packed sequences along
+    T (B = 1). Returns (Z [B, H, T, dv], W_out [N, H, dk, dv] or None). Z may be given; its rows
+    outside every sequence are left as they are (in a new Z they are undefined)."""
+    import torch
+    with _On("delta_fwd", Q, stream) as on:
+        B, Hk, H, T, dk, dv, n_seq, N = _delta_shapes("delta_fwd", on.device, Q, K, V, eta, g, W0,
+                                                      w0_per_seq, seq_start)
+        zt = torch.bfloat16 if z_bf16 else torch.float32
+        if Z is None:
+            Z = on.empty((B, H, T, dv), zt)
+        _tensors("delta_fwd", on.device, Z=(Z, (zt,), (B, H, T, dv)))
+        W_out = on.empty((N, H, dk, dv), torch.float32) if want_w else None
+        need = ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, _dtype_code(Q))
+        workspace = on.workspace("delta_fwd", workspace, need)
+        flags = (TTT_F_W0_PER_SEQ if w0_per_seq else 0) | (TTT_F_Z_BF16 if z_bf16 else 0)
+        ttt_delta_fwd(Q, K, V, eta, g, W0, Z, W_out, seq_start, n_seq, q_scale, B, Hk, H, T, dk,
+                      dv, _dtype_code(Q), flags, workspace, _nbytes(workspace), on.handle)
+    return Z, W_out
+
+
+def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, Z=None,
+                        stream=None):
+    """n tokens of the gated delta rule per row, the states updated in place (ttt_delta_decode).
+    Q, K [B, Hk, n, dk], V [B, H, n, dv], eta and g (or None) [B, H, n] fp32, W
+    [slots, H, dk, dv] fp32; row b continues state state_index[b] (int32 [B]; None: state b).
+    Rows whose index is outside the pool are padding: their Z is left as it is (undefined in a
+    new Z). The other rows' indices must be distinct. Returns Z [B, H, n, dv]."""
+    import torch
+    with _On("delta_decode", Q, stream) as on:
+        B, Hk, H, n, dk, dv, _, _ = _delta_shapes("delta_decode", on.device, Q, K, V, eta, g, None,
+                                                  False, None)
+        zt = torch.bfloat16 if z_bf16 else torch.float32
+        if W.dim() != 4:
+            raise ValueError("delta_decode: W must be [slots, H, dk, dv]")
+        if Z is None:
+            Z = on.empty((B, H, n, dv), zt)
+        _tensors("delta_decode", on.device, Z=(Z, (zt,), (B, H, n, dv)),
+                 W=(W, (torch.float32,), (W.shape[0], H, dk, dv)),
+                 state_index=(state_index, (torch.int32,), (B,)))
+        ttt_delta_decode(Q, K, V, eta, g, W, Z, state_index, W.shape[0], q_scale, B, Hk, H, n, dk,
+                         dv, _dtype_code(Q), TTT_F_Z_BF16 if z_bf16 else 0, on.handle)
+    return Z
+
+
+def delta_decode(q, k, v, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, z=None,
+                 stream=None):
+    """delta_decode_tokens for one token per row: q, k [B, Hk, dk], v [B, H, dv], eta and g (or
+    None) [B, H]. Returns z [B, H, dv]."""
+    one = lambda t: None if t is None else t.unsqueeze(2)  # noqa: E731
+    return delta_decode_tokens(one(q), one(k), one(v), one(eta), one(g), W,
+                               state_index=state_index, q_scale=q_scale, z_bf16=z_bf16, Z=one(z),
+                               stream=stream).squeeze(2)
+
+
+_ACTS = {"silu": 0, "sigmoid": TTT_F_GATE_SIGMOID}
+
+
+def _join_shapes(fn, dev, X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, rms, act):
+    """Checks the inputs of the join; returns B, H, T, d, flags and the parameters' shapes."""
+    import torch
+    if X.dim() != 3 or (Z is not None and Z.dim() != 4):
+        raise ValueError(f"{fn}: expected [B, T, D] and Z [B, H, T, d]")
+    if act not in _ACTS:
+        raise ValueError(f"{fn}: act must be one of {sorted(_ACTS)}, got {act!r}")
+    B, T, D = X.shape
+    H, d = (1, D) if Z is None else (Z.shape[1], Z.shape[3])
+    if H * d != D:
+        raise ValueError(f"{fn}: H * d = {H * d} is not D = {D}")
+    _dtype_code(X)
+    same, f32 = (X.dtype,), (torch.float32,)
+    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
+                  pre_beta=pre_beta)
+    for name, p in params.items():
+        if p is not None:
+            _tensors(fn, dev, **{name: (p, f32, (H, d) if tuple(p.shape) == (H, d) else (D,))})
+    _tensors(fn, dev, X=(X, same, (B, T, D)), gate=(gate, same, (B, T, D)),
+             Z=(Z, (torch.float32, torch.bfloat16), (B, H, T, d)))
+    flags = (TTT_F_RMS if rms else 0) | _ACTS[act]
+    if Z is not None and Z.dtype == torch.bfloat16:
+        flags |= TTT_F_Z_BF16
+    return B, H, T, d, flags
+
+
+def join_fwd(X, Z, gate=None, scale=None, post_gamma=None, post_beta=None, pre_gamma=None,
+             pre_beta=None, *, rms=False, act="silu", eps=1e-5, want_h=True, stream=None):
+    """The join between two blocks (ttt_join_fwd): r = x + scale act(gate) (Norm(z) post_gamma +
+    post_beta), h = Norm(r) pre_gamma + pre_beta. X, gate [B, T, H d] (bf16 or fp32), Z
+    [B, H, T, d] (fp32 or bf16; its norm is per head), the parameters [D] or [H, d] fp32, each
+    optional. Returns (R, Hn); Hn is None without want_h. With Z None only Hn = Norm(X) is
+    computed, and R is X."""
+    with _On("join_fwd", X, stream) as on:
+        B, H, T, d, flags = _join_shapes("join_fwd", on.device, X, Z, gate, scale, post_gamma,
+                                         post_beta, pre_gamma, pre_beta, rms, act)
+        R = None if Z is None else on.empty(X.shape, X.dtype)
+        Hn = on.empty(X.shape, X.dtype) if want_h else None
+        ttt_join_fwd(X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn, eps, B,
+                     H, T, d, _dtype_code(X), flags, on.handle)
+    return (X if Z is None else R), Hn
+
+
+def join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, dR, dH, *, rms=False,
+             act="silu", eps=1e-5, workspace=None, stream=None):
+    """Backward of join_fwd from the stored R (with Z None: X) and the gradients dR and dH
+    [B, T, D] fp32 of R and Hn (either may be None: zero). Returns a dict of fp32 gradients: X, and
+    for what was given Z, gate, scale, gamma1, beta1 (post_*), gamma2, beta2 (pre_*; not without
+    dH)."""
+    import torch
+    with _On("join_bwd", R, stream) as on:
+        B, H, T, d, flags = _join_shapes("join_bwd", on.device, R, Z, gate, scale, post_gamma,
+                                         post_beta, pre_gamma, pre_beta, rms, act)
+        f32 = torch.float32
+        _tensors("join_bwd", on.device, dR=(dR, (f32,), R.shape), dH=(dH, (f32,), R.shape))
+        want = dict(X=R, Z=Z, gate=gate, scale=scale, gamma1=post_gamma, beta1=post_beta)
+        if dH is not None:
+            want.update(gamma2=pre_gamma, beta2=pre_beta)
+        g = {n: on.empty(t.shape, f32) for n, t in want.items() if t is not None}
+        need = ttt_join_bwd_workspace_bytes(B, H, T, d)
+        workspace = on.workspace("join_bwd", workspace, need or 256)
+        ttt_join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, g["X"],
+                     g.get("Z"), g.get("gate"), g.get("scale"), g.get("gamma1"), g.get("beta1"),
+                     g.get("gamma2"), g.get("beta2"), eps, B, H, T, d, _dtype_code(R), flags,
+                     workspace, _nbytes(workspace), on.handle)
+    return g

@@ -11,6 +11,8 @@
 #include "../../include/ttt.h"
 #include "../../include/ttt_diag.h"
 #include "ttt_common.cuh"
+#include "ttt_delta.cuh"
+#include "ttt_join.cuh"
 
 namespace ttt {
 
@@ -700,6 +702,160 @@ ttt_status ttt_affine_prefix(const float *M, const float *N, const float *W0, fl
     timing_begin(cs);
     return launched(launch_affine_prefix(M, N, W0, W_in, W_end, S, H, nseg, d, seq_stride,
                                          seg_stride, per_seq, cs));
+}
+
+// Shapes of the gated delta rule; N is the number of sequences.
+static ttt_status check_delta_shape(int B, int Hk, int H, int T, int dk, int dv, int N) {
+    if (B <= 0 || Hk <= 0 || H <= 0 || T <= 0 || N <= 0 || H % Hk) return TTT_ERR_SHAPE;
+    if (!delta_supported(dk, dv)) return TTT_ERR_SHAPE;
+    if ((long long)B * H > (1LL << 24) || (long long)N * H > (1LL << 24) ||
+        (long long)B * H * T > (1LL << 33) || T > (1 << 30))
+        return TTT_ERR_SHAPE;
+    return TTT_OK;
+}
+
+size_t ttt_delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,
+                                 ttt_dtype dt) {
+    const int N = n_seq > 0 ? n_seq : B;
+    if (n_seq < 0 || (n_seq > 0 && B != 1) || (dt != TTT_BF16 && dt != TTT_FP32)) return 0;
+    if (check_delta_shape(B, Hk, H, T, dk, dv, N) != TTT_OK) return 0;
+    return delta_workspace_bytes(B, Hk, H, T, dk, dv, N, n_seq > 0, dt == TTT_BF16);
+}
+
+ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, const float *eta,
+                         const float *g, const float *W0, void *Z, float *W_out,
+                         const int *seq_start, int n_seq, float q_scale, int B, int Hk, int H,
+                         int T, int dk, int dv, ttt_dtype dt, unsigned flags, void *workspace,
+                         size_t workspace_bytes, ttt_stream stream) {
+    if (flags & ~(TTT_F_W0_PER_SEQ | TTT_F_Z_BF16)) return TTT_ERR_ARG;
+    if (!Q || !K || !V || !eta || !Z) return TTT_ERR_PTR;
+    if (seq_start ? (n_seq <= 0 || B != 1) : n_seq != 0) return TTT_ERR_ARG;
+    const int N = seq_start ? n_seq : B;
+    ttt_status st = check_delta_shape(B, Hk, H, T, dk, dv, N);
+    if (st != TTT_OK) return st;
+    if (dt != TTT_BF16 && dt != TTT_FP32) return TTT_ERR_DTYPE;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(Z) || !aligned16(W0) ||
+        !aligned16(W_out))
+        return TTT_ERR_ALIGN;
+    if (W_out && W_out == W0 && !(flags & TTT_F_W0_PER_SEQ)) return TTT_ERR_ARG;
+    const size_t need = ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+                 workspace_bytes < need))
+        return TTT_ERR_WORKSPACE;
+    st = check_arch();
+    if (st != TTT_OK) return st;
+    const void *ptrs[] = {Q, K, V, eta, g, W0, Z, W_out, seq_start, need ? workspace : nullptr};
+    st = check_device_ptrs(ptrs, 10);
+    if (st != TTT_OK) return st;
+    const DeltaArgs a{Q, K, V, eta, g, W0, Z, W_out, seq_start, B, Hk, H, T, dk, dv, N, q_scale,
+                      dt == TTT_BF16, (flags & TTT_F_W0_PER_SEQ) != 0,
+                      (flags & TTT_F_Z_BF16) != 0, workspace};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    timing_begin(cs);
+    return launched(launch_delta_fwd(a, cs));
+}
+
+ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V, const float *eta,
+                            const float *g, float *W, void *Z, const int *state_index,
+                            int n_slots, float q_scale, int B, int Hk, int H, int n, int dk,
+                            int dv, ttt_dtype dt, unsigned flags, ttt_stream stream) {
+    if (flags & ~TTT_F_Z_BF16) return TTT_ERR_ARG;
+    if (!Q || !K || !V || !eta || !W || !Z) return TTT_ERR_PTR;
+    ttt_status st = check_delta_shape(B, Hk, H, n, dk, dv, B);
+    if (st != TTT_OK) return st;
+    if (n_slots <= 0 || (!state_index && n_slots < B)) return TTT_ERR_SHAPE;
+    if (dt != TTT_BF16 && dt != TTT_FP32) return TTT_ERR_DTYPE;
+    if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(Z) || !aligned16(W))
+        return TTT_ERR_ALIGN;
+    st = check_arch();
+    if (st != TTT_OK) return st;
+    const void *ptrs[] = {Q, K, V, eta, g, W, Z, state_index};
+    st = check_device_ptrs(ptrs, 8);
+    if (st != TTT_OK) return st;
+    const DeltaArgs a{Q, K, V, eta, g, nullptr, Z, nullptr, nullptr, B, Hk, H, n, dk, dv, B,
+                      q_scale, dt == TTT_BF16, true, (flags & TTT_F_Z_BF16) != 0, nullptr};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    timing_begin(cs);
+    return launched(launch_delta_decode(a, W, state_index, n_slots, cs));
+}
+
+static ttt_status check_join_shape(int B, int H, int T, int d) {
+    if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || !join_supported(H, d)) return TTT_ERR_SHAPE;
+    if ((long long)B * T > (1LL << 34)) return TTT_ERR_SHAPE;
+    return TTT_OK;
+}
+
+ttt_status ttt_join_fwd(const void *X, const void *Z, const void *gate, const float *scale,
+                        const float *post_gamma, const float *post_beta, const float *pre_gamma,
+                        const float *pre_beta, void *R, void *Hn, float eps, int B, int H, int T,
+                        int d, ttt_dtype dt, unsigned flags, ttt_stream stream) {
+    if (flags & ~(TTT_F_Z_BF16 | TTT_F_RMS | TTT_F_GATE_SIGMOID)) return TTT_ERR_ARG;
+    if (!(eps > 0.f)) return TTT_ERR_ARG;
+    if (!X || (Z ? !R : !Hn)) return TTT_ERR_PTR;
+    if (!Z && (R || gate || scale || post_gamma || post_beta)) return TTT_ERR_ARG;
+    if (!Hn && (pre_gamma || pre_beta)) return TTT_ERR_ARG;
+    if (Hn && (Hn == R || Hn == X)) return TTT_ERR_ARG;
+    ttt_status st = check_join_shape(B, H, T, d);
+    if (st != TTT_OK) return st;
+    if (dt != TTT_BF16 && dt != TTT_FP32) return TTT_ERR_DTYPE;
+    const void *ptrs[] = {X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return TTT_ERR_ALIGN;
+    st = check_arch();
+    if (st != TTT_OK) return st;
+    st = check_device_ptrs(ptrs, 10);
+    if (st != TTT_OK) return st;
+    const JoinArgs a{X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn, B, H,
+                     T, d, eps, dt == TTT_BF16, (flags & TTT_F_Z_BF16) != 0,
+                     (flags & TTT_F_RMS) != 0, !(flags & TTT_F_GATE_SIGMOID)};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    timing_begin(cs);
+    return launched(launch_join_fwd(a, cs));
+}
+
+size_t ttt_join_bwd_workspace_bytes(int B, int H, int T, int d) {
+    return check_join_shape(B, H, T, d) == TTT_OK ? join_bwd_workspace_bytes(B, H, T, d) : 0;
+}
+
+ttt_status ttt_join_bwd(const void *R, const void *Z, const void *gate, const float *scale,
+                        const float *post_gamma, const float *post_beta, const float *pre_gamma,
+                        const float *dR, const float *dH, float *dX, float *dZ, float *dGate,
+                        float *dscale, float *dpost_gamma, float *dpost_beta, float *dpre_gamma,
+                        float *dpre_beta, float eps, int B, int H, int T, int d, ttt_dtype dt,
+                        unsigned flags, void *workspace, size_t workspace_bytes,
+                        ttt_stream stream) {
+    if (flags & ~(TTT_F_Z_BF16 | TTT_F_RMS | TTT_F_GATE_SIGMOID)) return TTT_ERR_ARG;
+    if (!(eps > 0.f)) return TTT_ERR_ARG;
+    if (!dX || (!dR && !dH) || (dH && !R) || (Z ? !dZ : !dH)) return TTT_ERR_PTR;
+    if (gate && !dGate) return TTT_ERR_PTR;
+    if (!Z && (gate || scale || post_gamma || post_beta || dZ || dscale || dpost_gamma ||
+               dpost_beta))
+        return TTT_ERR_ARG;
+    if (!gate && dGate) return TTT_ERR_ARG;
+    if (!dH && (dpre_gamma || dpre_beta)) return TTT_ERR_ARG;
+    if (static_cast<const float *>(dX) == dH && dH) return TTT_ERR_ARG;
+    ttt_status st = check_join_shape(B, H, T, d);
+    if (st != TTT_OK) return st;
+    if (dt != TTT_BF16 && dt != TTT_FP32) return TTT_ERR_DTYPE;
+    const void *ptrs[] = {R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, dX, dZ,
+                          dGate, dscale, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, workspace};
+    for (int i = 0; i < 12; ++i)
+        if (!aligned16(ptrs[i])) return TTT_ERR_ALIGN;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+        workspace_bytes < ttt_join_bwd_workspace_bytes(B, H, T, d))
+        return TTT_ERR_WORKSPACE;
+    st = check_arch();
+    if (st != TTT_OK) return st;
+    st = check_device_ptrs(ptrs, 18);
+    if (st != TTT_OK) return st;
+    const JoinBwdArgs a{R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, dX, dZ,
+                        dGate, dscale, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta,
+                        static_cast<float *>(workspace), B, H, T, d, eps, dt == TTT_BF16,
+                        (flags & TTT_F_Z_BF16) != 0, (flags & TTT_F_RMS) != 0,
+                        !(flags & TTT_F_GATE_SIGMOID)};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    timing_begin(cs);
+    return launched(launch_join_bwd(a, cs));
 }
 
 ttt_status ttt_device_status(ttt_stream stream) {
