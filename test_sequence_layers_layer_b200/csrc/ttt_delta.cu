@@ -210,10 +210,6 @@ cudaError_t launch_delta_decode(const DeltaArgs &a, float *W, const int *state_i
     return run_recurrent(r, a.B, a.dk, a.bf16, s);
 }
 
-size_t delta_workspace_bytes(int, int, int, int, int, int, int, bool, bool) { return 0; }
-cudaError_t launch_delta_fwd(const DeltaArgs &a, cudaStream_t s) {
-    return launch_delta_recurrent(a, s);
-}
 #endif  // TTT_HOST_RUN
 
 }  // namespace ttt

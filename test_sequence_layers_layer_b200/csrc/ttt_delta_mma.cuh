@@ -1,0 +1,141 @@
+// ttt_delta_mma.cuh -- the operand form of the chunked gated delta rule.
+//
+// An fp32 operand goes to the tensor cores as two fp16 terms under a
+// power-of-two scale of its row: with the row's largest size brought into
+// [2^13, 2^14), x s = hi + lo + e, hi = fp16(x s), lo = fp16(x s - hi) and |e| <= 2^-22
+// of |x s| (2^-25 absolute for the elements more than 2^17 below the largest): the
+// precision of fp32 products, in two or three fp16 products (lo lo is left
+// out) instead of the three or six that bf16 terms would take for the same bits. A
+// bf16 operand is one term, exact in fp16 (8 bits of 11) down to 2^-27 of its
+// row's largest size. The scales are taken out again in fp32, where the rows of
+// the result are scaled anyway.
+#pragma once
+
+#include "sm100.cuh"
+#include "ttt_delta.cuh"
+
+#include <cuda_fp16.h>
+
+namespace ttt {
+namespace delta {
+
+using namespace sm100;
+
+constexpr int C = kDeltaC;
+constexpr int kImg = C * C * 2;  // bytes of a 64 x 64 fp16 image
+
+// Per chunk and value head: eight vectors of 64 floats.
+enum Vec { kVk, kVt, kVu, kVq, kVp, kVeta, kVgam, kVspare, kVecs };
+// kVk  exp(G_j) / sK_j          (K S, Om K)            sX: the scale of row j of image X
+// kVt  1 / sT_i
+// kVu  exp(G_C - G_j) eta_j / sK_j
+// kVq  c exp(G_i) / sQ_i
+// kVp  1 / sP_i
+// kVeta: 1 / sK_j; kVgam: [0] exp(G_C); kVspare: 1 / sQ_i
+constexpr int kVecBytes = kVecs * C * 4;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Power of two s that brings amax into [2^13, 2^14), and 1 / s; both stay normal
+// numbers for any amax (zero, subnormal, infinity, NaN).
+__device__ __forceinline__ void pow2_scale(float amax, float &s, float &inv) {
+    const int e = (__float_as_int(amax) >> 23) & 255;
+    int f = 267 - e;
+    f = f > 253 ? 253 : f;
+    s = __int_as_float(f << 23);
+    inv = __int_as_float((254 - f) << 23);
+}
+
+__device__ __forceinline__ uint32_t h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// hi and lo terms of a pair already scaled.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = h2(a - f.x, b - f.y);
+}
+
+// Byte offset of the 16-byte unit (row, col .. col + 7) of a 64-row fp16 image:
+// 128-byte swizzled rows, 64 columns after one another.
+__device__ __forceinline__ uint32_t img_off(int row, int col) {
+    return (uint32_t)((col >> 6) * (C * 128) + (row >> 3) * 1024 + (row & 7) * 128 +
+                      ((((col & 63) >> 3) ^ (row & 7)) << 4));
+}
+
+// Shared address of this lane's row for an ldmatrix.x4 of a 16 x 16 block at
+// (row, col). Plain, as A: registers a0..a3. Plain, as B with the rows as n and
+// the columns as k: {b0, b1} of the first 8 rows, then of the next 8 (order 0, 2 / 1, 3).
+__device__ __forceinline__ uint32_t ldsm_addr(uint32_t img, int row, int col, int lane) {
+    return img + img_off(row + (lane & 15), col + (lane >> 4) * 8);
+}
+// B with rows as n: b0, b1 of rows row .. row + 7 in r[0], r[1], of the next 8 in r[2], r[3].
+__device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t img, int row, int col, int lane) {
+    ldsm_x4(r, img + img_off(row + ((lane >> 4) << 3) + (lane & 7), col + ((lane >> 3) & 1) * 8));
+}
+// B with rows as k: b0, b1 of columns col .. col + 7 in r[0], r[1], of the next 8 in r[2], r[3].
+__device__ __forceinline__ void load_bt(uint32_t (&r)[4], uint32_t img, int row, int col,
+                                        int lane) {
+    ldsm_x4_t(r, img + img_off(row + (lane & 15), col + (lane >> 4) * 8));
+}
+
+// Largest size over the four lanes that share a row.
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Workspace: per chunk slot and head, the images that the scans read.
+struct Plan {
+    int slots;          // chunk slots of all sequences
+    int terms;          // fp16 terms of Q and K: 1 (bf16 inputs) or 2
+    size_t kimg;        // bytes of one chunk's K (or Q) image, all terms
+    size_t oK, oQ, oT, oP, oV, end;
+};
+inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+inline Plan make_plan(int B, int Hk, int H, int T, int dk, int N, bool packed, bool bf16) {
+    Plan p;
+    // packed: sequence n starts at slot start / 64 + n, so that the slots of two
+    // sequences never meet, whatever the offsets
+    p.slots = packed ? T / C + N : B * ((T + C - 1) / C);
+    p.terms = bf16 ? 1 : 2;
+    p.kimg = (size_t)C * dk * 2 * p.terms;
+    size_t o = 0;
+    auto take = [&](size_t n) {
+        const size_t at = o;
+        o += up256(n);
+        return at;
+    };
+    p.oK = take((size_t)p.slots * Hk * p.kimg);
+    p.oQ = take((size_t)p.slots * Hk * p.kimg);
+    p.oT = take((size_t)p.slots * H * 2 * kImg);
+    p.oP = take((size_t)p.slots * H * 2 * kImg);
+    p.oV = take((size_t)p.slots * H * kVecBytes);
+    p.end = o;
+    return p;
+}
+
+// Where the kernels find the images of a chunk.
+struct Images {
+    char *K, *Q, *T, *P, *vec;
+    size_t kimg;
+};
+
+__device__ __forceinline__ int first_slot(const int *seq_start, int n, int T, int t0) {
+    return seq_start ? t0 / C + n : n * ((T + C - 1) / C);
+}
+
+// The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
+cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
+Images images_at(const Plan &p, void *workspace);
+
+}  // namespace delta
+}  // namespace ttt
