@@ -5,10 +5,14 @@
 // up to token i, D = diag(exp G), Gam_ij = exp(G_i - G_j):
 //   X = V - D K W,   (I + A) rho = X,   A_ij = Gam_ij (k_i.k_j) eta_j   (j < i)
 //   Z = c D Q W + P rho,                P_ij = c Gam_ij (q_i.k_j) eta_j (j <= i)
-//   W' = exp(G_C) W + sum_j exp(G_C - G_j) eta_j k_j^T rho_j.
-// T = (I + A)^-1, P and the decays depend on q, k, eta and g alone, so one kernel
-// forms them for all chunks in parallel; what is left to do one chunk after
-// the other are four small products.
+//   W' = exp(G_C) W + sum_j u_j k_j^T rho_j,  u_j = exp(G_C - G_j) eta_j.
+// T = (I + A)^-1, P and the decays depend on q, k, eta and g alone, and rho = T X
+// is linear in X, so one kernel forms
+//   M = P T [64][64] and H = T^T diag(u) K [64][dk]
+// for all chunks in parallel. One chunk after the other remains
+//   X = V - D K W,   Z = c D Q W + M X,   W' = exp(G_C) W + H^T X:
+// two products deep instead of three, and X is the only operand besides W that
+// has to be brought into operand form on the way.
 #include "../../include/ttt.h"
 #include "ttt_delta_mma.cuh"
 
@@ -19,7 +23,6 @@ namespace {
 // ---------------------------------------------------------------- preparation
 
 constexpr int kPrepThreads = 128;
-constexpr int kLtStride = 68, kTmStride = 65;
 
 struct PrepArgs {
     const void *Q, *K;
@@ -113,23 +116,92 @@ __device__ __forceinline__ void convert_rows(const void *src, size_t row0, int l
     }
 }
 
+constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices (floats)
+
+// Shared memory: K and Q images, A and T in fp32; the images that go out take
+// the places of what is no longer needed (T's terms and then M over A, H's high
+// terms over Q, its low terms over T).
 template <int DK, bool BF16>
 constexpr int prep_smem() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 4 * (C * kLtStride + C * kTmStride) + 4 * 6 * C;
+    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * (5 * C + 8) + 4 * 3 * 16 * 18;
+}
+
+// T = (I + L)^-1 for L strictly lower triangular, by 16 x 16 blocks in fp32: the four
+// diagonal blocks by forward substitution (a lane per column), then the blocks
+// below the diagonal, those nearest to it first:
+//   T_ab = -T_aa sum_{b <= c < a} L_ac T_cb.
+// Leaves the upper blocks of T as they are. Barriers inside; Y: 3 x 16 x 18 floats.
+__device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (lane < 16) {
+        const float *l = L + 16 * warp * kLd + 16 * warp;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+        for (int k = 0; k < 15; ++k)
+#pragma unroll
+            for (int i = k + 1; i < 16; ++i) x[i] = fmaf(-l[i * kLd + k], x[k], x[i]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kLd + 16 * warp + lane] = x[i];
+    }
+    __syncthreads();
+    const int r = tid >> 3, c = (tid & 7) * 2;  // every thread two outputs of each block
+#pragma unroll
+    for (int dist = 1; dist < 4; ++dist) {
+#pragma unroll
+        for (int b = 0; b < 4 - dist; ++b) {
+            float y0 = 0.f, y1 = 0.f;
+            const float *l = L + (16 * (b + dist) + r) * kLd + 16 * b;
+            const float *t = T + 16 * b * kLd + 16 * b + c;
+#pragma unroll 4
+            for (int k = 0; k < 16 * dist; k += 4) {
+                const float4 l4 = *reinterpret_cast<const float4 *>(l + k);
+                const float lk[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 t2 = *reinterpret_cast<const float2 *>(t + (k + e) * kLd);
+                    y0 = fmaf(lk[e], t2.x, y0);
+                    y1 = fmaf(lk[e], t2.y, y1);
+                }
+            }
+            *reinterpret_cast<float2 *>(Y + (b * 16 + r) * 18 + c) = make_float2(y0, y1);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < 4 - dist; ++b) {
+            float y0 = 0.f, y1 = 0.f;
+            const float *t = T + (16 * (b + dist) + r) * kLd + 16 * (b + dist);
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const float4 t4 = *reinterpret_cast<const float4 *>(t + k);
+                const float tk[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y2 = *reinterpret_cast<const float2 *>(Y + (b * 16 + k + e) * 18 + c);
+                    y0 = fmaf(-tk[e], y2.x, y0);
+                    y1 = fmaf(-tk[e], y2.y, y1);
+                }
+            }
+            *reinterpret_cast<float2 *>(T + (16 * (b + dist) + r) * kLd + 16 * b + c) =
+                make_float2(y0, y1);
+        }
+        __syncthreads();
+    }
 }
 
 // One block per chunk and key head, its value heads one after the other.
-// The inverse is a forward substitution in fp32: thread j < 64 holds column j of
-// T in registers; step k takes x_i -= A_ik x_k for i > k, A's columns read as
-// broadcasts.
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
     extern __shared__ __align__(1024) char psm[];
     constexpr int IMG = C * DK * 2 * (BF16 ? 1 : 2);
     char *sK = psm, *sQ = sK + IMG;
-    float *Lt = reinterpret_cast<float *>(sQ + IMG);  // A transposed: Lt[k][i] = A_ik
-    float *Tm = Lt + C * kLtStride;
-    float *iK = Tm + C * kTmStride, *iQ = iK + C, *Gh = iQ + C, *Gl = Gh + C, *eta = Gl + C;
+    float *L = reinterpret_cast<float *>(sQ + IMG);  // A of the chunk, row-major
+    float *T = L + C * kLd;
+    float *iK = T + C * kLd, *iQ = iK + C, *Gh = iQ + C, *Gl = Gh + C, *eta = Gl + C;
+    float *red = eta + C, *Y = red + 8;
+    char *sT = reinterpret_cast<char *>(L);   // T's two terms, then M's
+    char *sHl = reinterpret_cast<char *>(T);  // H's low terms; its high terms over Q
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
     int n, t0, len;
     if (!find_chunk(a, slot, n, t0, len)) return;
@@ -184,7 +256,8 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
         const size_t hslot = (size_t)slot * a.H + h;
         float *vec = reinterpret_cast<float *>(a.im.vec + hslot * kVecBytes);
-        __syncthreads();  // the head before is done with the shared buffers
+        if (r > 0 && tid == 0) bulk_wait_read<0>();  // the head before has gone out
+        __syncthreads();
         if (warp == 0) {
             // sums of decays in double, handed on as two floats: differences of
             // sums stay exact to the last bit of the decays. A decay below -200
@@ -221,96 +294,203 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         }
         __syncthreads();
 
-        // A (transposed) and P from the products
-        float pm[2] = {0.f, 0.f}, P[8][4];
+        // A and P from the products
+        float P[8][4];
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int nt = 0; nt < 8; ++nt) {
+            float av[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * warp + gq + (e >> 1) * 8, j = 8 * nt + 2 * q4 + (e & 1);
-                float av = 0.f, pv = 0.f;
+                av[e] = 0.f;
+                P[nt][e] = 0.f;
                 if (j <= i) {
                     const float gam = expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j])) * eta[j] * iK[j];
-                    pv = a.q_scale * gam * (qk[nt][e] * iQ[i]);
-                    if (j < i) av = gam * (kk[nt][e] * iK[i]);
+                    P[nt][e] = a.q_scale * gam * (qk[nt][e] * iQ[i]);
+                    if (j < i) av[e] = gam * (kk[nt][e] * iK[i]);
                 }
-                Lt[j * kLtStride + i] = av;
-                P[nt][e] = pv;
-                pm[e >> 1] = fmaxf(pm[e >> 1], fabsf(pv));
             }
-        float sp[2], ip[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) pow2_scale(quad_max(pm[x]), sp[x], ip[x]);
-        char *gP = a.im.P + hslot * 2 * kImg;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t hi, lo;
-                split_f16(P[nt][2 * x] * sp[x], P[nt][2 * x + 1] * sp[x], hi, lo);
-                const uint32_t o = img_off(16 * warp + gq + 8 * x, 8 * nt) + 4 * q4;
-                *reinterpret_cast<uint32_t *>(gP + o) = hi;
-                *reinterpret_cast<uint32_t *>(gP + kImg + o) = lo;
-            }
-        if (q4 == 0) {
-            vec[kVp * C + 16 * warp + gq] = ip[0];
-            vec[kVp * C + 16 * warp + gq + 8] = ip[1];
+            float *l = L + (16 * warp + gq) * kLd + 8 * nt + 2 * q4;
+            *reinterpret_cast<float2 *>(l) = make_float2(av[0], av[1]);
+            *reinterpret_cast<float2 *>(l + 8 * kLd) = make_float2(av[2], av[3]);
         }
         if (tid < C) {
-            const float G = Gh[tid] + Gl[tid], GC = Gh[C - 1];
-            const float dec = expf(G), rest = expf((GC - Gh[tid]) + (Gl[C - 1] - Gl[tid]));
+            const float dec = expf(Gh[tid] + Gl[tid]);
             vec[kVk * C + tid] = dec * iK[tid];
-            vec[kVu * C + tid] = rest * eta[tid] * iK[tid];
             vec[kVq * C + tid] = a.q_scale * dec * iQ[tid];
-            vec[kVeta * C + tid] = iK[tid];
-            vec[kVspare * C + tid] = iQ[tid];
-            vec[kVgam * C + tid] = expf(GC + Gl[C - 1]);
+            vec[kVik * C + tid] = iK[tid];
+            vec[kViq * C + tid] = iQ[tid];
+            vec[kVgh * C + tid] = Gh[tid];
+            vec[kVgl * C + tid] = Gl[tid];
         }
         __syncthreads();
+        invert(L, T, Y);
 
-        if (tid < C) {
-            float x[C];
+        // T's terms, row by row (over A); what T's rows were divided by goes to `it`
+        float *it = Y;
+        {
+            const int row = tid >> 1, side = tid & 1;
+            const float *t = T + row * kLd + 32 * side;
+            float v[32], m = 0.f;
 #pragma unroll
-            for (int i = 0; i < C; ++i) x[i] = i == tid ? 1.f : 0.f;
-#pragma unroll
-            for (int k = 0; k < C - 1; ++k) {
-                const float xk = x[k];
-#pragma unroll
-                for (int i = (k + 1) & ~3; i < C; i += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(Lt + k * kLtStride + i);
-                    if (i > k) x[i] = fmaf(-l.x, xk, x[i]);
-                    if (i + 1 > k) x[i + 1] = fmaf(-l.y, xk, x[i + 1]);
-                    if (i + 2 > k) x[i + 2] = fmaf(-l.z, xk, x[i + 2]);
-                    if (i + 3 > k) x[i + 3] = fmaf(-l.w, xk, x[i + 3]);
-                }
+            for (int j = 0; j < 32; j += 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(t + j);
+                v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
             }
 #pragma unroll
-            for (int i = 0; i < C; ++i) Tm[i * kTmStride + tid] = x[i];
-        }
-        __syncthreads();
-        {
-            const int row = tid >> 1, half = tid & 1;
-            const float *t = Tm + row * kTmStride + 32 * half;
-            float m = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(t[j]));
+            for (int j = 0; j < 32; ++j) {
+                if (32 * side + j > row) v[j] = 0.f;
+                m = fmaxf(m, fabsf(v[j]));
+            }
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             float s, is;
             pow2_scale(m, s, is);
-            char *gT = a.im.T + hslot * 2 * kImg;
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    split_f16(t[j + 2 * e] * s, t[j + 2 * e + 1] * s, hi[e], lo[e]);
-                const uint32_t o = img_off(row, 32 * half + j);
-                *reinterpret_cast<uint4 *>(gT + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(gT + kImg + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    split_f16(v[j + 2 * e] * s, v[j + 2 * e + 1] * s, hi[e], lo[e]);
+                const uint32_t o = img_off(row, 32 * side + j);
+                const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4 *>(sT + o) = h4;
+                *reinterpret_cast<uint4 *>(sT + kImg + o) = l4;
+                if (a.im.T) {
+                    char *gT = a.im.T + hslot * 2 * kImg;
+                    *reinterpret_cast<uint4 *>(gT + o) = h4;
+                    *reinterpret_cast<uint4 *>(gT + kImg + o) = l4;
+                }
             }
-            if (half == 0) vec[kVt * C + row] = is;
+            if (side == 0) it[row] = is, vec[kVit * C + row] = is;
+        }
+        __syncthreads();
+
+        // M = P T: rows i of this warp; T's row scales go into P's columns
+        float M[8][4] = {}, sM[2], iM[2];
+        const uint32_t uT = smem_u32(sT);
+        {
+            float sP[2], iP[2];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float2 t2 = *reinterpret_cast<const float2 *>(it + 8 * nt + 2 * q4);
+                P[nt][0] *= t2.x, P[nt][1] *= t2.y, P[nt][2] *= t2.x, P[nt][3] *= t2.y;
+            }
+            row_scales<8>(P, sP, iP);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                if (jj > warp) break;
+                uint32_t hi[4], lo[4];
+                a_terms(P[2 * jj], P[2 * jj + 1], sP, hi, lo);
+#pragma unroll
+                for (int np = 0; np <= jj; ++np) {
+                    uint32_t th[4], tl[4];
+                    load_bt(th, uT, 16 * jj, 16 * np, lane);
+                    load_bt(tl, uT + kImg, 16 * jj, 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(M[2 * np + x], hi, th[2 * x], th[2 * x + 1]);
+                        mma_f16(M[2 * np + x], lo, th[2 * x], th[2 * x + 1]);
+                        mma_f16(M[2 * np + x], hi, tl[2 * x], tl[2 * x + 1]);
+                    }
+                }
+            }
+            row_scales<8>(M, sM, iM);
+            if (q4 == 0) {
+                vec[kVm * C + 16 * warp + gq] = iP[0] * iM[0];
+                vec[kVm * C + 16 * warp + gq + 8] = iP[1] * iM[1];
+            }
+        }
+        // H = T^T diag(u) K: rows j of this warp, summed over tokens i >= j
+        float Hc[DK / 8][4] = {}, iA[2];
+        {
+            const float GC = Gh[C - 1], GCl = Gl[C - 1];
+            float A[8][4] = {}, sA[2];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                if (nt < 2 * warp) continue;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = 8 * nt + 2 * q4 + x;
+                    const float u = expf((GC - Gh[i]) + (GCl - Gl[i])) * eta[i] * iK[i];
+                    const float *t = T + i * kLd + 16 * warp + gq;
+                    // inside the diagonal block T holds zeros above the diagonal
+                    A[nt][x] = u * t[0];
+                    A[nt][2 + x] = u * t[8];
+                }
+            }
+            row_scales<8>(A, sA, iA);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb < warp) continue;
+                uint32_t hi[4], lo[4];
+                a_terms(A[2 * kb], A[2 * kb + 1], sA, hi, lo);
+#pragma unroll
+                for (int np = 0; np < DK / 16; ++np) {
+                    uint32_t bb[4];
+                    load_bt(bb, uK, 16 * kb, 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(Hc[2 * np + x], lo, bb[2 * x], bb[2 * x + 1]);
+                    }
+                    if (!BF16) {
+                        load_bt(bb, uK + C * DK * 2, 16 * kb, 16 * np, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
+                    }
+                }
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < DK / 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    Hc[nt][e] *= iA[e >> 1];
+                    m = fmaxf(m, fabsf(Hc[nt][e]));
+                }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) red[warp] = m;
+        }
+        __syncthreads();  // T (both forms) is read, the four maxima are there
+        float sH, iH;
+        pow2_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), sH, iH);
+        if (tid == 0) {
+            vec[kVs * C] = expf(Gh[C - 1] + Gl[C - 1]);
+            vec[kVs * C + 1] = iH;
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t hi, lo;
+                split_f16(M[nt][2 * x] * sM[x], M[nt][2 * x + 1] * sM[x], hi, lo);
+                const uint32_t o = img_off(16 * warp + gq + 8 * x, 8 * nt) + 4 * q4;
+                *reinterpret_cast<uint32_t *>(sT + o) = hi;
+                *reinterpret_cast<uint32_t *>(sT + kImg + o) = lo;
+            }
+#pragma unroll
+        for (int nt = 0; nt < DK / 8; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t hi, lo;
+                split_f16(Hc[nt][2 * x] * sH, Hc[nt][2 * x + 1] * sH, hi, lo);
+                const uint32_t o = img_off(16 * warp + gq + 8 * x, 8 * nt) + 4 * q4;
+                *reinterpret_cast<uint32_t *>(sQ + o) = hi;
+                *reinterpret_cast<uint32_t *>(sHl + o) = lo;
+            }
+        fence_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            bulk_store(a.im.M + hslot * 2 * kImg, sT, 2 * kImg);
+            bulk_store(a.im.H + hslot * a.im.himg, sQ, C * DK * 2);
+            bulk_store(a.im.H + hslot * a.im.himg + C * DK * 2, sHl, C * DK * 2);
+            bulk_commit();
         }
     }
+    if (tid == 0) bulk_wait<0>();
 }
 
 // ---------------------------------------------------------------- scan
@@ -322,41 +502,48 @@ struct ScanArgs {
     float *W_out;
     const int *seq_start;
     int B, Hk, H, T, dv, w_heads;  // w_heads: 0 when W0 is shared by the sequences
-    int warps;                     // compute warps of a block, 16 columns of W each
+    int cgs;                       // column groups of a block: 16 columns of W, two warps each
     int stages;
     Images im;
+    float *saveS, *saveX;          // kSave: [slot][H][DK][dv] and [slot][H][64][dv]
     int *status;
 };
 
-constexpr int kScanStatus = 61;
-
-// Bytes of one stage: K, Q, T (two terms), P (one or two), vectors.
-template <int DK, bool BF16, bool ZF>
+// Bytes of one stage: K, (Q,) H (two terms), (M, one or two terms,) vectors.
+template <int DK, bool BF16, int MODE>
 constexpr int scan_stage_bytes() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * kImg + (ZF ? 2 : 1) * kImg + kVecBytes;
+    return (MODE == kSave ? 1 : 2) * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 +
+           (MODE == kSave ? 0 : MODE == kZ32 ? 2 : 1) * kImg + kScanVecBytes;
 }
 template <bool BF16>
 constexpr int v_tile_bytes() { return BF16 ? C * 32 : C * 20 * 4; }
+// A warp's own area behind the stages: its V tile and what it hands its partner.
+template <bool BF16, int MODE>
+constexpr int warp_bytes() { return v_tile_bytes<BF16>() + (MODE == kSave ? 4096 : 6144); }
 
-// Scan over the chunks. A warp owns 16 columns of W for the whole sequence, as the
-// rows of W^T [16][DK] in accumulator registers: accumulator fragments
-// packed pairwise are A fragments, so W^T K^T, X^T T^T, rho^T P^T and
-// rho^T K follow one another in registers, and no warp waits for another.
+// Scan over the chunks. Two warps own 16 columns of W for the whole sequence, as
+// rows of W^T [16][DK] in accumulator registers, half of DK each: accumulator
+// fragments packed pairwise are A fragments, so W^T K^T, X^T M^T and X^T H follow
+// one another in registers, and the only thing the two hand one another is
+// their halves of the sums over DK, once a chunk, through shared memory. Both
+// then form X (the same bits), each writes Z of half the tokens and updates its
+// half of W. Column groups know nothing of one another.
 // The chunk's images come through a ring of shared-memory stages, filled with
 // bulk copies that the first thread issues; V through registers, one chunk ahead.
-// ZF: Z in fp32, its products with two terms.
-template <int DK, bool BF16, bool ZF>
+template <int DK, bool BF16, int MODE>
 __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(1024) char ssm[];
     __shared__ uint64_t full[4], empty[4];
     __shared__ int abort_flag;
-    constexpr int STAGE = scan_stage_bytes<DK, BF16, ZF>();
+    constexpr bool ZF = MODE == kZ32, SAVE = MODE == kSave;
+    constexpr int STAGE = scan_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
-    constexpr int NT = DK / 8;
-    const int groups = a.dv / (16 * a.warps);
+    constexpr int NT = DK / 16;  // 8-column tiles of this warp's half of W^T
+    constexpr int oH = SAVE ? KALL : 2 * KALL, oM = oH + 2 * KIMG;
+    const int groups = a.dv / (16 * a.cgs);
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp & 1;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -368,7 +555,7 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
         abort_flag = 0;
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], a.warps);
+            mbar_init(&empty[s], 2 * a.cgs);
         }
         fence_mbar_init();
     }
@@ -385,18 +572,23 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
         const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
         mbar_arrive_expect_tx(&full[s], STAGE);
         bulk_load(d, a.im.K + ks * KALL, KALL, &full[s]);
-        bulk_load(d + KALL, a.im.Q + ks * KALL, KALL, &full[s]);
-        bulk_load(d + 2 * KALL, a.im.T + hs * 2 * kImg, 2 * kImg, &full[s]);
-        bulk_load(d + 2 * KALL + 2 * kImg, a.im.P + hs * 2 * kImg, (ZF ? 2 : 1) * kImg, &full[s]);
-        bulk_load(d + STAGE - kVecBytes, a.im.vec + hs * kVecBytes, kVecBytes, &full[s]);
+        if (!SAVE) bulk_load(d + KALL, a.im.Q + ks * KALL, KALL, &full[s]);
+        bulk_load(d + oH, a.im.H + hs * 2 * KIMG, 2 * KIMG, &full[s]);
+        if (!SAVE) bulk_load(d + oM, a.im.M + hs * 2 * kImg, (ZF ? 2 : 1) * kImg, &full[s]);
+        bulk_load(d + STAGE - kScanVecBytes, a.im.vec + hs * kVecBytes, kScanVecBytes, &full[s]);
     };
     if (tid == 0)
         for (int c = 0; c < nchunk && c < a.stages - 1; ++c) fill(c);
 
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = (grp * a.warps + warp) * 16;
+    const int v0 = (grp * a.cgs + (warp >> 1)) * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *vt = ssm + a.stages * STAGE + warp * v_tile_bytes<BF16>();
+    char *own = ssm + a.stages * STAGE + warp * warp_bytes<BF16, MODE>();
+    char *vt = own;
+    float4 *give = reinterpret_cast<float4 *>(own + v_tile_bytes<BF16>()) + lane;
+    const float4 *take = reinterpret_cast<const float4 *>(
+                             ssm + a.stages * STAGE + (warp ^ 1) * warp_bytes<BF16, MODE>() +
+                             v_tile_bytes<BF16>()) + lane;
     constexpr int VU = BF16 ? 4 : 8;  // 16-byte units of V per lane
     uint4 vr[VU];
     auto fetch_v = [&](int c) {
@@ -413,81 +605,109 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
             }
         }
     };
-    // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns 8 nt + 2 q4 + {0, 1}
+    // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns k0 + 8 nt + 2 q4 + {0, 1}
+    const int k0 = half * (DK / 2);
     float S[NT][4];
-    const size_t state = (size_t)DK * a.dv;
-    const float *w0 =
-        a.W0 ? a.W0 + ((size_t)n * a.w_heads + h) * state + v0 : nullptr;
+    const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
+    const float *w0 = a.W0 ? a.W0 + ((size_t)n * a.w_heads + h) * state + mine : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            S[nt][e] = w0 ? w0[(size_t)(8 * nt + 2 * q4 + (e & 1)) * a.dv + gq + (e >> 1) * 8] : 0.f;
+            S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
     if (nchunk > 0) fetch_v(0);
 
     for (int c = 0; c < nchunk; ++c) {
         const int s = c % a.stages;
         if (tid == 0 && c + a.stages - 1 < nchunk) fill(c + a.stages - 1);
-        if (!mbar_wait_warp(&full[s], (c / a.stages) & 1, abort, a.status, kScanStatus)) {
+        const bool ok = mbar_wait_warp(&full[s], (c / a.stages) & 1, abort, a.status, kScanStatus);
+        const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
+        const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
+        // both warps are past reading what the other gave for the chunk before;
+        // and leave together when a wait has run out
+        if (named_bar_or(1 + (warp >> 1), 64, !ok)) {
             // copies in flight land before the block's shared memory goes
             if (tid == 0)
                 for (int p = c; p < c + a.stages && p < nchunk; ++p)
                     mbar_drain(&full[p % a.stages], (p / a.stages) & 1);
             return;
         }
-        const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uT = uQ + KALL,
-                       uP = uT + 2 * kImg;
-        const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kVecBytes);
-
-        // X^T = W^T K^T, Z^T = W^T Q^T (both still scaled)
-        float X[8][4] = {}, Z[8][4] = {};
-        float iS[2];
-        {
-            float sS[2];
+        if (SAVE) {
+            float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float m = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    m = fmaxf(m, fmaxf(fabsf(S[nt][2 * x]), fabsf(S[nt][2 * x + 1])));
-                pow2_scale(quad_max(m), sS[x], iS[x]);
-            }
-#pragma unroll
-            for (int kk = 0; kk < DK / 16; ++kk) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int nt = 2 * kk + (r >> 1), x = r & 1;
-                    split_f16(S[nt][2 * x] * sS[x], S[nt][2 * x + 1] * sS[x], hi[r], lo[r]);
-                }
-#pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    uint32_t bk[4], bq[4];
-                    load_b(bk, uK, 16 * np, 16 * kk, lane);
-                    load_b(bq, uQ, 16 * np, 16 * kk, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(X[2 * np + x], hi, bk[2 * x], bk[2 * x + 1]);
-                        mma_f16(X[2 * np + x], lo, bk[2 * x], bk[2 * x + 1]);
-                        mma_f16(Z[2 * np + x], hi, bq[2 * x], bq[2 * x + 1]);
-                        if (ZF) mma_f16(Z[2 * np + x], lo, bq[2 * x], bq[2 * x + 1]);
-                    }
-                    if (!BF16) {
-                        load_b(bk, uK + KIMG, 16 * np, 16 * kk, lane);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(X[2 * np + x], hi, bk[2 * x], bk[2 * x + 1]);
-                        if (ZF) {
-                            load_b(bq, uQ + KIMG, 16 * np, 16 * kk, lane);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                mma_f16(Z[2 * np + x], hi, bq[2 * x], bq[2 * x + 1]);
-                        }
-                    }
-                }
-            }
+                for (int e = 0; e < 4; ++e)
+                    ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
         }
 
-        // X = V - D K W
+        // X^T = W^T K^T, Z^T = W^T Q^T over this warp's half of DK
+        float X[8][4] = {}, Z[8][4] = {};
+        {
+            float sS[2], iS[2];
+            row_scales<NT>(S, sS, iS);
+#pragma unroll
+            for (int kk = 0; kk < NT / 2; ++kk) {
+                uint32_t hi[4], lo[4], bb[4][4];
+                a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) load_b(bb[np], uK, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                if (!SAVE) {
+#pragma unroll
+                    for (int np = 0; np < 4; ++np) load_b(bb[np], uQ, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+                        mma_f16(Z[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                    if (ZF)
+#pragma unroll
+                        for (int nt = 0; nt < 8; ++nt)
+                            mma_f16(Z[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                }
+                if (!BF16) {
+#pragma unroll
+                    for (int np = 0; np < 4; ++np)
+                        load_b(bb[np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+                        mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                    if (ZF) {
+#pragma unroll
+                        for (int np = 0; np < 4; ++np)
+                            load_b(bb[np], uQ + KIMG, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                        for (int nt = 0; nt < 8; ++nt)
+                            mma_f16(Z[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[nt][e] *= iS[e >> 1], Z[nt][e] *= iS[e >> 1];
+        }
+        // hand over: all of X, and Z of the tokens that the partner writes. The
+        // 16-token blocks 0 and 3 are the first warp's, 1 and 2 the second's, so
+        // that both take the same share of the triangle P.
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) give[32 * nt] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
+        if (!SAVE) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float(&zA)[4] = Z[2 * (y ? 2 : 1) + x], (&zB)[4] = Z[2 * (y ? 3 : 0) + x];
+                    give[32 * (8 + 2 * y + x)] =
+                        half ? make_float4(zB[0], zB[1], zB[2], zB[3])
+                             : make_float4(zA[0], zA[1], zA[2], zA[3]);
+                }
+        }
+        // V of this chunk to shared memory, the next chunk's on its way
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
             const int u = lane + 32 * i;
@@ -497,8 +717,11 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
             char *d = BF16 ? vt + row * 32 + ((part ^ ((row >> 2) & 1)) << 4) : vt + row * 80 + part * 16;
             *reinterpret_cast<uint4 *>(d) = vr[i];
         }
-        __syncwarp();
         if (c + 1 < nchunk) fetch_v(c + 1);
+        named_bar(1 + (warp >> 1), 64);
+
+        // X = V - D K W
+        float m0 = 0.f, m1 = 0.f;
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             float v[2][4];
@@ -523,168 +746,129 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * np + 8 * x + 2 * q4);
-                float(&X4)[4] = X[2 * np + x];
-                X4[0] = v[x][0] - ck.x * (iS[0] * X4[0]);
-                X4[1] = v[x][1] - ck.y * (iS[0] * X4[1]);
-                X4[2] = v[x][2] - ck.x * (iS[1] * X4[2]);
-                X4[3] = v[x][3] - ck.y * (iS[1] * X4[3]);
+                const int nt = 2 * np + x;
+                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 8 * nt + 2 * q4);
+                const float4 o = take[32 * nt];
+                // first half plus second half, in both warps
+                X[nt][0] = v[x][0] - ck.x * (X[nt][0] + o.x);
+                X[nt][1] = v[x][1] - ck.y * (X[nt][1] + o.y);
+                X[nt][2] = v[x][2] - ck.x * (X[nt][2] + o.z);
+                X[nt][3] = v[x][3] - ck.y * (X[nt][3] + o.w);
+                m0 = fmaxf(m0, fmaxf(fabsf(X[nt][0]), fabsf(X[nt][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(X[nt][2]), fabsf(X[nt][3])));
             }
         }
-        __syncwarp();
 
-        // rho^T = X^T T^T
-        float rho[8][4] = {};
-        {
-            float sX[2], iX[2];
+        if (SAVE) {
+            float *wx = a.saveX + ((size_t)(slot0 + c) * a.H + h) * C * a.dv + v0 + gq;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float m = 0.f;
+            for (int y = 0; y < 4; ++y) {
+                const int nt = 4 * half + y;
+                float x[4];  // chosen by value: a pointer into X would send it to memory
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    m = fmaxf(m, fmaxf(fabsf(X[nt][2 * x]), fabsf(X[nt][2 * x + 1])));
-                pow2_scale(quad_max(m), sX[x], iX[x]);
+                for (int e = 0; e < 4; ++e) x[e] = half ? X[4 + y][e] : X[y][e];
+                float *w = wx + (size_t)(8 * nt + 2 * q4) * a.dv;
+                w[0] = x[0], w[8] = x[2], w[a.dv] = x[1], w[a.dv + 8] = x[3];
             }
+        }
+        // X's terms, for both products that take it
+        uint32_t hi[4][4], lo[4][4];
+        float sX[2], iX[2];
+        pow2_scale(quad_max(m0), sX[0], iX[0]);
+        pow2_scale(quad_max(m1), sX[1], iX[1]);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) a_terms(X[2 * jj], X[2 * jj + 1], sX, hi[jj], lo[jj]);
+
+        // Z^T += X^T M^T of this warp's tokens
+        if (!SAVE) {
+            float Y[4][4] = {};
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                uint32_t hi[4], lo[4];
+                uint32_t bb[2][4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int nt = 2 * jj + (r >> 1), x = r & 1;
-                    split_f16(X[nt][2 * x] * sX[x], X[nt][2 * x + 1] * sX[x], hi[r], lo[r]);
-                }
-#pragma unroll
-                for (int np = jj; np < 4; ++np) {  // T_ij is zero for i < j
-                    uint32_t th[4], tl[4];
-                    load_b(th, uT, 16 * np, 16 * jj, lane);
-                    load_b(tl, uT + kImg, 16 * np, 16 * jj, lane);
+                for (int y = 0; y < 2; ++y) {
+                    const int np = half ? 1 + y : 3 * y;
+                    if (np < jj) continue;  // M_ij is zero for i < j; the same for the whole warp
+                    load_b(bb[y], uM, 16 * np, 16 * jj, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(rho[2 * np + x], hi, th[2 * x], th[2 * x + 1]);
-                        mma_f16(rho[2 * np + x], lo, th[2 * x], th[2 * x + 1]);
-                        mma_f16(rho[2 * np + x], hi, tl[2 * x], tl[2 * x + 1]);
+                        mma_f16(Y[2 * y + x], hi[jj], bb[y][2 * x], bb[y][2 * x + 1]);
+                        if (ZF) mma_f16(Y[2 * y + x], lo[jj], bb[y][2 * x], bb[y][2 * x + 1]);
+                    }
+                    if (ZF) {
+                        load_b(bb[y], uM + kImg, 16 * np, 16 * jj, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            mma_f16(Y[2 * y + x], hi[jj], bb[y][2 * x], bb[y][2 * x + 1]);
                     }
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 it = *reinterpret_cast<const float2 *>(vec + kVt * C + 8 * nt + 2 * q4);
-                rho[nt][0] *= iX[0] * it.x;
-                rho[nt][1] *= iX[0] * it.y;
-                rho[nt][2] *= iX[1] * it.x;
-                rho[nt][3] *= iX[1] * it.y;
-            }
-        }
-
-        // Z^T += rho^T P^T
-        {
-            float sR[2], iR[2], Y[8][4] = {};
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float m = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    m = fmaxf(m, fmaxf(fabsf(rho[nt][2 * x]), fabsf(rho[nt][2 * x + 1])));
-                pow2_scale(quad_max(m), sR[x], iR[x]);
-            }
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int nt = 2 * jj + (r >> 1), x = r & 1;
-                    split_f16(rho[nt][2 * x] * sR[x], rho[nt][2 * x + 1] * sR[x], hi[r], lo[r]);
-                }
-#pragma unroll
-                for (int np = jj; np < 4; ++np) {
-                    uint32_t ph[4], pl[4];
-                    load_b(ph, uP, 16 * np, 16 * jj, lane);
-                    if (ZF) load_b(pl, uP + kImg, 16 * np, 16 * jj, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(Y[2 * np + x], hi, ph[2 * x], ph[2 * x + 1]);
-                        if (ZF) {
-                            mma_f16(Y[2 * np + x], lo, ph[2 * x], ph[2 * x + 1]);
-                            mma_f16(Y[2 * np + x], hi, pl[2 * x], pl[2 * x + 1]);
+                for (int x = 0; x < 2; ++x) {
+                    const int nt = 2 * (half ? 1 + y : 3 * y) + x;
+                    const float(&zA)[4] = Z[2 * (y ? 2 : 1) + x], (&zB)[4] = Z[2 * (y ? 3 : 0) + x];
+                    const float4 o = take[32 * (8 + 2 * y + x)];
+                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + 8 * nt + 2 * q4);
+                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + 8 * nt + 2 * q4);
+                    const float(&y4)[4] = Y[2 * y + x];
+                    const float z0 = cq.x * ((half ? zA[0] : zB[0]) + o.x) + im.x * (iX[0] * y4[0]);
+                    const float z1 = cq.y * ((half ? zA[1] : zB[1]) + o.y) + im.y * (iX[0] * y4[1]);
+                    const float z2 = cq.x * ((half ? zA[2] : zB[2]) + o.z) + im.x * (iX[1] * y4[2]);
+                    const float z3 = cq.y * ((half ? zA[3] : zB[3]) + o.w) + im.y * (iX[1] * y4[3]);
+                    if (ZF) {
+                        const int t = c * C + 8 * nt + 2 * q4;
+                        float *z = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
+                        if (t < len) z[0] = z0, z[8] = z2;
+                        if (t + 1 < len) z[a.dv] = z1, z[a.dv + 8] = z3;
+                    } else {
+                        // 8 x 8 blocks transposed between the lanes: a token per row
+                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(z0, z1);
+                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(z2, z3);
+                        const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
+                        const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
+                        const int t = c * C + 8 * nt + gq;
+                        if (t < len) {
+                            uint32_t *z = reinterpret_cast<uint32_t *>(
+                                static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
+                            z[0] = r0;
+                            z[4] = r1;
                         }
                     }
                 }
-            }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + 8 * nt + 2 * q4);
-                const float2 ip = *reinterpret_cast<const float2 *>(vec + kVp * C + 8 * nt + 2 * q4);
-                const float z0 = cq.x * (iS[0] * Z[nt][0]) + ip.x * (iR[0] * Y[nt][0]);
-                const float z1 = cq.y * (iS[0] * Z[nt][1]) + ip.y * (iR[0] * Y[nt][1]);
-                const float z2 = cq.x * (iS[1] * Z[nt][2]) + ip.x * (iR[1] * Y[nt][2]);
-                const float z3 = cq.y * (iS[1] * Z[nt][3]) + ip.y * (iR[1] * Y[nt][3]);
-                if (ZF) {
-                    const int t = c * C + 8 * nt + 2 * q4;
-                    float *z = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
-                    if (t < len) z[0] = z0, z[8] = z2;
-                    if (t + 1 < len) z[a.dv] = z1, z[a.dv + 8] = z3;
-                } else {
-                    // 8 x 8 blocks transposed between the lanes: a token per row
-                    const __nv_bfloat162 p0 = __floats2bfloat162_rn(z0, z1);
-                    const __nv_bfloat162 p1 = __floats2bfloat162_rn(z2, z3);
-                    const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
-                    const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
-                    const int t = c * C + 8 * nt + gq;
-                    if (t < len) {
-                        uint32_t *z = reinterpret_cast<uint32_t *>(
-                            static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
-                        z[0] = r0;
-                        z[4] = r1;
-                    }
-                }
-            }
         }
 
-        // W'^T = exp(G_C) W^T + (rho u)^T K
+        // W'^T = exp(G_C) W^T + X^T H
         {
-            float sR[2], iR[2];
-            float m0 = 0.f, m1 = 0.f;
+            const float gam = vec[kVs * C], iH = vec[kVs * C + 1];
+            const float iU[2] = {iX[0] * iH, iX[1] * iH};
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 cu = *reinterpret_cast<const float2 *>(vec + kVu * C + 8 * nt + 2 * q4);
-                rho[nt][0] *= cu.x, rho[nt][1] *= cu.y, rho[nt][2] *= cu.x, rho[nt][3] *= cu.y;
-                m0 = fmaxf(m0, fmaxf(fabsf(rho[nt][0]), fabsf(rho[nt][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(rho[nt][2]), fabsf(rho[nt][3])));
-            }
-            pow2_scale(quad_max(m0), sR[0], iR[0]);
-            pow2_scale(quad_max(m1), sR[1], iR[1]);
-            uint32_t hi[4][4], lo[4][4];
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int nt = 2 * jj + (r >> 1), x = r & 1;
-                    split_f16(rho[nt][2 * x] * sR[x], rho[nt][2 * x + 1] * sR[x], hi[jj][r], lo[jj][r]);
-                }
-            const float gam = vec[kVgam * C];
-#pragma unroll
-            for (int np = 0; np < DK / 16; ++np) {
-                float U[2][4] = {};
+            for (int np = 0; np < NT / 2; np += 2) {  // two 16-column blocks: four chains
+                float U[4][4] = {};
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bk[4];
-                    load_bt(bk, uK, 16 * jj, 16 * np, lane);
+                    uint32_t bb[2][4], bl[2][4];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(U[x], hi[jj], bk[2 * x], bk[2 * x + 1]);
-                        mma_f16(U[x], lo[jj], bk[2 * x], bk[2 * x + 1]);
+                    for (int y = 0; y < 2; ++y) {
+                        load_bt(bb[y], uH, 16 * jj, k0 + 16 * (np + y), lane);
+                        load_bt(bl[y], uH + KIMG, 16 * jj, k0 + 16 * (np + y), lane);
                     }
-                    if (!BF16) {
-                        load_bt(bk, uK + KIMG, 16 * jj, 16 * np, lane);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(U[x], hi[jj], bk[2 * x], bk[2 * x + 1]);
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        mma_f16(U[x], hi[jj], bb[x >> 1][2 * (x & 1)], bb[x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_f16(U[x], lo[jj], bb[x >> 1][2 * (x & 1)], bb[x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_f16(U[x], hi[jj], bl[x >> 1][2 * (x & 1)], bl[x >> 1][2 * (x & 1) + 1]);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        S[2 * np + x][e] = fmaf(iR[e >> 1], U[x][e], gam * S[2 * np + x][e]);
+                        S[2 * np + x][e] = fmaf(iU[e >> 1], U[x][e], gam * S[2 * np + x][e]);
             }
         }
         __syncwarp();
@@ -692,12 +876,12 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
     }
 
     if (a.W_out) {
-        float *w = a.W_out + ((size_t)n * a.H + h) * state + v0;
+        float *w = a.W_out + ((size_t)n * a.H + h) * state + mine;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                w[(size_t)(8 * nt + 2 * q4 + (e & 1)) * a.dv + gq + (e >> 1) * 8] = S[nt][e];
+                w[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
     }
 }
 
@@ -713,37 +897,37 @@ cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
     return e;
 }
 
-// Compute warps of a block: all of a head's columns when there are heads enough
-// to fill the SMs, else half or a quarter of them, so that more SMs take part.
-int scan_warps(long long heads, int dv) {
-    int w = dv / 16;
-    while (w > 2 && heads * (dv / (16 * w)) < 148) w /= 2;
-    return w;
-}
-
-template <int DK, bool BF16, bool ZF>
+template <int DK, bool BF16, int MODE>
 cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
-    r.warps = scan_warps((long long)N * r.H, r.dv);
-    constexpr int stage = scan_stage_bytes<DK, BF16, ZF>();
-    const int vbytes = r.warps * v_tile_bytes<BF16>();
-    r.stages = (226 * 1024 - vbytes) / stage;
+    r.cgs = scan_groups((long long)N * r.H, r.dv);
+    constexpr int stage = scan_stage_bytes<DK, BF16, MODE>();
+    const int wbytes = 2 * r.cgs * warp_bytes<BF16, MODE>();
+    r.stages = (226 * 1024 - wbytes) / stage;
     r.stages = r.stages > 3 ? 3 : r.stages;
-    const int smem = r.stages * stage + vbytes;
-    cudaError_t e = cudaFuncSetAttribute(delta_scan_kernel<DK, BF16, ZF>,
+    const int smem = r.stages * stage + wbytes;
+    cudaError_t e = cudaFuncSetAttribute(delta_scan_kernel<DK, BF16, MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.warps)));
-    delta_scan_kernel<DK, BF16, ZF><<<grid, 32 * r.warps, smem, s>>>(r);
+    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
+    delta_scan_kernel<DK, BF16, MODE><<<grid, 64 * r.cgs, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
 }
 
+template <int DK, bool BF16>
+cudaError_t scan_mode(const ScanArgs &r, int N, int mode, cudaStream_t s) {
+    return mode == kZ16   ? scan_inst<DK, BF16, kZ16>(r, N, s)
+           : mode == kZ32 ? scan_inst<DK, BF16, kZ32>(r, N, s)
+                          : scan_inst<DK, BF16, kSave>(r, N, s);
+}
+
 }  // namespace
 
-Images images_at(const Plan &p, void *workspace) {
+Images images_at(const Plan &p, void *workspace, bool bwd) {
     char *w = static_cast<char *>(workspace);
-    return Images{w + p.oK, w + p.oQ, w + p.oT, w + p.oP, w + p.oV, p.kimg};
+    return Images{w + p.oK, w + p.oQ, w + p.oM, w + p.oH, bwd ? w + p.oT : nullptr, w + p.oV,
+                  p.kimg, p.himg};
 }
 
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s) {
@@ -753,6 +937,28 @@ cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cud
     return a.bf16 ? prep_inst<128, true>(r, blocks, s) : prep_inst<128, false>(r, blocks, s);
 }
 
+// Column groups of a block (one block per SM): one or two leave each warp a
+// scheduler of its own, four share them. The fewest rounds of blocks over the 148
+// SMs win, a round of four-group blocks counted 1.6 times.
+int scan_groups(long long heads, int dv) {
+    int best = 1;
+    double least = 1e30;
+    for (int cgs = 1; cgs <= 4; cgs *= 2) {
+        const double rounds = (double)((heads * (dv / (16 * cgs)) + 147) / 148) * (cgs == 4 ? 1.6 : 1.0);
+        if (rounds <= least) least = rounds, best = cgs;
+    }
+    return best;
+}
+
+cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
+                        cudaStream_t s) {
+    const ScanArgs r{a.V, a.W0, a.Z, a.W_out, a.seq_start, a.B, a.Hk, a.H, a.T, a.dv,
+                     a.w0_per_seq ? a.H : 0, 0, 0, im, saveS, saveX, device_status_word()};
+    if (a.dk == 64)
+        return a.bf16 ? scan_mode<64, true>(r, a.N, mode, s) : scan_mode<64, false>(r, a.N, mode, s);
+    return a.bf16 ? scan_mode<128, true>(r, a.N, mode, s) : scan_mode<128, false>(r, a.N, mode, s);
+}
+
 }  // namespace delta
 
 using namespace delta;
@@ -760,22 +966,15 @@ using namespace delta;
 size_t delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed,
                              bool bf16) {
     (void)dv;
-    return make_plan(B, Hk, H, T, dk, N, packed, bf16).end;
+    return make_plan(B, Hk, H, T, dk, N, packed, bf16, false).end;
 }
 
 cudaError_t launch_delta_fwd(const DeltaArgs &a, cudaStream_t s) {
-    const Plan p = make_plan(a.B, a.Hk, a.H, a.T, a.dk, a.N, a.seq_start != nullptr, a.bf16);
-    const Images im = images_at(p, a.workspace);
-    cudaError_t e = launch_prep(a, p, im, s);
+    const Plan p = make_plan(a.B, a.Hk, a.H, a.T, a.dk, a.N, a.seq_start != nullptr, a.bf16, false);
+    const Images im = images_at(p, a.workspace, false);
+    const cudaError_t e = launch_prep(a, p, im, s);
     if (e != cudaSuccess) return e;
-    const ScanArgs r{a.V, a.W0, a.Z, a.W_out, a.seq_start, a.B, a.Hk, a.H, a.T, a.dv,
-                     a.w0_per_seq ? a.H : 0, 0, 0, im, device_status_word()};
-    if (a.dk == 64) {
-        if (a.bf16) return a.z_bf16 ? scan_inst<64, true, false>(r, a.N, s) : scan_inst<64, true, true>(r, a.N, s);
-        return a.z_bf16 ? scan_inst<64, false, false>(r, a.N, s) : scan_inst<64, false, true>(r, a.N, s);
-    }
-    if (a.bf16) return a.z_bf16 ? scan_inst<128, true, false>(r, a.N, s) : scan_inst<128, true, true>(r, a.N, s);
-    return a.z_bf16 ? scan_inst<128, false, false>(r, a.N, s) : scan_inst<128, false, true>(r, a.N, s);
+    return launch_scan(a, im, a.z_bf16 ? kZ16 : kZ32, nullptr, nullptr, s);
 }
 
 }  // namespace ttt

@@ -24,15 +24,21 @@ using namespace sm100;
 constexpr int C = kDeltaC;
 constexpr int kImg = C * C * 2;  // bytes of a 64 x 64 fp16 image
 
-// Per chunk and value head: eight vectors of 64 floats.
-enum Vec { kVk, kVt, kVu, kVq, kVp, kVeta, kVgam, kVspare, kVecs };
-// kVk  exp(G_j) / sK_j          (K S, Om K)            sX: the scale of row j of image X
-// kVt  1 / sT_i
-// kVu  exp(G_C - G_j) eta_j / sK_j
-// kVq  c exp(G_i) / sQ_i
-// kVp  1 / sP_i
-// kVeta: 1 / sK_j; kVgam: [0] exp(G_C); kVspare: 1 / sQ_i
-constexpr int kVecBytes = kVecs * C * 4;
+// Per chunk and value head: vectors of 64 floats; sX is the scale of row j
+// of image X. The scans read the first four.
+enum Vec {
+    kVk,   // exp(G_j) / sK_j
+    kVq,   // c exp(G_i) / sQ_i
+    kVm,   // 1 / sM_i
+    kVs,   // [0] exp(G_C), [1] 1 / sH (one scale for the image of H)
+    kVik,  // 1 / sK_j
+    kViq,  // 1 / sQ_i
+    kVgh,  // G_j as the sum of two floats
+    kVgl,
+    kVit,  // 1 / sT_i
+    kVecs
+};
+constexpr int kVecBytes = kVecs * C * 4, kScanVecBytes = 4 * C * 4;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -93,21 +99,55 @@ __device__ __forceinline__ float quad_max(float v) {
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+// A fragments of a 16 x 16 block held as two accumulator tiles (columns 0..7 and
+// 8..15), both terms; s: the scales of rows gq and gq + 8.
+__device__ __forceinline__ void a_terms(const float (&t0)[4], const float (&t1)[4],
+                                        const float (&s)[2], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split_f16(t0[0] * s[0], t0[1] * s[0], hi[0], lo[0]);
+    split_f16(t0[2] * s[1], t0[3] * s[1], hi[1], lo[1]);
+    split_f16(t1[0] * s[0], t1[1] * s[0], hi[2], lo[2]);
+    split_f16(t1[2] * s[1], t1[3] * s[1], hi[3], lo[3]);
+}
+// Scales of a warp's two rows over N accumulator tiles.
+template <int N>
+__device__ __forceinline__ void row_scales(const float (&t)[N][4], float (&s)[2], float (&inv)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, fmaxf(fabsf(t[i][2 * x]), fabsf(t[i][2 * x + 1])));
+        pow2_scale(quad_max(m), s[x], inv[x]);
+    }
+}
+
+__device__ __forceinline__ void named_bar(int id, int nthreads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// What a scan writes: Z as bf16, Z as fp32, or (for the backward) the weight
+// each chunk starts from and X.
+enum ScanMode { kZ16, kZ32, kSave };
+constexpr int kScanStatus = 61;
+
 // Workspace: per chunk slot and head, the images that the scans read.
+//   K, Q [key head]: the chunk's rows, one fp16 term (bf16 inputs) or two
+//   M, H [value head], two terms each: M = P T [64][64], H = T^T diag(u) K [64][dk]
+//   T [value head], two terms, only for the backward
+//   vec [value head]: the vectors above
 struct Plan {
     int slots;          // chunk slots of all sequences
-    int terms;          // fp16 terms of Q and K: 1 (bf16 inputs) or 2
-    size_t kimg;        // bytes of one chunk's K (or Q) image, all terms
-    size_t oK, oQ, oT, oP, oV, end;
+    size_t kimg, himg;  // bytes of one chunk's K (or Q), and H
+    size_t oK, oQ, oM, oH, oT, oV, end;
 };
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-inline Plan make_plan(int B, int Hk, int H, int T, int dk, int N, bool packed, bool bf16) {
+inline Plan make_plan(int B, int Hk, int H, int T, int dk, int N, bool packed, bool bf16,
+                      bool bwd) {
     Plan p;
     // packed: sequence n starts at slot start / 64 + n, so that the slots of two
     // sequences never meet, whatever the offsets
     p.slots = packed ? T / C + N : B * ((T + C - 1) / C);
-    p.terms = bf16 ? 1 : 2;
-    p.kimg = (size_t)C * dk * 2 * p.terms;
+    p.kimg = (size_t)C * dk * 2 * (bf16 ? 1 : 2);
+    p.himg = (size_t)C * dk * 2 * 2;
     size_t o = 0;
     auto take = [&](size_t n) {
         const size_t at = o;
@@ -116,17 +156,19 @@ inline Plan make_plan(int B, int Hk, int H, int T, int dk, int N, bool packed, b
     };
     p.oK = take((size_t)p.slots * Hk * p.kimg);
     p.oQ = take((size_t)p.slots * Hk * p.kimg);
-    p.oT = take((size_t)p.slots * H * 2 * kImg);
-    p.oP = take((size_t)p.slots * H * 2 * kImg);
+    p.oM = take((size_t)p.slots * H * 2 * kImg);
+    p.oH = take((size_t)p.slots * H * p.himg);
     p.oV = take((size_t)p.slots * H * kVecBytes);
+    p.oT = o;
+    if (bwd) take((size_t)p.slots * H * 2 * kImg);
     p.end = o;
     return p;
 }
 
-// Where the kernels find the images of a chunk.
+// Where the kernels find the images of a chunk; T is NULL in the forward.
 struct Images {
-    char *K, *Q, *T, *P, *vec;
-    size_t kimg;
+    char *K, *Q, *M, *H, *T, *vec;
+    size_t kimg, himg;
 };
 
 __device__ __forceinline__ int first_slot(const int *seq_start, int n, int T, int t0) {
@@ -135,7 +177,10 @@ __device__ __forceinline__ int first_slot(const int *seq_start, int n, int T, in
 
 // The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
-Images images_at(const Plan &p, void *workspace);
+Images images_at(const Plan &p, void *workspace, bool bwd);
+int scan_groups(long long heads, int dv);
+cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
+                        cudaStream_t s);
 
 }  // namespace delta
 }  // namespace ttt
