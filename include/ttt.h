@@ -499,6 +499,31 @@ TTT_API ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, co
                                  void *workspace, size_t workspace_bytes, ttt_stream stream);
 
 /*
+ * Gated delta rule backward: the gradients of every input of ttt_delta_fwd,
+ * through the weight updates, given dZ [B][H][T][dv] fp32 and, optionally,
+ * dW_out [N][H][dk][dv] fp32 (NULL: zero). Outputs fp32, overwritten:
+ *   dQ, dK [B][Hk][T][dk] (summed over the value heads that share them),
+ *   dV [B][H][T][dv], deta [B][H][T], dg [B][H][T] (with g, else NULL), dW0
+ *   (with W0, else NULL) [N][H][dk][dv] with TTT_F_W0_PER_SEQ, else [H][dk][dv],
+ *   summed over the sequences. Tokens outside every packed sequence get zeros.
+ * Inputs, types and limits as ttt_delta_fwd; the forward is run again, nothing
+ * is kept from it. workspace: at least ttt_delta_bwd_workspace_bytes(...) bytes,
+ * 256-byte aligned, clobbered (per chunk of 64 tokens and head 8 dk dv + 256 dv
+ * bytes for the weights and gradients at its ends, and the forward's images);
+ * calls that share one must not overlap on the GPU. Deterministic: no atomics.
+ * flags: TTT_F_W0_PER_SEQ.
+ */
+TTT_API size_t ttt_delta_bwd_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv,
+                                             int n_seq, ttt_dtype dt);
+TTT_API ttt_status ttt_delta_bwd(const void *Q, const void *K, const void *V, const float *eta,
+                                 const float *g, const float *W0, const float *dZ,
+                                 const float *dW_out, float *dQ, float *dK, float *dV, float *deta,
+                                 float *dg, float *dW0, const int *seq_start, int n_seq,
+                                 float q_scale, int B, int Hk, int H, int T, int dk, int dv,
+                                 ttt_dtype dt, unsigned flags, void *workspace,
+                                 size_t workspace_bytes, ttt_stream stream);
+
+/*
  * Gated delta rule decode: n tokens per row, the states in a pool, updated in
  * place, exactly as n calls with one token. Q, K [B][Hk][n][dk], V [B][H][n][dv],
  * eta, g [B][H][n] (g NULL: no decay), Z [B][H][n][dv].

@@ -99,6 +99,11 @@ def lib() -> ctypes.CDLL:
         L.ttt_delta_fwd.restype = _I
         L.ttt_delta_fwd.argtypes = ([_P] * 9 + [_I, ctypes.c_float] + [_I] * 7
                                     + [ctypes.c_uint, _P, ctypes.c_size_t, _P])
+        L.ttt_delta_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.ttt_delta_bwd_workspace_bytes.argtypes = [_I] * 8
+        L.ttt_delta_bwd.restype = _I
+        L.ttt_delta_bwd.argtypes = ([_P] * 15 + [_I, ctypes.c_float] + [_I] * 7
+                                    + [ctypes.c_uint, _P, ctypes.c_size_t, _P])
         L.ttt_delta_decode.restype = _I
         L.ttt_delta_decode.argtypes = ([_P] * 8 + [_I, ctypes.c_float] + [_I] * 7
                                        + [ctypes.c_uint, _P])
@@ -348,6 +353,20 @@ def ttt_delta_fwd(Q, K, V, eta, g, W0, Z, W_out, seq_start, n_seq, q_scale, B, H
                              _ptr(W_out), _ptr(seq_start), n_seq, q_scale, B, Hk, H, T, dk, dv,
                              dt, flags, _ptr(workspace), workspace_bytes, _stream(stream))
     return _check("ttt_delta_fwd", rc) if check else rc
+
+
+def ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt) -> int:
+    return int(lib().ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt))
+
+
+def ttt_delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out, dQ, dK, dV, deta, dg, dW0, seq_start, n_seq,
+                  q_scale, B, Hk, H, T, dk, dv, dt, flags, workspace, workspace_bytes, stream=None,
+                  check=True):
+    rc = lib().ttt_delta_bwd(*[_ptr(x) for x in (Q, K, V, eta, g, W0, dZ, dW_out, dQ, dK, dV, deta,
+                                                 dg, dW0, seq_start)],
+                             n_seq, q_scale, B, Hk, H, T, dk, dv, dt, flags, _ptr(workspace),
+                             workspace_bytes, _stream(stream))
+    return _check("ttt_delta_bwd", rc) if check else rc
 
 
 def ttt_delta_decode(Q, K, V, eta, g, W, Z, state_index, n_slots, q_scale, B, Hk, H, n, dk, dv,
@@ -784,6 +803,29 @@ def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None
         ttt_delta_fwd(Q, K, V, eta, g, W0, Z, W_out, seq_start, n_seq, q_scale, B, Hk, H, T, dk,
                       dv, _dtype_code(Q), flags, workspace, _nbytes(workspace), on.handle)
     return Z, W_out
+
+
+def delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out=None, *, w0_per_seq=False, seq_start=None,
+              q_scale=1.0, workspace=None, stream=None):
+    """Gated delta rule backward (ttt_delta_bwd): the gradients of sum(Z dZ) + sum(W_out dW_out)
+    for delta_fwd's inputs, as a dict of fp32 tensors Q, K, V, eta and, for what was given, g and
+    W0. dZ [B, H, T, dv] and dW_out [N, H, dk, dv] (or None) are fp32."""
+    import torch
+    with _On("delta_bwd", Q, stream) as on:
+        B, Hk, H, T, dk, dv, n_seq, N = _delta_shapes("delta_bwd", on.device, Q, K, V, eta, g, W0,
+                                                      w0_per_seq, seq_start)
+        f32 = torch.float32
+        _tensors("delta_bwd", on.device, dZ=(dZ, (f32,), (B, H, T, dv)),
+                 dW_out=(dW_out, (f32,), (N, H, dk, dv)))
+        grads = {n: on.empty(t.shape, f32) for n, t in
+                 dict(Q=Q, K=K, V=V, eta=eta, g=g, W0=W0).items() if t is not None}
+        need = ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, _dtype_code(Q))
+        workspace = on.workspace("delta_bwd", workspace, need or 256)
+        ttt_delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out, grads["Q"], grads["K"], grads["V"],
+                      grads["eta"], grads.get("g"), grads.get("W0"), seq_start, n_seq, q_scale, B,
+                      Hk, H, T, dk, dv, _dtype_code(Q), TTT_F_W0_PER_SEQ if w0_per_seq else 0,
+                      workspace, _nbytes(workspace), on.handle)
+    return grads
 
 
 def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, Z=None,

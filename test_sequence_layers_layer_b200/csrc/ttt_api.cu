@@ -755,6 +755,49 @@ ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, const floa
     return launched(launch_delta_fwd(a, cs));
 }
 
+size_t ttt_delta_bwd_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,
+                                     ttt_dtype dt) {
+    const int N = n_seq > 0 ? n_seq : B;
+    if (n_seq < 0 || (n_seq > 0 && B != 1) || (dt != TTT_BF16 && dt != TTT_FP32)) return 0;
+    if (check_delta_shape(B, Hk, H, T, dk, dv, N) != TTT_OK) return 0;
+    return delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, N, n_seq > 0, dt == TTT_BF16);
+}
+
+ttt_status ttt_delta_bwd(const void *Q, const void *K, const void *V, const float *eta,
+                         const float *g, const float *W0, const float *dZ, const float *dW_out,
+                         float *dQ, float *dK, float *dV, float *deta, float *dg, float *dW0,
+                         const int *seq_start, int n_seq, float q_scale, int B, int Hk, int H,
+                         int T, int dk, int dv, ttt_dtype dt, unsigned flags, void *workspace,
+                         size_t workspace_bytes, ttt_stream stream) {
+    if (flags & ~TTT_F_W0_PER_SEQ) return TTT_ERR_ARG;
+    if (!Q || !K || !V || !eta || !dZ || !dQ || !dK || !dV || !deta) return TTT_ERR_PTR;
+    if ((g && !dg) || (W0 && !dW0)) return TTT_ERR_PTR;
+    if ((dg && !g) || (dW0 && !W0)) return TTT_ERR_ARG;
+    if (seq_start ? (n_seq <= 0 || B != 1) : n_seq != 0) return TTT_ERR_ARG;
+    const int N = seq_start ? n_seq : B;
+    ttt_status st = check_delta_shape(B, Hk, H, T, dk, dv, N);
+    if (st != TTT_OK) return st;
+    if (dt != TTT_BF16 && dt != TTT_FP32) return TTT_ERR_DTYPE;
+    const void *ptrs[] = {Q, K, V, W0, dZ, dW_out, dQ, dK, dV, dW0, eta, g, deta, dg, seq_start,
+                          workspace};
+    for (int i = 0; i < 10; ++i)
+        if (!aligned16(ptrs[i])) return TTT_ERR_ALIGN;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+        workspace_bytes < ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt))
+        return TTT_ERR_WORKSPACE;
+    st = check_arch();
+    if (st != TTT_OK) return st;
+    st = check_device_ptrs(ptrs, 16);
+    if (st != TTT_OK) return st;
+    const DeltaBwdArgs a{{Q, K, V, eta, g, W0, nullptr, nullptr, seq_start, B, Hk, H, T, dk, dv, N,
+                          q_scale, dt == TTT_BF16, (flags & TTT_F_W0_PER_SEQ) != 0, false,
+                          workspace},
+                         dZ, dW_out, dQ, dK, dV, deta, dg, dW0};
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    timing_begin(cs);
+    return launched(launch_delta_bwd(a, cs));
+}
+
 ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V, const float *eta,
                             const float *g, float *W, void *Z, const int *state_index,
                             int n_slots, float q_scale, int B, int Hk, int H, int n, int dk,

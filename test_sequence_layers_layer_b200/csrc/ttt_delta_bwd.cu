@@ -1,0 +1,1022 @@
+// ttt_delta_bwd.cu -- backward of the gated delta rule, chunked.
+//
+// With the chunk's X = V - D K W, rho = T X, Z = c D Q W + M X,
+// W' = exp(G_C) W + H^T X (ttt_delta_chunk.cu) and Om = dL/dW':
+//   dX = M^T dZ + H Om = dV
+//   dL/dW = exp(G_C) Om + c Q^T D dZ - K^T D dX          (the reverse scan)
+// and per chunk, all chunks at once,
+//   phi_ij = c Gam_ij (dZ_i.rho_j) (j <= i),  eps_ij = -Gam_ij (dX_i.rho_j) (j < i)
+//   dQ = c D dZ W^T + (phi eta) K
+//   dK = -D dX W^T + diag(exp(G_C - G) eta) rho Om^T + (phi eta)^T Q + (E + E^T) K,
+//        E_ij = eps_ij eta_j
+//   deta_j = sum_i phi_ij (q_i.k_j) + sum_i eps_ij (k_i.k_j) + exp(G_C - G_j) k_j.(Om rho_j)
+//   dG_i = sum_j eta_j (phi_ij q_i.k_j + eps_ij k_i.k_j) - eta_i (the sums of deta_i)
+//          + q_i.(c D_i W dZ_i) - k_i.(D_i W dX_i),
+//   dG_C += sum_j eta_j exp(G_C - G_j) k_j.(Om rho_j) + exp(G_C) <W, Om>,
+//   dg_t = sum_{i >= t} dG_i.
+// The forward scan runs again first and keeps W at the start of each chunk and
+// X; the reverse scan keeps Om at its end. Everything is fp32, its products two
+// fp16 terms an operand (ttt_delta_mma.cuh). No atomics: every sum has one order.
+#include "../../include/ttt.h"
+#include "ttt_delta_mma.cuh"
+
+namespace ttt {
+namespace delta {
+namespace {
+
+// ---------------------------------------------------------------- reverse scan
+
+struct RevArgs {
+    const float *dZ, *dW_out;
+    float *dV, *dW0;               // dW0 [N][H][DK][dv] or NULL
+    const int *seq_start;
+    int B, Hk, H, T, dv, cgs, stages;
+    Images im;
+    float *saveO;                  // [slot][H][DK][dv]
+    int *status;
+};
+
+constexpr int kZTile = C * 20 * 4;  // 64 tokens x 16 columns, rows of 80 bytes
+constexpr int kRevWarpBytes = kZTile + 4096;
+
+template <int DK, bool BF16>
+constexpr int rev_stage_bytes() {
+    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 + 2 * kImg + kScanVecBytes;
+}
+
+// The mirror of the forward scan: two warps own 16 columns of Om, as rows of
+// Om^T in registers, half of DK each. dX^T = Om^T H^T + dZ^T M is summed over
+// both halves of DK, and over the two halves of the tokens for dZ^T M (blocks 0, 3
+// and 1, 2: the same share of the triangle), in one exchange.
+template <int DK, bool BF16>
+__global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
+    extern __shared__ __align__(1024) char ssm[];
+    __shared__ uint64_t full[4], empty[4];
+    __shared__ int abort_flag;
+    constexpr int STAGE = rev_stage_bytes<DK, BF16>();
+    constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
+    constexpr int NT = DK / 16;
+    constexpr int oH = 2 * KALL, oM = oH + 2 * KIMG;
+    const int groups = a.dv / (16 * a.cgs);
+    const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
+    const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp & 1;
+    int t0, len;
+    delta_span(a.seq_start, n, a.T, t0, len);
+    const int nchunk = (len + C - 1) / C;
+    const int slot0 = first_slot(a.seq_start, n, a.T, t0);
+    const int b = a.seq_start ? 0 : n;
+    volatile int *abort = &abort_flag;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 2 * a.cgs);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+
+    // step i works on chunk nchunk - 1 - i
+    auto fill = [&](int i) {
+        const int s = i % a.stages, c = nchunk - 1 - i;
+        if (i >= a.stages &&
+            !mbar_wait(&empty[s], ((i / a.stages) & 1) ^ 1, abort, a.status, kScanStatus))
+            return;
+        char *d = ssm + s * STAGE;
+        const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
+        mbar_arrive_expect_tx(&full[s], STAGE);
+        bulk_load(d, a.im.K + ks * KALL, KALL, &full[s]);
+        bulk_load(d + KALL, a.im.Q + ks * KALL, KALL, &full[s]);
+        bulk_load(d + oH, a.im.H + hs * 2 * KIMG, 2 * KIMG, &full[s]);
+        bulk_load(d + oM, a.im.M + hs * 2 * kImg, 2 * kImg, &full[s]);
+        bulk_load(d + STAGE - kScanVecBytes, a.im.vec + hs * kVecBytes, kScanVecBytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int i = 0; i < nchunk && i < a.stages - 1; ++i) fill(i);
+
+    const int gq = lane >> 2, q4 = lane & 3;
+    const int v0 = (grp * a.cgs + (warp >> 1)) * 16;
+    const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
+    char *own = ssm + a.stages * STAGE + warp * kRevWarpBytes;
+    float *zt = reinterpret_cast<float *>(own);
+    float4 *give = reinterpret_cast<float4 *>(own + kZTile) + lane;
+    const float4 *take = reinterpret_cast<const float4 *>(
+                             ssm + a.stages * STAGE + (warp ^ 1) * kRevWarpBytes + kZTile) + lane;
+    uint4 zr[8];
+    auto fetch_z = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int u = lane + 32 * i, row = u >> 2, part = u & 3;
+            zr[i] = make_uint4(0, 0, 0, 0);
+            if (c * C + row < len)
+                zr[i] = *reinterpret_cast<const uint4 *>(a.dZ + (vrow + c * C + row) * a.dv + v0 +
+                                                         4 * part);
+        }
+    };
+    const int k0 = half * (DK / 2);
+    float S[NT][4];
+    const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
+    const float *w0 = a.dW_out ? a.dW_out + ((size_t)n * a.H + h) * state + mine : nullptr;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
+    if (nchunk > 0) fetch_z(nchunk - 1);
+
+    for (int i = 0; i < nchunk; ++i) {
+        const int s = i % a.stages, c = nchunk - 1 - i;
+        if (tid == 0 && i + a.stages - 1 < nchunk) fill(i + a.stages - 1);
+        const bool ok = mbar_wait_warp(&full[s], (i / a.stages) & 1, abort, a.status, kScanStatus);
+        const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
+        const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
+        // both warps are past reading what the other gave for the chunk before;
+        // and leave together when a wait has run out
+        if (named_bar_or(1 + (warp >> 1), 64, !ok)) {
+            if (tid == 0)
+                for (int p = i; p < i + a.stages && p < nchunk; ++p)
+                    mbar_drain(&full[p % a.stages], (p / a.stages) & 1);
+            return;
+        }
+        {
+            float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int u = lane + 32 * j;
+            *reinterpret_cast<uint4 *>(zt + (u >> 2) * 20 + (u & 3) * 4) = zr[j];
+        }
+        __syncwarp();
+        if (i + 1 < nchunk) fetch_z(c - 1);
+
+        // dX^T = Om^T H^T over this warp's half of DK
+        float X[8][4] = {};
+        {
+            float sS[2], iS[2];
+            row_scales<NT>(S, sS, iS);
+#pragma unroll
+            for (int kk = 0; kk < NT / 2; ++kk) {
+                uint32_t hi[4], lo[4], bb[4][4];
+                a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) load_b(bb[np], uH, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int np = 0; np < 4; ++np)
+                    load_b(bb[np], uH + KIMG, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+            }
+            const float iH = vec[kVs * C + 1];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[nt][e] *= iS[e >> 1] * iH;
+        }
+        // + dZ^T M over this warp's tokens
+        {
+            float A[4][4], D[8][4] = {}, sA[2], iA[2];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int nt = 2 * ((y >> 1) ? (half ? 2 : 3) : (half ? 1 : 0)) + (y & 1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * nt + 2 * q4 + (e & 1);
+                    A[y][e] = zt[t * 20 + gq + (e >> 1) * 8] * vec[kVm * C + t];
+                }
+            }
+            row_scales<4>(A, sA, iA);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t hi[4], lo[4];
+                a_terms(A[2 * y], A[2 * y + 1], sA, hi, lo);
+                const int ii = y ? (half ? 2 : 3) : (half ? 1 : 0);
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    if (np > ii) continue;  // M_ij is zero for i < j; the same for the whole warp
+                    uint32_t bh[4], bl[4];
+                    load_bt(bh, uM, 16 * ii, 16 * np, lane);
+                    load_bt(bl, uM + kImg, 16 * ii, 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(D[2 * np + x], hi, bh[2 * x], bh[2 * x + 1]);
+                        mma_f16(D[2 * np + x], lo, bh[2 * x], bh[2 * x + 1]);
+                        mma_f16(D[2 * np + x], hi, bl[2 * x], bl[2 * x + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[nt][e] = fmaf(iA[e >> 1], D[nt][e], X[nt][e]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) give[32 * nt] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
+        named_bar(1 + (warp >> 1), 64);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const float4 o = take[32 * nt];
+            X[nt][0] += o.x, X[nt][1] += o.y, X[nt][2] += o.z, X[nt][3] += o.w;
+        }
+        // dV of half of the tokens
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int t = c * C + 8 * (4 * half + y) + 2 * q4;
+            float x[4];  // chosen by value: a pointer into X would send it to memory
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = half ? X[4 + y][e] : X[y][e];
+            float *w = a.dV + (vrow + t) * a.dv + v0 + gq;
+            if (t < len) w[0] = x[0], w[8] = x[2];
+            if (t + 1 < len) w[a.dv] = x[1], w[a.dv + 8] = x[3];
+        }
+
+        // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K), both under one scale
+        {
+            float Zq[8][4], sA[2], iA[2];
+            float m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * nt + 2 * q4 + (e & 1);
+                    Zq[nt][e] = zt[t * 20 + gq + (e >> 1) * 8] * vec[kVq * C + t];
+                    X[nt][e] *= -vec[kVk * C + t];
+                    m[e >> 1] = fmaxf(m[e >> 1], fmaxf(fabsf(Zq[nt][e]), fabsf(X[nt][e])));
+                }
+            pow2_scale(quad_max(m[0]), sA[0], iA[0]);
+            pow2_scale(quad_max(m[1]), sA[1], iA[1]);
+            uint32_t zh[4][4], zl[4][4], xh[4][4], xl[4][4];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                a_terms(Zq[2 * jj], Zq[2 * jj + 1], sA, zh[jj], zl[jj]);
+                a_terms(X[2 * jj], X[2 * jj + 1], sA, xh[jj], xl[jj]);
+            }
+            const float gam = vec[kVs * C];
+#pragma unroll
+            for (int np = 0; np < NT / 2; ++np) {
+                float U[4][4] = {};  // dZ^T Q in 0, 1 and dX^T K in 2, 3
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    uint32_t bq[4], bk[4];
+                    load_bt(bq, uQ, 16 * jj, k0 + 16 * np, lane);
+                    load_bt(bk, uK, 16 * jj, k0 + 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(U[x], zh[jj], bq[2 * x], bq[2 * x + 1]);
+                        mma_f16(U[2 + x], xh[jj], bk[2 * x], bk[2 * x + 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(U[x], zl[jj], bq[2 * x], bq[2 * x + 1]);
+                        mma_f16(U[2 + x], xl[jj], bk[2 * x], bk[2 * x + 1]);
+                    }
+                    if (!BF16) {
+                        load_bt(bq, uQ + KIMG, 16 * jj, k0 + 16 * np, lane);
+                        load_bt(bk, uK + KIMG, 16 * jj, k0 + 16 * np, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mma_f16(U[x], zh[jj], bq[2 * x], bq[2 * x + 1]);
+                            mma_f16(U[2 + x], xh[jj], bk[2 * x], bk[2 * x + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        S[2 * np + x][e] =
+                            fmaf(iA[e >> 1], U[x][e] + U[2 + x][e], gam * S[2 * np + x][e]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    if (a.dW0) {
+        float *w = a.dW0 + ((size_t)n * a.H + h) * state + mine;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+    }
+}
+
+// ---------------------------------------------------------------- per-chunk gradients
+
+struct GradArgs {
+    const float *dZ, *dV;          // [B][H][T][dv]; dV = dX
+    const float *eta;
+    const float *saveS, *saveX, *saveO;
+    float *dQ, *dK, *deta, *dg;    // dg NULL without a gate
+    const int *seq_start;
+    int B, Hk, H, T, N;
+    float q_scale;
+    Images im;
+};
+
+constexpr int kGradThreads = 256;
+
+// Shared memory: K and Q images; a region that first holds X and T, then W
+// and Om, then the three 64 x 64 images; rho; vectors and partial sums.
+template <int DK, int DV, bool BF16>
+struct GradSmem {
+    static constexpr int IMG = C * DK * 2 * (BF16 ? 1 : 2);
+    static constexpr int W = DK * DV * 2 * 2;          // W (or Om), two terms
+    static constexpr int R = C * DV * 2 * 2;           // rho (or X), two terms
+    static constexpr int big1 = 2 * W, big2 = R + 2 * kImg, big3 = 6 * kImg;
+    static constexpr int big = big1 > big2 ? (big1 > big3 ? big1 : big3) : (big2 > big3 ? big2 : big3);
+    static constexpr int oBig = 2 * IMG, oR = oBig + big, oF = oR + R;
+    // floats: Gh, Gl, eta, iR, iT (5 x 64), iS, iO (2 x 128), row maxima (2 x 64), 64
+    static constexpr int bytes = oF + 4 * (5 * C + 2 * 128 + 2 * C + 64);
+};
+
+// Row (c0 .. c0 + 7) units of an fp32 matrix row, scaled to two fp16 terms.
+__device__ __forceinline__ void put8(const float (&x)[8], float s, char *hi, char *lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split_f16(x[2 * j] * s, x[2 * j + 1] * s, h[j], l[j]);
+    *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ void get8(float (&x)[8], const float *p) {
+    const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+}
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+    return m;
+}
+__device__ __forceinline__ float2 h2f(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// A fragments of 16 rows (first row: p) of an fp32 matrix in global memory, rows
+// past `rows` zero, and the rows' scales.
+template <int KT>
+struct RowFrags {
+    float v[2 * KT][4];
+    float s[2], inv[2];
+    __device__ __forceinline__ void load(const float *p, int ld, int row0, int rows, int gq, int q4) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int row = row0 + gq + 8 * x;
+            const float *r = p + (size_t)row * ld + 2 * q4;
+#pragma unroll
+            for (int nt = 0; nt < 2 * KT; ++nt) {
+                float2 u = make_float2(0.f, 0.f);
+                if (row < rows) u = *reinterpret_cast<const float2 *>(r + 8 * nt);
+                v[nt][2 * x] = u.x;
+                v[nt][2 * x + 1] = u.y;
+            }
+        }
+        row_scales<2 * KT>(v, s, inv);
+    }
+};
+
+// One block per chunk and key head, its value heads one after the other; dQ and
+// dK of the chunk stay in registers and are added up over them. Warp (mt, hf)
+// holds the rows of tokens 16 mt .. 16 mt + 15 and half of the columns.
+template <int DK, int DV, bool BF16>
+__global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a) {
+    extern __shared__ __align__(1024) char gsm[];
+    using SM = GradSmem<DK, DV, BF16>;
+    constexpr int IMG = SM::IMG, KIMG = C * DK * 2;
+    constexpr int NK = DK / 16;  // 8-column tiles of half of DK
+    constexpr int NV = DV / 16;
+    constexpr int KV = DV / 16;  // 16-deep steps over DV
+    char *sK = gsm, *sQ = sK + IMG, *big = gsm + SM::oBig, *sR = gsm + SM::oR;
+    float *Gh = reinterpret_cast<float *>(gsm + SM::oF), *Gl = Gh + C, *eta = Gl + C, *iR = eta + C,
+          *iTs = iR + C, *iS = iTs + C, *iO = iS + 128, *rmax = iO + 128, *red = rmax + 2 * C;
+    // partial sums over the warps, in the place of rho once it is read
+    float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 2 * C, *colp = dotp + 2 * C,
+          *dG = colp + 4 * C, *kt = dG + C;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
+    const int mt = warp & 3, hf = warp >> 2;
+    const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
+    int n, t0, len;
+    if (!ChunkSearch{a.seq_start, a.T, a.N}.find(slot, n, t0, len)) return;
+    const int b = a.seq_start ? 0 : n;
+    const size_t kslot = (size_t)slot * a.Hk + hk;
+    for (int u = tid; u < IMG / 16; u += kGradThreads) {
+        reinterpret_cast<uint4 *>(sK)[u] = reinterpret_cast<const uint4 *>(a.im.K + kslot * IMG)[u];
+        reinterpret_cast<uint4 *>(sQ)[u] = reinterpret_cast<const uint4 *>(a.im.Q + kslot * IMG)[u];
+    }
+    const uint32_t uK = smem_u32(sK), uQ = smem_u32(sQ), uB = smem_u32(big), uR = smem_u32(sR);
+    float dQ[NK][4] = {}, dK[NK][4] = {};
+    const int rep = a.H / a.Hk;
+    const int row[2] = {16 * mt + gq, 16 * mt + gq + 8};
+    const int n0 = hf * (DK / 2);  // this warp's columns of DK
+
+    for (int r = 0; r < rep; ++r) {
+        const int h = hk * rep + r;
+        const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
+        const size_t hslot = (size_t)slot * a.H + h;
+        const float *vec = reinterpret_cast<const float *>(a.im.vec + hslot * kVecBytes);
+        __syncthreads();  // the head before is done with shared memory
+        if (tid < C) {
+            Gh[tid] = vec[kVgh * C + tid];
+            Gl[tid] = vec[kVgl * C + tid];
+            iTs[tid] = vec[kVit * C + tid];
+            eta[tid] = tid < len ? a.eta[hrow + tid] : 0.f;
+        }
+        // X under one scale, and T
+        {
+            constexpr int U = C * DV / 8 / kGradThreads;
+            const float *gx = a.saveX + hslot * C * DV;
+            float x[U][8], m = 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                get8(x[i], gx + (size_t)(tid + kGradThreads * i) * 8);
+                m = fmaxf(m, max8(x[i]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0) red[warp] = m;
+            for (int u = tid; u < 2 * kImg / 16; u += kGradThreads)
+                reinterpret_cast<uint4 *>(big + SM::R)[u] =
+                    reinterpret_cast<const uint4 *>(a.im.T + hslot * 2 * kImg)[u];
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+            float s, is;
+            pow2_scale(m, s, is);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = tid + kGradThreads * i, rw = u / (DV / 8), col = (u % (DV / 8)) * 8;
+                char *d = big + img_off(rw, col);
+                put8(x[i], s, d, d + C * DV * 2);
+            }
+            if (tid == 0) red[8] = is;
+        }
+        __syncthreads();
+        // rho = T X: 16 tokens, half of DV
+        {
+            float rho[NV][4] = {};
+            const uint32_t uT = uB + SM::R;
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                if (jj > mt) break;
+                uint32_t th[4], tl[4];
+                ldsm_x4(th, ldsm_addr(uT, 16 * mt, 16 * jj, lane));
+                ldsm_x4(tl, ldsm_addr(uT + kImg, 16 * mt, 16 * jj, lane));
+#pragma unroll
+                for (int np = 0; np < NV / 2; ++np) {
+                    uint32_t xh[4], xl[4];
+                    load_bt(xh, uB, 16 * jj, hf * (DV / 2) + 16 * np, lane);
+                    load_bt(xl, uB + C * DV * 2, 16 * jj, hf * (DV / 2) + 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(rho[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
+                        mma_f16(rho[2 * np + x], tl, xh[2 * x], xh[2 * x + 1]);
+                        mma_f16(rho[2 * np + x], th, xl[2 * x], xl[2 * x + 1]);
+                    }
+                }
+            }
+            float m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < NV; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    rho[nt][e] *= iTs[row[e >> 1]] * red[8];
+                    m[e >> 1] = fmaxf(m[e >> 1], fabsf(rho[nt][e]));
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                m[x] = quad_max(m[x]);
+                if (q4 == 0) rmax[hf * C + row[x]] = m[x];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float s, is;
+                pow2_scale(fmaxf(rmax[row[x]], rmax[C + row[x]]), s, is);
+                if (q4 == 0 && hf == 0) iR[row[x]] = is;
+#pragma unroll
+                for (int nt = 0; nt < NV; ++nt) {
+                    uint32_t hi, lo;
+                    split_f16(rho[nt][2 * x] * s, rho[nt][2 * x + 1] * s, hi, lo);
+                    const uint32_t o = img_off(row[x], hf * (DV / 2) + 8 * nt) + 4 * q4;
+                    *reinterpret_cast<uint32_t *>(sR + o) = hi;
+                    *reinterpret_cast<uint32_t *>(sR + C * DV * 2 + o) = lo;
+                }
+            }
+        }
+        // W and Om, row by row (rows of DK), and <W, Om>
+        float wo = 0.f;
+        {
+            constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
+            const float *gw = a.saveS + hslot * DK * DV, *go = a.saveO + hslot * DK * DV;
+#pragma unroll 2
+            for (int p = 0; p < DK / RPP; ++p) {
+                const int rw = p * RPP + tid / LPR, col = (tid % LPR) * 8;
+                float w[8], o[8];
+                get8(w, gw + (size_t)rw * DV + col);
+                get8(o, go + (size_t)rw * DV + col);
+                float mw = max8(w), mo = max8(o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wo = fmaf(w[j], o[j], wo);
+#pragma unroll
+                for (int x = 1; x < LPR; x <<= 1) {
+                    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, x));
+                    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, x));
+                }
+                float s, is;
+                // 64 rows of DK an image, its two terms behind one another
+                char *d = big + (rw >> 6) * (C * DV * 4) + img_off(rw & 63, col);
+                pow2_scale(mw, s, is);
+                put8(w, s, d, d + C * DV * 2);
+                if (tid % LPR == 0) iS[rw] = is;
+                pow2_scale(mo, s, is);
+                put8(o, s, d + SM::W, d + SM::W + C * DV * 2);
+                if (tid % LPR == 0) iO[rw] = is;
+            }
+            wo = warp_sum(wo);
+            if (lane == 0) red[16 + warp] = wo;
+        }
+        __syncthreads();
+
+        const float GC = Gh[C - 1], GCl = Gl[C - 1];
+        float dec[2], rest[2];  // exp(G_i), exp(G_C - G_i) of this thread's two rows
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            dec[x] = expf(Gh[row[x]] + Gl[row[x]]);
+            rest[x] = expf((GC - Gh[row[x]]) + (GCl - Gl[row[x]]));
+        }
+        const uint32_t uW = uB + (n0 >> 6) * (C * DV * 4), uO = uW + SM::W;
+        const int nrow = n0 & 63;
+        float phi[4][4] = {}, eps[4][4] = {};  // tokens 32 hf + ..
+        float dot[2] = {0.f, 0.f}, ktp[2] = {0.f, 0.f};
+        // dZ, then dX, against W and rho
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            RowFrags<KV> f;
+            f.load((pass ? a.dV : a.dZ) + hrow * DV, DV, 16 * mt, len, gq, q4);
+            float N[NK][4] = {};
+            float(&cc)[4][4] = pass ? eps : phi;
+#pragma unroll
+            for (int kk = 0; kk < KV; ++kk) {
+                uint32_t hi[4], lo[4];
+                a_terms(f.v[2 * kk], f.v[2 * kk + 1], f.s, hi, lo);
+#pragma unroll
+                for (int np = 0; np < NK / 2; ++np) {
+                    uint32_t wh[4], wl[4];
+                    load_b(wh, uW, nrow + 16 * np, 16 * kk, lane);
+                    load_b(wl, uW + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(N[2 * np + x], hi, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(N[2 * np + x], lo, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(N[2 * np + x], hi, wl[2 * x], wl[2 * x + 1]);
+                    }
+                }
+#pragma unroll
+                for (int np = 0; np < 2; ++np) {
+                    if (2 * hf + np > mt) continue;  // above the diagonal
+                    uint32_t rh[4], rl[4];
+                    load_b(rh, uR, 32 * hf + 16 * np, 16 * kk, lane);
+                    load_b(rl, uR + C * DV * 2, 32 * hf + 16 * np, 16 * kk, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(cc[2 * np + x], hi, rh[2 * x], rh[2 * x + 1]);
+                        mma_f16(cc[2 * np + x], lo, rh[2 * x], rh[2 * x + 1]);
+                        mma_f16(cc[2 * np + x], hi, rl[2 * x], rl[2 * x + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int col = n0 + 8 * nt + 2 * q4;
+                    const float w = (pass ? -dec[x] : a.q_scale * dec[x]) * f.inv[x];
+                    const float y0 = w * N[nt][2 * x] * iS[col], y1 = w * N[nt][2 * x + 1] * iS[col + 1];
+                    const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
+                    const char *im = pass ? sK : sQ;
+                    float2 kq = h2f(*reinterpret_cast<const uint32_t *>(im + o));
+                    if (!BF16) {
+                        const float2 l = h2f(*reinterpret_cast<const uint32_t *>(im + KIMG + o));
+                        kq.x += l.x, kq.y += l.y;
+                    }
+                    const float inv = vec[(pass ? kVik : kViq) * C + row[x]];
+                    dot[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), dot[x]);
+                    float *d = pass ? &dK[nt][2 * x] : &dQ[nt][2 * x];
+                    d[0] += y0, d[1] += y1;
+                }
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    cc[nt][e] *= f.inv[e >> 1] * iR[32 * hf + 8 * nt + 2 * q4 + (e & 1)];
+        }
+        // rho against Om
+        {
+            float N[NK][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < KV; ++kk) {
+                uint32_t hi[4], lo[4];
+                ldsm_x4(hi, ldsm_addr(uR, 16 * mt, 16 * kk, lane));
+                ldsm_x4(lo, ldsm_addr(uR + C * DV * 2, 16 * mt, 16 * kk, lane));
+#pragma unroll
+                for (int np = 0; np < NK / 2; ++np) {
+                    uint32_t wh[4], wl[4];
+                    load_b(wh, uO, nrow + 16 * np, 16 * kk, lane);
+                    load_b(wl, uO + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(N[2 * np + x], hi, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(N[2 * np + x], lo, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(N[2 * np + x], hi, wl[2 * x], wl[2 * x + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int col = n0 + 8 * nt + 2 * q4;
+                    const float w = rest[x] * iR[row[x]];
+                    const float y0 = w * N[nt][2 * x] * iO[col], y1 = w * N[nt][2 * x + 1] * iO[col + 1];
+                    const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
+                    float2 kq = h2f(*reinterpret_cast<const uint32_t *>(sK + o));
+                    if (!BF16) {
+                        const float2 l = h2f(*reinterpret_cast<const uint32_t *>(sK + KIMG + o));
+                        kq.x += l.x, kq.y += l.y;
+                    }
+                    const float inv = vec[kVik * C + row[x]];
+                    ktp[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), ktp[x]);
+                    dK[nt][2 * x] = fmaf(eta[row[x]], y0, dK[nt][2 * x]);
+                    dK[nt][2 * x + 1] = fmaf(eta[row[x]], y1, dK[nt][2 * x + 1]);
+                }
+        }
+        // the triangle: q_i.k_j and k_i.k_j of this warp's 16 x 32 block
+        float kk2[4][4] = {}, qk2[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < DK; k += 16) {
+            uint32_t ak[4], aq[4], akl[4], aql[4];
+            ldsm_x4(ak, ldsm_addr(uK, 16 * mt, k, lane));
+            ldsm_x4(aq, ldsm_addr(uQ, 16 * mt, k, lane));
+            if (!BF16) {
+                ldsm_x4(akl, ldsm_addr(uK + KIMG, 16 * mt, k, lane));
+                ldsm_x4(aql, ldsm_addr(uQ + KIMG, 16 * mt, k, lane));
+            }
+#pragma unroll
+            for (int np = 0; np < 2; ++np) {
+                if (2 * hf + np > mt) continue;
+                uint32_t bb[4];
+                load_b(bb, uK, 32 * hf + 16 * np, k, lane);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    mma_f16(kk2[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
+                    mma_f16(qk2[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
+                    if (!BF16) {
+                        mma_f16(kk2[2 * np + x], akl, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(qk2[2 * np + x], aql, bb[2 * x], bb[2 * x + 1]);
+                    }
+                }
+                if (!BF16) {
+                    load_b(bb, uK + KIMG, 32 * hf + 16 * np, k, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(kk2[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(qk2[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // rho, W and Om are read
+        float rs[2] = {0.f, 0.f}, mx[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            float cs[2] = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = row[e >> 1], j = 32 * hf + 8 * nt + 2 * q4 + (e & 1);
+                float p = 0.f, q = 0.f;
+                if (j <= i) {
+                    const float gam = expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j]));
+                    const float ikj = vec[kVik * C + j];
+                    p = a.q_scale * gam * phi[nt][e];
+                    if (j < i) q = -gam * eps[nt][e];
+                    const float w = ikj * (p * qk2[nt][e] * vec[kViq * C + i] +
+                                           q * kk2[nt][e] * vec[kVik * C + i]);
+                    cs[e & 1] += w;
+                    rs[e >> 1] = fmaf(eta[j], w, rs[e >> 1]);
+                    p *= eta[j];
+                    q *= eta[j];
+                    // as operands: the rows of K and Q they meet carry their scales
+                    mx[0] = fmaxf(mx[0], fabsf(p * ikj));
+                    mx[1] = fmaxf(mx[1], fabsf(p * vec[kViq * C + i]));
+                    mx[2] = fmaxf(mx[2], fabsf(q) * fmaxf(ikj, vec[kVik * C + i]));
+                }
+                phi[nt][e] = p;
+                eps[nt][e] = q;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
+                if (gq == 0) colp[mt * C + 32 * hf + 8 * nt + 2 * q4 + x] = cs[x];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float d = dot[x] + rs[x], k2 = ktp[x];
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+                k2 += __shfl_xor_sync(0xffffffffu, k2, o);
+            }
+            if (q4 == 0) rowp[hf * C + row[x]] = d, dotp[hf * C + row[x]] = k2;
+        }
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
+            if (lane == 0) red[32 + 8 * y + warp] = mx[y];
+        }
+        __syncthreads();  // sums and maxima are there
+        float sx[3], ix[3];
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) m = fmaxf(m, red[32 + 8 * y + w]);
+            pow2_scale(m, sx[y], ix[y]);
+        }
+        char *i1 = big, *i2 = big + 2 * kImg, *i3 = big + 4 * kImg;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            const int j0 = 32 * hf + 8 * nt + 2 * q4;
+            const float k0 = vec[kVik * C + j0], k1 = vec[kVik * C + j0 + 1];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = row[x];
+                const float qi = vec[kViq * C + i], ki = vec[kVik * C + i];
+                const float p0 = phi[nt][2 * x], p1 = phi[nt][2 * x + 1];
+                const float e0 = eps[nt][2 * x], e1 = eps[nt][2 * x + 1];
+                const uint32_t o = img_off(i, 32 * hf + 8 * nt) + 4 * q4;
+                uint32_t hi, lo;
+                split_f16(p0 * k0 * sx[0], p1 * k1 * sx[0], hi, lo);
+                *reinterpret_cast<uint32_t *>(i1 + o) = hi;
+                *reinterpret_cast<uint32_t *>(i1 + kImg + o) = lo;
+                split_f16(p0 * qi * sx[1], p1 * qi * sx[1], hi, lo);
+                *reinterpret_cast<uint32_t *>(i2 + o) = hi;
+                *reinterpret_cast<uint32_t *>(i2 + kImg + o) = lo;
+                // E + E^T: the element below the diagonal, and its mirror
+                uint32_t uh, ul;
+                split_f16(e0 * k0 * sx[2], e1 * k1 * sx[2], hi, lo);
+                split_f16(e0 * ki * sx[2], e1 * ki * sx[2], uh, ul);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = j0 + y;
+                    if (j > i) continue;
+                    const uint32_t ol = img_off(i, j & ~7) + 2 * (j & 7);
+                    *reinterpret_cast<uint16_t *>(i3 + ol) = (uint16_t)(hi >> (16 * y));
+                    *reinterpret_cast<uint16_t *>(i3 + kImg + ol) = (uint16_t)(lo >> (16 * y));
+                    if (j == i) continue;
+                    const uint32_t ou = img_off(j, i & ~7) + 2 * (i & 7);
+                    *reinterpret_cast<uint16_t *>(i3 + ou) = (uint16_t)(uh >> (16 * y));
+                    *reinterpret_cast<uint16_t *>(i3 + kImg + ou) = (uint16_t)(ul >> (16 * y));
+                }
+            }
+        }
+        if (tid < C) {
+            const float cs = (colp[tid] + colp[C + tid]) + (colp[2 * C + tid] + colp[3 * C + tid]);
+            const float k2 = dotp[tid] + dotp[C + tid];
+            if (tid < len) a.deta[hrow + tid] = cs + k2;
+            dG[tid] = (rowp[tid] + rowp[C + tid]) - eta[tid] * (cs + k2);
+            kt[tid] = eta[tid] * k2;
+        }
+        __syncthreads();
+        if (a.dg && tid < C && tid < len) {
+            // sums in double: the terms of later tokens cancel
+            double s = 0.0, w = 0.0;
+            for (int i = C - 1; i >= tid; --i) s += (double)dG[i];
+            for (int i = 0; i < C; ++i) w += (double)kt[i];
+            double d = 0.0;
+            for (int i = 0; i < 8; ++i) d += (double)red[16 + i];
+            a.dg[hrow + tid] = (float)(s + w + (double)expf(GC + GCl) * d);
+        }
+        // dQ += (phi eta) K, dK += (phi eta)^T Q + (E + E^T) K
+        const uint32_t u1 = smem_u32(i1), u2 = smem_u32(i2), u3 = smem_u32(i3);
+#pragma unroll
+        for (int np = 0; np < NK / 2; ++np) {
+            float q[2][4] = {}, k[2][4] = {}, e[2][4] = {};
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                uint32_t bk[4], bq[4], bkl[4], bql[4], ah[4], al[4];
+                load_bt(bk, uK, 16 * jj, n0 + 16 * np, lane);
+                load_bt(bq, uQ, 16 * jj, n0 + 16 * np, lane);
+                if (!BF16) {
+                    load_bt(bkl, uK + KIMG, 16 * jj, n0 + 16 * np, lane);
+                    load_bt(bql, uQ + KIMG, 16 * jj, n0 + 16 * np, lane);
+                }
+                auto add = [&](float(&acc)[2][4], const uint32_t(&bh)[4], const uint32_t(&bl)[4]) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(acc[x], ah, bh[2 * x], bh[2 * x + 1]);
+                        mma_f16(acc[x], al, bh[2 * x], bh[2 * x + 1]);
+                        if (!BF16) mma_f16(acc[x], ah, bl[2 * x], bl[2 * x + 1]);
+                    }
+                };
+                if (jj <= mt) {
+                    ldsm_x4(ah, ldsm_addr(u1, 16 * mt, 16 * jj, lane));
+                    ldsm_x4(al, ldsm_addr(u1 + kImg, 16 * mt, 16 * jj, lane));
+                    add(q, bk, bkl);
+                }
+                if (jj >= mt) {  // A = (phi eta)^T: read across
+                    const uint32_t o = img_off(16 * jj + (lane & 7) + ((lane >> 4) << 3),
+                                               16 * mt + ((lane >> 3) & 1) * 8);
+                    ldsm_x4_t(ah, u2 + o);
+                    ldsm_x4_t(al, u2 + kImg + o);
+                    add(k, bq, bql);
+                }
+                ldsm_x4(ah, ldsm_addr(u3, 16 * mt, 16 * jj, lane));
+                ldsm_x4(al, ldsm_addr(u3 + kImg, 16 * mt, 16 * jj, lane));
+                add(e, bk, bkl);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    dQ[2 * np + x][y] = fmaf(ix[0], q[x][y], dQ[2 * np + x][y]);
+                    dK[2 * np + x][y] += fmaf(ix[1], k[x][y], ix[2] * e[x][y]);
+                }
+        }
+    }
+    const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        if (row[x] < len)
+#pragma unroll
+            for (int nt = 0; nt < NK; ++nt) {
+                const size_t at = (krow + row[x]) * DK + n0 + 8 * nt + 2 * q4;
+                *reinterpret_cast<float2 *>(a.dQ + at) = make_float2(dQ[nt][2 * x], dQ[nt][2 * x + 1]);
+                *reinterpret_cast<float2 *>(a.dK + at) = make_float2(dK[nt][2 * x], dK[nt][2 * x + 1]);
+            }
+}
+
+// Sum over the sequences of a shared start weight's gradient, in order.
+__global__ void __launch_bounds__(256) delta_sum_kernel(const float *per_seq, float *out, int N,
+                                                        size_t n4) {
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    const float4 *p = reinterpret_cast<const float4 *>(per_seq) + i;
+    float4 s = p[0];
+    for (int k = 1; k < N; ++k) {
+        const float4 v = p[(size_t)k * n4];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    reinterpret_cast<float4 *>(out)[i] = s;
+}
+
+// Zero gradients for the tokens in front of the first packed sequence and behind the last.
+__global__ void __launch_bounds__(256) delta_outside_kernel(float *dQ, float *dK, float *dV,
+                                                            float *deta, float *dg,
+                                                            const int *seq_start, int N, int Hk,
+                                                            int H, int T, int dk, int dv) {
+    int first, last, len;
+    delta_span(seq_start, 0, T, first, len);
+    delta_span(seq_start, N - 1, T, last, len);
+    last += len;
+    if (last < first) last = first;
+    const int h = blockIdx.x, out = first + (T - last);
+    auto clear = [&](float *p, int d) {
+        for (size_t i = threadIdx.x; i < (size_t)out * d; i += 256) {
+            const int t = (int)(i / d);
+            p[((size_t)h * T + (t < first ? t : t - first + last)) * d + i % d] = 0.f;
+        }
+    };
+    clear(dV, dv);
+    clear(deta, 1);
+    if (dg) clear(dg, 1);
+    if (h < Hk) {
+        clear(dQ, dk);
+        clear(dK, dk);
+    }
+}
+
+struct BwdPlan {
+    Plan p;
+    size_t oS, oO, oX, oW, end;
+};
+BwdPlan bwd_plan(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed, bool bf16) {
+    BwdPlan q;
+    q.p = make_plan(B, Hk, H, T, dk, N, packed, bf16, true);
+    const size_t st = up256((size_t)q.p.slots * H * dk * dv * 4);
+    q.oS = q.p.end;
+    q.oO = q.oS + st;
+    q.oX = q.oO + st;
+    q.oW = q.oX + up256((size_t)q.p.slots * H * C * dv * 4);
+    q.end = q.oW + up256((size_t)N * H * dk * dv * 4);
+    return q;
+}
+
+template <int DK, bool BF16>
+cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
+    r.cgs = scan_groups((long long)N * r.H, r.dv);
+    constexpr int stage = rev_stage_bytes<DK, BF16>();
+    // two stages at least, so that the next chunk is loaded during this one
+    while (r.cgs > 1 && 2 * stage + 2 * r.cgs * kRevWarpBytes > 226 * 1024) r.cgs /= 2;
+    const int wbytes = 2 * r.cgs * kRevWarpBytes;
+    r.stages = (226 * 1024 - wbytes) / stage;
+    r.stages = r.stages > 3 ? 3 : r.stages;
+    const int smem = r.stages * stage + wbytes;
+    cudaError_t e = cudaFuncSetAttribute(delta_rev_kernel<DK, BF16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
+    delta_rev_kernel<DK, BF16><<<grid, 64 * r.cgs, smem, s>>>(r);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch(s);
+    return e;
+}
+
+template <int DK, int DV, bool BF16>
+cudaError_t grad_inst(const GradArgs &r, int blocks, cudaStream_t s) {
+    constexpr int smem = GradSmem<DK, DV, BF16>::bytes;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<DK, DV, BF16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    delta_grad_kernel<DK, DV, BF16><<<blocks, kGradThreads, smem, s>>>(r);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch(s);
+    return e;
+}
+template <int DK, int DV>
+cudaError_t grad_type(const GradArgs &r, bool bf16, int blocks, cudaStream_t s) {
+    return bf16 ? grad_inst<DK, DV, true>(r, blocks, s) : grad_inst<DK, DV, false>(r, blocks, s);
+}
+
+}  // namespace
+}  // namespace delta
+
+using namespace delta;
+
+size_t delta_bwd_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed,
+                                 bool bf16) {
+    return bwd_plan(B, Hk, H, T, dk, dv, N, packed, bf16).end;
+}
+
+cudaError_t launch_delta_bwd(const DeltaBwdArgs &g, cudaStream_t s) {
+    DeltaArgs a = g.f;
+    const BwdPlan q = bwd_plan(a.B, a.Hk, a.H, a.T, a.dk, a.dv, a.N, a.seq_start != nullptr, a.bf16);
+    char *ws = static_cast<char *>(a.workspace);
+    const Images im = images_at(q.p, ws, true);
+    float *saveS = reinterpret_cast<float *>(ws + q.oS), *saveO = reinterpret_cast<float *>(ws + q.oO),
+          *saveX = reinterpret_cast<float *>(ws + q.oX), *sums = reinterpret_cast<float *>(ws + q.oW);
+    a.Z = nullptr;
+    a.W_out = nullptr;
+    cudaError_t e = launch_prep(a, q.p, im, s);
+    if (e != cudaSuccess) return e;
+    e = launch_scan(a, im, kSave, saveS, saveX, s);
+    if (e != cudaSuccess) return e;
+    const bool sum = g.dW0 && !a.w0_per_seq;
+    const RevArgs r{g.dZ, g.dW_out, g.dV, sum ? sums : g.dW0, a.seq_start, a.B, a.Hk, a.H, a.T,
+                    a.dv, 0, 0, im, saveO, device_status_word()};
+    if (a.dk == 64) e = a.bf16 ? rev_inst<64, true>(r, a.N, s) : rev_inst<64, false>(r, a.N, s);
+    else e = a.bf16 ? rev_inst<128, true>(r, a.N, s) : rev_inst<128, false>(r, a.N, s);
+    if (e != cudaSuccess) return e;
+    const GradArgs d{g.dZ, g.dV, a.eta, saveS, saveX, saveO, g.dQ, g.dK, g.deta, g.dg, a.seq_start,
+                     a.B, a.Hk, a.H, a.T, a.N, a.q_scale, im};
+    const int blocks = q.p.slots * a.Hk;
+    if (a.dk == 64)
+        e = a.dv == 64 ? grad_type<64, 64>(d, a.bf16, blocks, s) : grad_type<64, 128>(d, a.bf16, blocks, s);
+    else
+        e = a.dv == 64 ? grad_type<128, 64>(d, a.bf16, blocks, s) : grad_type<128, 128>(d, a.bf16, blocks, s);
+    if (e != cudaSuccess) return e;
+    if (sum) {
+        const size_t n4 = (size_t)a.H * a.dk * a.dv / 4;
+        delta_sum_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(sums, g.dW0, a.N, n4);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        count_launch(s);
+    }
+    if (a.seq_start) {
+        delta_outside_kernel<<<a.H, 256, 0, s>>>(g.dQ, g.dK, g.dV, g.deta, g.dg, a.seq_start, a.N,
+                                                 a.Hk, a.H, a.T, a.dk, a.dv);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) count_launch(s);
+    }
+    return e;
+}
+
+}  // namespace ttt

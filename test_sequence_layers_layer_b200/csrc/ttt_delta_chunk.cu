@@ -33,36 +33,6 @@ struct PrepArgs {
     Images im;
 };
 
-// Sequence and chunk of a slot; false for a slot that no chunk uses.
-__device__ __forceinline__ bool find_chunk(const PrepArgs &a, int slot, int &n, int &t0, int &len) {
-    int c;
-    if (!a.seq_start) {
-        const int per = (a.T + C - 1) / C;
-        n = slot / per;
-        c = slot - n * per;
-        t0 = 0;
-        len = a.T;
-    } else {
-        // the last sequence whose first slot is not behind this one
-        int lo = 0, hi = a.N - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            int s, l;
-            delta_span(a.seq_start, mid, a.T, s, l);
-            if (s / C + mid <= slot) lo = mid;
-            else hi = mid - 1;
-        }
-        n = lo;
-        delta_span(a.seq_start, n, a.T, t0, len);
-        c = slot - (t0 / C + n);
-        if (c < 0) return false;
-    }
-    t0 += c * C;
-    len -= c * C;
-    len = len < C ? len : C;
-    return len > 0;
-}
-
 // One 64-row image of Q or K: rows in global memory to scaled fp16 terms, in
 // shared memory and in the workspace; inv[row] = 1 / scale.
 template <int DK, bool BF16>
@@ -204,7 +174,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
     char *sHl = reinterpret_cast<char *>(T);  // H's low terms; its high terms over Q
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
     int n, t0, len;
-    if (!find_chunk(a, slot, n, t0, len)) return;
+    if (!ChunkSearch{a.seq_start, a.T, a.N}.find(slot, n, t0, len)) return;
     const int b = a.seq_start ? 0 : n;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const size_t kslot = (size_t)slot * a.Hk + hk;

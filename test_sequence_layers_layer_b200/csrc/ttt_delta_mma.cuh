@@ -175,6 +175,41 @@ __device__ __forceinline__ int first_slot(const int *seq_start, int n, int T, in
     return seq_start ? t0 / C + n : n * ((T + C - 1) / C);
 }
 
+// Sequence of a slot, and its chunk's first token (inside the batch row) and
+// length; false for a slot that no chunk uses.
+struct ChunkSearch {
+    const int *seq_start;
+    int T, N;
+    __device__ __forceinline__ bool find(int slot, int &n, int &t0, int &len) const {
+        int c;
+        if (!seq_start) {
+            const int per = (T + C - 1) / C;
+            n = slot / per;
+            c = slot - n * per;
+            t0 = 0;
+            len = T;
+        } else {
+            // the last sequence whose first slot is not behind this one
+            int lo = 0, hi = N - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                int s, l;
+                delta_span(seq_start, mid, T, s, l);
+                if (s / C + mid <= slot) lo = mid;
+                else hi = mid - 1;
+            }
+            n = lo;
+            delta_span(seq_start, n, T, t0, len);
+            c = slot - (t0 / C + n);
+            if (c < 0) return false;
+        }
+        t0 += c * C;
+        len -= c * C;
+        len = len < C ? len : C;
+        return len > 0;
+    }
+};
+
 // The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
 Images images_at(const Plan &p, void *workspace, bool bwd);
