@@ -36,31 +36,32 @@ struct RevArgs {
     int *status;
 };
 
-constexpr int kZTile = C * 20 * 4;  // 64 tokens x 16 columns, rows of 80 bytes
-constexpr int kRevWarpBytes = kZTile + 4096;
-
 template <int DK, bool BF16>
 constexpr int rev_stage_bytes() {
     return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 + 2 * kImg + kScanVecBytes;
 }
+// A column group's area: shares of dX [to][from][2 tiles], terms of dX [4 blocks][hi, lo],
+// of dZ [4 blocks][for M: hi, lo, for Q: hi, lo], 1 / their scales.
+constexpr int kRevGroupBytes = 16 * 1024 + 4096 + 8192 + 1024;
 
-// The mirror of the forward scan: two warps own 16 columns of Om, as rows of
-// Om^T in registers, half of DK each. dX^T = Om^T H^T + dZ^T M is summed over
-// both halves of DK, and over the two halves of the tokens for dZ^T M (blocks 0, 3
-// and 1, 2: the same share of the triangle), in one exchange.
+// The mirror of the forward scan: four warps own 16 columns of Om, as the rows of
+// Om^T in registers, a quarter of DK each. Before the first meeting each hands
+// out its quarter's share of Om^T H^T, and the operand forms of dZ of its block of
+// 16 tokens; then warp p puts dX of block p together (with dZ^T M over the blocks from
+// p on), and after the second meeting each updates its quarter of Om.
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
+__global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_rev_kernel(RevArgs a) {
     extern __shared__ __align__(1024) char ssm[];
     __shared__ uint64_t full[4], empty[4];
     __shared__ int abort_flag;
     constexpr int STAGE = rev_stage_bytes<DK, BF16>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
-    constexpr int NT = DK / 16;
+    constexpr int NT = DK / 32, KK = DK / 64;
     constexpr int oH = 2 * KALL, oM = oH + 2 * KIMG;
     const int groups = a.dv / (16 * a.cgs);
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp & 1;
+    const int tid = threadIdx.x, lane = tid & 31, cg = tid >> 7, p = (tid >> 5) & 3;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
         abort_flag = 0;
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2 * a.cgs);
+            mbar_init(&empty[s], 4 * a.cgs);
         }
         fence_mbar_init();
     }
@@ -97,25 +98,26 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
         for (int i = 0; i < nchunk && i < a.stages - 1; ++i) fill(i);
 
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = (grp * a.cgs + (warp >> 1)) * 16;
+    const int v0 = (grp * a.cgs + cg) * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *own = ssm + a.stages * STAGE + warp * kRevWarpBytes;
-    float *zt = reinterpret_cast<float *>(own);
-    float4 *give = reinterpret_cast<float4 *>(own + kZTile) + lane;
-    const float4 *take = reinterpret_cast<const float4 *>(
-                             ssm + a.stages * STAGE + (warp ^ 1) * kRevWarpBytes + kZTile) + lane;
-    uint4 zr[8];
+    char *area = ssm + a.stages * STAGE + cg * kRevGroupBytes;
+    float4 *part = reinterpret_cast<float4 *>(area) + lane;                // [to][from][tile][32]
+    uint4 *xfr = reinterpret_cast<uint4 *>(area + 16 * 1024) + lane;       // [block][hi, lo][32]
+    uint4 *zfr = reinterpret_cast<uint4 *>(area + 20 * 1024) + lane;       // [block][M hi, lo, Q hi, lo][32]
+    float *iXs = reinterpret_cast<float *>(area + 28 * 1024), *iZm = iXs + 64, *iZq = iZm + 64;
+
+    // dZ of this lane's places in block p
+    float z[2][4];
     auto fetch_z = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int u = lane + 32 * i, row = u >> 2, part = u & 3;
-            zr[i] = make_uint4(0, 0, 0, 0);
-            if (c * C + row < len)
-                zr[i] = *reinterpret_cast<const uint4 *>(a.dZ + (vrow + c * C + row) * a.dv + v0 +
-                                                         4 * part);
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = c * C + 16 * p + 8 * x + 2 * q4 + (e & 1);
+                z[x][e] = t < len ? a.dZ[(vrow + t) * a.dv + v0 + gq + (e >> 1) * 8] : 0.f;
+            }
     };
-    const int k0 = half * (DK / 2);
+    const int k0 = p * (DK / 4);
     float S[NT][4];
     const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
     const float *w0 = a.dW_out ? a.dW_out + ((size_t)n * a.H + h) * state + mine : nullptr;
@@ -132,37 +134,18 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
         const bool ok = mbar_wait_warp(&full[s], (i / a.stages) & 1, abort, a.status, kScanStatus);
         const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
         const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
-        // both warps are past reading what the other gave for the chunk before;
-        // and leave together when a wait has run out
-        if (named_bar_or(1 + (warp >> 1), 64, !ok)) {
-            if (tid == 0)
-                for (int p = i; p < i + a.stages && p < nchunk; ++p)
-                    mbar_drain(&full[p % a.stages], (p / a.stages) & 1);
-            return;
-        }
-        {
+        if (ok) {
             float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int u = lane + 32 * j;
-            *reinterpret_cast<uint4 *>(zt + (u >> 2) * 20 + (u & 3) * 4) = zr[j];
-        }
-        __syncwarp();
-        if (i + 1 < nchunk) fetch_z(c - 1);
-
-        // dX^T = Om^T H^T over this warp's half of DK
-        float X[8][4] = {};
-        {
-            float sS[2], iS[2];
+            // Om^T H^T over this warp's quarter of DK
+            float X[8][4] = {}, sS[2], iS[2];
             row_scales<NT>(S, sS, iS);
 #pragma unroll
-            for (int kk = 0; kk < NT / 2; ++kk) {
+            for (int kk = 0; kk < KK; ++kk) {
                 uint32_t hi[4], lo[4], bb[4][4];
                 a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
 #pragma unroll
@@ -180,125 +163,132 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(RevArgs a) {
                 for (int nt = 0; nt < 8; ++nt)
                     mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
             }
-            const float iH = vec[kVs * C + 1];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) X[nt][e] *= iS[e >> 1] * iH;
-        }
-        // + dZ^T M over this warp's tokens
-        {
-            float A[4][4], D[8][4] = {}, sA[2], iA[2];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int nt = 2 * ((y >> 1) ? (half ? 2 : 3) : (half ? 1 : 0)) + (y & 1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * nt + 2 * q4 + (e & 1);
-                    A[y][e] = zt[t * 20 + gq + (e >> 1) * 8] * vec[kVm * C + t];
-                }
-            }
-            row_scales<4>(A, sA, iA);
+                part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
+                    iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
+            // dZ of block p as an operand for M (M's row scales in it) and for c D Q
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
+                float A[2][4], sA[2], iA[2];
                 uint32_t hi[4], lo[4];
-                a_terms(A[2 * y], A[2 * y + 1], sA, hi, lo);
-                const int ii = y ? (half ? 2 : 3) : (half ? 1 : 0);
 #pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    if (np > ii) continue;  // M_ij is zero for i < j; the same for the whole warp
-                    uint32_t bh[4], bl[4];
-                    load_bt(bh, uM, 16 * ii, 16 * np, lane);
-                    load_bt(bl, uM + kImg, 16 * ii, 16 * np, lane);
+                for (int x = 0; x < 2; ++x) {
+                    const float2 f = *reinterpret_cast<const float2 *>(
+                        vec + (y ? kVq : kVm) * C + 16 * p + 8 * x + 2 * q4);
+                    A[x][0] = z[x][0] * f.x, A[x][1] = z[x][1] * f.y;
+                    A[x][2] = z[x][2] * f.x, A[x][3] = z[x][3] * f.y;
+                }
+                row_scales<2>(A, sA, iA);
+                a_terms(A[0], A[1], sA, hi, lo);
+                zfr[32 * (4 * p + 2 * y)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                zfr[32 * (4 * p + 2 * y + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                float *q = y ? iZq : iZm;
+                if (q4 == 0) q[16 * p + gq] = iA[0], q[16 * p + gq + 8] = iA[1];
+            }
+        }
+        // the first meeting; all leave together when a wait has run out
+        if (named_bar_or(1 + cg, 128, !ok)) {
+            if (tid == 0)
+                for (int j = i; j < i + a.stages && j < nchunk; ++j)
+                    mbar_drain(&full[j % a.stages], (j / a.stages) & 1);
+            return;
+        }
+        if (i + 1 < nchunk) fetch_z(c - 1);
+        // dX of block p
+        {
+            float X[2][4];
+            const float iH = vec[kVs * C + 1 + p];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(D[2 * np + x], hi, bh[2 * x], bh[2 * x + 1]);
-                        mma_f16(D[2 * np + x], lo, bh[2 * x], bh[2 * x + 1]);
-                        mma_f16(D[2 * np + x], hi, bl[2 * x], bl[2 * x + 1]);
-                    }
+            for (int x = 0; x < 2; ++x) {
+                float4 o = part[32 * (8 * p + x)];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) {
+                    const float4 u = part[32 * (8 * p + 2 * w + x)];
+                    o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
+                }
+                X[x][0] = iH * o.x, X[x][1] = iH * o.y, X[x][2] = iH * o.z, X[x][3] = iH * o.w;
+            }
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) {
+                if (ii < p) continue;  // M_ij is zero for i < j; the same for the whole warp
+                const uint4 fh = zfr[32 * (4 * ii)], fl = zfr[32 * (4 * ii + 1)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float i0 = iZm[16 * ii + gq], i1 = iZm[16 * ii + gq + 8];
+                float d[2][4] = {};
+                uint32_t bh[4], bl[4];
+                load_bt(bh, uM, 16 * ii, 16 * p, lane);
+                load_bt(bl, uM + kImg, 16 * ii, 16 * p, lane);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    mma_f16(d[x], hi, bh[2 * x], bh[2 * x + 1]);
+                    mma_f16(d[x], lo, bh[2 * x], bh[2 * x + 1]);
+                    mma_f16(d[x], hi, bl[2 * x], bl[2 * x + 1]);
+                    X[x][0] = fmaf(i0, d[x][0], X[x][0]);
+                    X[x][1] = fmaf(i0, d[x][1], X[x][1]);
+                    X[x][2] = fmaf(i1, d[x][2], X[x][2]);
+                    X[x][3] = fmaf(i1, d[x][3], X[x][3]);
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) X[nt][e] = fmaf(iA[e >> 1], D[nt][e], X[nt][e]);
+            for (int x = 0; x < 2; ++x) {
+                const int t = c * C + 16 * p + 8 * x + 2 * q4;
+                float *w = a.dV + (vrow + t) * a.dv + v0 + gq;
+                if (t < len) w[0] = X[x][0], w[8] = X[x][2];
+                if (t + 1 < len) w[a.dv] = X[x][1], w[a.dv + 8] = X[x][3];
+                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
+                X[x][0] *= -ck.x, X[x][1] *= -ck.y, X[x][2] *= -ck.x, X[x][3] *= -ck.y;
+            }
+            float sX[2], iX[2];
+            uint32_t hi[4], lo[4];
+            row_scales<2>(X, sX, iX);
+            a_terms(X[0], X[1], sX, hi, lo);
+            xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
         }
+        // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K); dZ's part before the meeting
+        const float gam = vec[kVs * C];
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) give[32 * nt] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
-        named_bar(1 + (warp >> 1), 64);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            const float4 o = take[32 * nt];
-            X[nt][0] += o.x, X[nt][1] += o.y, X[nt][2] += o.z, X[nt][3] += o.w;
-        }
-        // dV of half of the tokens
+            for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int t = c * C + 8 * (4 * half + y) + 2 * q4;
-            float x[4];  // chosen by value: a pointer into X would send it to memory
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = half ? X[4 + y][e] : X[y][e];
-            float *w = a.dV + (vrow + t) * a.dv + v0 + gq;
-            if (t < len) w[0] = x[0], w[8] = x[2];
-            if (t + 1 < len) w[a.dv] = x[1], w[a.dv + 8] = x[3];
-        }
-
-        // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K), both under one scale
-        {
-            float Zq[8][4], sA[2], iA[2];
-            float m[2] = {0.f, 0.f};
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * nt + 2 * q4 + (e & 1);
-                    Zq[nt][e] = zt[t * 20 + gq + (e >> 1) * 8] * vec[kVq * C + t];
-                    X[nt][e] *= -vec[kVk * C + t];
-                    m[e >> 1] = fmaxf(m[e >> 1], fmaxf(fabsf(Zq[nt][e]), fabsf(X[nt][e])));
-                }
-            pow2_scale(quad_max(m[0]), sA[0], iA[0]);
-            pow2_scale(quad_max(m[1]), sA[1], iA[1]);
-            uint32_t zh[4][4], zl[4][4], xh[4][4], xl[4][4];
+        for (int y = 0; y < 2; ++y) {
+            if (y == 1) named_bar(1 + cg, 128);  // the second meeting
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                a_terms(Zq[2 * jj], Zq[2 * jj + 1], sA, zh[jj], zl[jj]);
-                a_terms(X[2 * jj], X[2 * jj + 1], sA, xh[jj], xl[jj]);
-            }
-            const float gam = vec[kVs * C];
+                const uint4 fh = y ? xfr[32 * (2 * jj)] : zfr[32 * (4 * jj + 2)];
+                const uint4 fl = y ? xfr[32 * (2 * jj + 1)] : zfr[32 * (4 * jj + 3)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float *q = y ? iXs : iZq;
+                const float i0 = q[16 * jj + gq], i1 = q[16 * jj + gq + 8];
+                const uint32_t img = y ? uK : uQ;
+                float U[NT][4] = {};
+                uint32_t bb[KK][4];
 #pragma unroll
-            for (int np = 0; np < NT / 2; ++np) {
-                float U[4][4] = {};  // dZ^T Q in 0, 1 and dX^T K in 2, 3
+                for (int np = 0; np < KK; ++np) load_bt(bb[np], img, 16 * jj, k0 + 16 * np, lane);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bq[4], bk[4];
-                    load_bt(bq, uQ, 16 * jj, k0 + 16 * np, lane);
-                    load_bt(bk, uK, 16 * jj, k0 + 16 * np, lane);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(U[x], zh[jj], bq[2 * x], bq[2 * x + 1]);
-                        mma_f16(U[2 + x], xh[jj], bk[2 * x], bk[2 * x + 1]);
-                    }
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+                if (!BF16) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(U[x], zl[jj], bq[2 * x], bq[2 * x + 1]);
-                        mma_f16(U[2 + x], xl[jj], bk[2 * x], bk[2 * x + 1]);
-                    }
-                    if (!BF16) {
-                        load_bt(bq, uQ + KIMG, 16 * jj, k0 + 16 * np, lane);
-                        load_bt(bk, uK + KIMG, 16 * jj, k0 + 16 * np, lane);
+                    for (int np = 0; np < KK; ++np)
+                        load_bt(bb[np], img + KIMG, 16 * jj, k0 + 16 * np, lane);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            mma_f16(U[x], zh[jj], bq[2 * x], bq[2 * x + 1]);
-                            mma_f16(U[2 + x], xh[jj], bk[2 * x], bk[2 * x + 1]);
-                        }
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(U[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[2 * np + x][e] =
-                            fmaf(iA[e >> 1], U[x][e] + U[2 + x][e], gam * S[2 * np + x][e]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    S[nt][0] = fmaf(i0, U[nt][0], S[nt][0]);
+                    S[nt][1] = fmaf(i0, U[nt][1], S[nt][1]);
+                    S[nt][2] = fmaf(i1, U[nt][2], S[nt][2]);
+                    S[nt][3] = fmaf(i1, U[nt][3], S[nt][3]);
+                }
             }
         }
         __syncwarp();
@@ -931,11 +921,11 @@ BwdPlan bwd_plan(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed
 
 template <int DK, bool BF16>
 cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
-    r.cgs = scan_groups((long long)N * r.H, r.dv);
+    r.cgs = scan_groups((long long)N * r.H, DK, r.dv);
     constexpr int stage = rev_stage_bytes<DK, BF16>();
-    // two stages at least, so that the next chunk is loaded during this one
-    while (r.cgs > 1 && 2 * stage + 2 * r.cgs * kRevWarpBytes > 226 * 1024) r.cgs /= 2;
-    const int wbytes = 2 * r.cgs * kRevWarpBytes;
+    // two stages if that can be, so that the next chunk is loaded during this one
+    while (r.cgs > 1 && 2 * stage + r.cgs * kRevGroupBytes > 226 * 1024) r.cgs /= 2;
+    const int wbytes = r.cgs * kRevGroupBytes;
     r.stages = (226 * 1024 - wbytes) / stage;
     r.stages = r.stages > 3 ? 3 : r.stages;
     const int smem = r.stages * stage + wbytes;
@@ -943,7 +933,7 @@ cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
-    delta_rev_kernel<DK, BF16><<<grid, 64 * r.cgs, smem, s>>>(r);
+    delta_rev_kernel<DK, BF16><<<grid, 128 * r.cgs, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;

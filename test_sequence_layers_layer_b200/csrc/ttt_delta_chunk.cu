@@ -22,7 +22,7 @@ namespace {
 
 // ---------------------------------------------------------------- preparation
 
-constexpr int kPrepThreads = 128;
+constexpr int kPrepThreads = 256;
 
 struct PrepArgs {
     const void *Q, *K;
@@ -33,36 +33,39 @@ struct PrepArgs {
     Images im;
 };
 
-// One 64-row image of Q or K: rows in global memory to scaled fp16 terms, in
-// shared memory and in the workspace; inv[row] = 1 / scale.
+// A 64-row image of Q or K by 128 threads: rows in global memory to scaled fp16
+// terms, in shared memory and in the workspace; inv[row] = 1 / scale. All loads
+// are on their way before the first is used.
 template <int DK, bool BF16>
 __device__ __forceinline__ void convert_rows(const void *src, size_t row0, int len, char *sm,
-                                             char *gm, float *inv) {
-    constexpr int LPR = DK / 8, RPP = kPrepThreads / LPR;  // lanes per row, rows per pass
-    const int sub = threadIdx.x % LPR;
+                                             char *gm, float *inv, int tid) {
+    constexpr int LPR = DK / 8, RPP = 128 / LPR, NP = C / RPP;  // lanes per row, rows per pass
+    const int sub = tid % LPR;
+    uint4 raw[NP][BF16 ? 1 : 2];
 #pragma unroll
-    for (int p = 0; p < C / RPP; ++p) {
-        const int row = p * RPP + threadIdx.x / LPR;
-        float x[8] = {};
-        if (row < len) {
-            const size_t at = (row0 + row) * DK + sub * 8;
-            if (BF16) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(src) + at);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int p = 0; p < NP; ++p) {
+        const int row = p * RPP + tid / LPR;
+        const size_t at = (row0 + row) * DK + sub * 8;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(w[j] << 16);
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-                }
-            } else {
-                const float4 *f =
-                    reinterpret_cast<const float4 *>(static_cast<const float *>(src) + at);
-                const float4 u = f[0], v = f[1];
-                x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-                x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-            }
+        for (int y = 0; y < (BF16 ? 1 : 2); ++y) {
+            raw[p][y] = make_uint4(0, 0, 0, 0);
+            if (row < len)
+                raw[p][y] = BF16 ? *reinterpret_cast<const uint4 *>(
+                                       static_cast<const __nv_bfloat16 *>(src) + at)
+                                 : *reinterpret_cast<const uint4 *>(
+                                       static_cast<const float *>(src) + at + 4 * y);
         }
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int row = p * RPP + tid / LPR;
+        float x[8];
+        const uint32_t w[8] = {raw[p][0].x, raw[p][0].y, raw[p][0].z, raw[p][0].w,
+                               raw[p][BF16 ? 0 : 1].x, raw[p][BF16 ? 0 : 1].y,
+                               raw[p][BF16 ? 0 : 1].z, raw[p][BF16 ? 0 : 1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = __uint_as_float(!BF16 ? w[j] : (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
@@ -93,7 +96,7 @@ constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices (floats)
 // terms over Q, its low terms over T).
 template <int DK, bool BF16>
 constexpr int prep_smem() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * (5 * C + 8) + 4 * 3 * 16 * 18;
+    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * 5 * C + 4 * 3 * 16 * 18;
 }
 
 // T = (I + L)^-1 for L strictly lower triangular, by 16 x 16 blocks in fp32: the four
@@ -103,28 +106,34 @@ constexpr int prep_smem() {
 // Leaves the upper blocks of T as they are. Barriers inside; Y: 3 x 16 x 18 floats.
 __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (lane < 16) {
+    if (warp < 4 && lane < 16) {
         const float *l = L + 16 * warp * kLd + 16 * warp;
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
 #pragma unroll
-        for (int k = 0; k < 15; ++k)
+        for (int i = 1; i < 16; ++i)  // row i of L as vectors: the same for all lanes
 #pragma unroll
-            for (int i = k + 1; i < 16; ++i) x[i] = fmaf(-l[i * kLd + k], x[k], x[i]);
+            for (int k4 = 0; k4 < i; k4 += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(l + i * kLd + k4);
+                x[i] = fmaf(-v.x, x[k4], x[i]);
+                if (k4 + 1 < i) x[i] = fmaf(-v.y, x[k4 + 1], x[i]);
+                if (k4 + 2 < i) x[i] = fmaf(-v.z, x[k4 + 2], x[i]);
+                if (k4 + 3 < i) x[i] = fmaf(-v.w, x[k4 + 3], x[i]);
+            }
 #pragma unroll
         for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kLd + 16 * warp + lane] = x[i];
     }
     __syncthreads();
-    const int r = tid >> 3, c = (tid & 7) * 2;  // every thread two outputs of each block
+    // half of the threads a block, two outputs each
+    const int side = tid >> 7, r = (tid & 127) >> 3, c = (tid & 7) * 2;
 #pragma unroll
     for (int dist = 1; dist < 4; ++dist) {
-#pragma unroll
-        for (int b = 0; b < 4 - dist; ++b) {
+        for (int b = side; b < 4 - dist; b += 2) {
             float y0 = 0.f, y1 = 0.f;
             const float *l = L + (16 * (b + dist) + r) * kLd + 16 * b;
             const float *t = T + 16 * b * kLd + 16 * b + c;
-#pragma unroll 4
+#pragma unroll
             for (int k = 0; k < 16 * dist; k += 4) {
                 const float4 l4 = *reinterpret_cast<const float4 *>(l + k);
                 const float lk[4] = {l4.x, l4.y, l4.z, l4.w};
@@ -138,8 +147,7 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
             *reinterpret_cast<float2 *>(Y + (b * 16 + r) * 18 + c) = make_float2(y0, y1);
         }
         __syncthreads();
-#pragma unroll
-        for (int b = 0; b < 4 - dist; ++b) {
+        for (int b = side; b < 4 - dist; b += 2) {
             float y0 = 0.f, y1 = 0.f;
             const float *t = T + (16 * (b + dist) + r) * kLd + 16 * (b + dist);
 #pragma unroll
@@ -160,16 +168,17 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
     }
 }
 
-// One block per chunk and key head, its value heads one after the other.
+// One block per chunk and key head, its value heads one after the other. Warps
+// 0..3 work for Z (q_i.k_j, P, M), warps 4..7 for the weight (k_i.k_j, A, H), 16 rows
+// each; the inverse between them takes all.
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a) {
     extern __shared__ __align__(1024) char psm[];
-    constexpr int IMG = C * DK * 2 * (BF16 ? 1 : 2);
+    constexpr int KIMG = C * DK * 2, IMG = KIMG * (BF16 ? 1 : 2);
     char *sK = psm, *sQ = sK + IMG;
     float *L = reinterpret_cast<float *>(sQ + IMG);  // A of the chunk, row-major
     float *T = L + C * kLd;
-    float *iK = T + C * kLd, *iQ = iK + C, *Gh = iQ + C, *Gl = Gh + C, *eta = Gl + C;
-    float *red = eta + C, *Y = red + 8;
+    float *iK = T + C * kLd, *iQ = iK + C, *Gh = iQ + C, *Gl = Gh + C, *eta = Gl + C, *Y = eta + C;
     char *sT = reinterpret_cast<char *>(L);   // T's two terms, then M's
     char *sHl = reinterpret_cast<char *>(T);  // H's low terms; its high terms over Q
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -177,45 +186,36 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
     if (!ChunkSearch{a.seq_start, a.T, a.N}.find(slot, n, t0, len)) return;
     const int b = a.seq_start ? 0 : n;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
+    const int mt = warp & 3;
+    const bool forw = warp >= 4;  // works for the weight
     const size_t kslot = (size_t)slot * a.Hk + hk;
     const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;
-    convert_rows<DK, BF16>(a.K, krow, len, sK, a.im.K + kslot * a.im.kimg, iK);
-    convert_rows<DK, BF16>(a.Q, krow, len, sQ, a.im.Q + kslot * a.im.kimg, iQ);
+    if (forw) convert_rows<DK, BF16>(a.K, krow, len, sK, a.im.K + kslot * a.im.kimg, iK, tid & 127);
+    else convert_rows<DK, BF16>(a.Q, krow, len, sQ, a.im.Q + kslot * a.im.kimg, iQ, tid);
     __syncthreads();
 
-    // k_i.k_j and q_i.k_j of this warp's 16 rows i, columns j up to the diagonal
-    float kk[8][4] = {}, qk[8][4] = {};
-    const uint32_t uK = smem_u32(sK), uQ = smem_u32(sQ);
+    // k_i.k_j or q_i.k_j of this warp's 16 rows i, columns j up to the diagonal
+    float kk[8][4] = {};
+    const uint32_t uK = smem_u32(sK), uA = forw ? uK : smem_u32(sQ);
 #pragma unroll
     for (int k = 0; k < DK; k += 16) {
-        uint32_t ak[4], aq[4], akl[4], aql[4];
-        ldsm_x4(ak, ldsm_addr(uK, 16 * warp, k, lane));
-        ldsm_x4(aq, ldsm_addr(uQ, 16 * warp, k, lane));
-        if (!BF16) {
-            ldsm_x4(akl, ldsm_addr(uK + C * DK * 2, 16 * warp, k, lane));
-            ldsm_x4(aql, ldsm_addr(uQ + C * DK * 2, 16 * warp, k, lane));
-        }
+        uint32_t ah[4], al[4];
+        ldsm_x4(ah, ldsm_addr(uA, 16 * mt, k, lane));
+        if (!BF16) ldsm_x4(al, ldsm_addr(uA + KIMG, 16 * mt, k, lane));
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
-            if (np > warp) break;
+            if (np > mt) break;
             uint32_t bb[4];
             load_b(bb, uK, 16 * np, k, lane);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                mma_f16(kk[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
-                mma_f16(qk[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
-                if (!BF16) {
-                    mma_f16(kk[2 * np + x], akl, bb[2 * x], bb[2 * x + 1]);
-                    mma_f16(qk[2 * np + x], aql, bb[2 * x], bb[2 * x + 1]);
-                }
+                mma_f16(kk[2 * np + x], ah, bb[2 * x], bb[2 * x + 1]);
+                if (!BF16) mma_f16(kk[2 * np + x], al, bb[2 * x], bb[2 * x + 1]);
             }
             if (!BF16) {
-                load_b(bb, uK + C * DK * 2, 16 * np, k, lane);
+                load_b(bb, uK + KIMG, 16 * np, k, lane);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mma_f16(kk[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
-                    mma_f16(qk[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
-                }
+                for (int x = 0; x < 2; ++x) mma_f16(kk[2 * np + x], ah, bb[2 * x], bb[2 * x + 1]);
             }
         }
     }
@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         const size_t hslot = (size_t)slot * a.H + h;
         float *vec = reinterpret_cast<float *>(a.im.vec + hslot * kVecBytes);
         if (r > 0 && tid == 0) bulk_wait_read<0>();  // the head before has gone out
-        __syncthreads();
         if (warp == 0) {
             // sums of decays in double, handed on as two floats: differences of
             // sums stay exact to the last bit of the decays. A decay below -200
@@ -264,25 +263,28 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         }
         __syncthreads();
 
-        // A and P from the products
+        // A (to shared memory) or P (kept) from the products
         float P[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            float av[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) P[nt][e] = 0.f;
+            if (nt >= 2 * mt + 2) continue;  // above the diagonal
+            const int j0 = 8 * nt + 2 * q4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 16 * warp + gq + (e >> 1) * 8, j = 8 * nt + 2 * q4 + (e & 1);
-                av[e] = 0.f;
-                P[nt][e] = 0.f;
-                if (j <= i) {
+                const int i = 16 * mt + gq + (e >> 1) * 8, j = j0 + (e & 1);
+                if (forw ? j < i : j <= i) {
                     const float gam = expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j])) * eta[j] * iK[j];
-                    P[nt][e] = a.q_scale * gam * (qk[nt][e] * iQ[i]);
-                    if (j < i) av[e] = gam * (kk[nt][e] * iK[i]);
+                    P[nt][e] = gam * (kk[nt][e] * (forw ? iK[i] : iQ[i]));
+                    if (!forw) P[nt][e] *= a.q_scale;
                 }
             }
-            float *l = L + (16 * warp + gq) * kLd + 8 * nt + 2 * q4;
-            *reinterpret_cast<float2 *>(l) = make_float2(av[0], av[1]);
-            *reinterpret_cast<float2 *>(l + 8 * kLd) = make_float2(av[2], av[3]);
+            if (forw) {
+                float *l = L + (16 * mt + gq) * kLd + j0;
+                *reinterpret_cast<float2 *>(l) = make_float2(P[nt][0], P[nt][1]);
+                *reinterpret_cast<float2 *>(l + 8 * kLd) = make_float2(P[nt][2], P[nt][3]);
+            }
         }
         if (tid < C) {
             const float dec = expf(Gh[tid] + Gl[tid]);
@@ -299,29 +301,28 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         // T's terms, row by row (over A); what T's rows were divided by goes to `it`
         float *it = Y;
         {
-            const int row = tid >> 1, side = tid & 1;
-            const float *t = T + row * kLd + 32 * side;
-            float v[32], m = 0.f;
+            const int row = tid >> 2, side = tid & 3;
+            const float *t = T + row * kLd + 16 * side;
+            float v[16], m = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
+            for (int j = 0; j < 16; j += 4) {
                 const float4 u = *reinterpret_cast<const float4 *>(t + j);
                 v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (32 * side + j > row) v[j] = 0.f;
+            for (int j = 0; j < 16; ++j) {
+                if (16 * side + j > row) v[j] = 0.f;
                 m = fmaxf(m, fabsf(v[j]));
             }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             float s, is;
-            pow2_scale(m, s, is);
+            pow2_scale(quad_max(m), s, is);
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < 16; j += 8) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     split_f16(v[j + 2 * e] * s, v[j + 2 * e + 1] * s, hi[e], lo[e]);
-                const uint32_t o = img_off(row, 32 * side + j);
+                const uint32_t o = img_off(row, 16 * side + j);
                 const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 *reinterpret_cast<uint4 *>(sT + o) = h4;
@@ -336,11 +337,10 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
         }
         __syncthreads();
 
-        // M = P T: rows i of this warp; T's row scales go into P's columns
-        float M[8][4] = {}, sM[2], iM[2];
-        const uint32_t uT = smem_u32(sT);
-        {
-            float sP[2], iP[2];
+        if (!forw) {
+            // M = P T: rows i of this warp; T's row scales go into P's columns
+            float M[8][4] = {}, sM[2], iM[2], sP[2], iP[2];
+            const uint32_t uT = smem_u32(sT);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 t2 = *reinterpret_cast<const float2 *>(it + 8 * nt + 2 * q4);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
             row_scales<8>(P, sP, iP);
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                if (jj > warp) break;
+                if (jj > mt) break;
                 uint32_t hi[4], lo[4];
                 a_terms(P[2 * jj], P[2 * jj + 1], sP, hi, lo);
 #pragma unroll
@@ -367,23 +367,32 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
             }
             row_scales<8>(M, sM, iM);
             if (q4 == 0) {
-                vec[kVm * C + 16 * warp + gq] = iP[0] * iM[0];
-                vec[kVm * C + 16 * warp + gq + 8] = iP[1] * iM[1];
+                vec[kVm * C + 16 * mt + gq] = iP[0] * iM[0];
+                vec[kVm * C + 16 * mt + gq + 8] = iP[1] * iM[1];
             }
-        }
-        // H = T^T diag(u) K: rows j of this warp, summed over tokens i >= j
-        float Hc[DK / 8][4] = {}, iA[2];
-        {
+            named_bar(1, 128);  // T's terms are read
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t hi, lo;
+                    split_f16(M[nt][2 * x] * sM[x], M[nt][2 * x + 1] * sM[x], hi, lo);
+                    const uint32_t o = img_off(16 * mt + gq + 8 * x, 8 * nt) + 4 * q4;
+                    *reinterpret_cast<uint32_t *>(sT + o) = hi;
+                    *reinterpret_cast<uint32_t *>(sT + kImg + o) = lo;
+                }
+        } else {
+            // H = T^T diag(u) K: rows j of this warp, summed over tokens i >= j
+            float Hc[DK / 8][4] = {}, A[8][4] = {}, sA[2], iA[2];
             const float GC = Gh[C - 1], GCl = Gl[C - 1];
-            float A[8][4] = {}, sA[2];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
-                if (nt < 2 * warp) continue;
+                if (nt < 2 * mt) continue;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int i = 8 * nt + 2 * q4 + x;
                     const float u = expf((GC - Gh[i]) + (GCl - Gl[i])) * eta[i] * iK[i];
-                    const float *t = T + i * kLd + 16 * warp + gq;
+                    const float *t = T + i * kLd + 16 * mt + gq;
                     // inside the diagonal block T holds zeros above the diagonal
                     A[nt][x] = u * t[0];
                     A[nt][2 + x] = u * t[8];
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
             row_scales<8>(A, sA, iA);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
-                if (kb < warp) continue;
+                if (kb < mt) continue;
                 uint32_t hi[4], lo[4];
                 a_terms(A[2 * kb], A[2 * kb + 1], sA, hi, lo);
 #pragma unroll
@@ -405,58 +414,44 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_kernel(PrepArgs a) {
                         mma_f16(Hc[2 * np + x], lo, bb[2 * x], bb[2 * x + 1]);
                     }
                     if (!BF16) {
-                        load_bt(bb, uK + C * DK * 2, 16 * kb, 16 * np, lane);
+                        load_bt(bb, uK + KIMG, 16 * kb, 16 * np, lane);
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
                             mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
                     }
                 }
             }
-            float m = 0.f;
+            // one scale for the 16 rows: they are one step of the sums over tokens
+            float m[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < DK / 8; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    Hc[nt][e] *= iA[e >> 1];
-                    m = fmaxf(m, fabsf(Hc[nt][e]));
+                for (int e = 0; e < 4; ++e) m[e >> 1] = fmaxf(m[e >> 1], fabsf(Hc[nt][e]));
+            float mm = fmaxf(m[0] * iA[0], m[1] * iA[1]), sH, iH;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+            pow2_scale(mm, sH, iH);
+            if (lane == 0) vec[kVs * C + 1 + mt] = iH;
+            if (tid == 128) vec[kVs * C] = expf(GC + GCl);
+            const float sHr[2] = {iA[0] * sH, iA[1] * sH};
+            named_bar(2, 128);  // T is read
+#pragma unroll
+            for (int nt = 0; nt < DK / 8; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t hi, lo;
+                    split_f16(Hc[nt][2 * x] * sHr[x], Hc[nt][2 * x + 1] * sHr[x], hi, lo);
+                    const uint32_t o = img_off(16 * mt + gq + 8 * x, 8 * nt) + 4 * q4;
+                    *reinterpret_cast<uint32_t *>(sQ + o) = hi;
+                    *reinterpret_cast<uint32_t *>(sHl + o) = lo;
                 }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) red[warp] = m;
         }
-        __syncthreads();  // T (both forms) is read, the four maxima are there
-        float sH, iH;
-        pow2_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), sH, iH);
-        if (tid == 0) {
-            vec[kVs * C] = expf(Gh[C - 1] + Gl[C - 1]);
-            vec[kVs * C + 1] = iH;
-        }
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t hi, lo;
-                split_f16(M[nt][2 * x] * sM[x], M[nt][2 * x + 1] * sM[x], hi, lo);
-                const uint32_t o = img_off(16 * warp + gq + 8 * x, 8 * nt) + 4 * q4;
-                *reinterpret_cast<uint32_t *>(sT + o) = hi;
-                *reinterpret_cast<uint32_t *>(sT + kImg + o) = lo;
-            }
-#pragma unroll
-        for (int nt = 0; nt < DK / 8; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t hi, lo;
-                split_f16(Hc[nt][2 * x] * sH, Hc[nt][2 * x + 1] * sH, hi, lo);
-                const uint32_t o = img_off(16 * warp + gq + 8 * x, 8 * nt) + 4 * q4;
-                *reinterpret_cast<uint32_t *>(sQ + o) = hi;
-                *reinterpret_cast<uint32_t *>(sHl + o) = lo;
-            }
         fence_async_smem();
         __syncthreads();
         if (tid == 0) {
             bulk_store(a.im.M + hslot * 2 * kImg, sT, 2 * kImg);
-            bulk_store(a.im.H + hslot * a.im.himg, sQ, C * DK * 2);
-            bulk_store(a.im.H + hslot * a.im.himg + C * DK * 2, sHl, C * DK * 2);
+            bulk_store(a.im.H + hslot * a.im.himg, sQ, KIMG);
+            bulk_store(a.im.H + hslot * a.im.himg + KIMG, sHl, KIMG);
             bulk_commit();
         }
     }
@@ -472,7 +467,7 @@ struct ScanArgs {
     float *W_out;
     const int *seq_start;
     int B, Hk, H, T, dv, w_heads;  // w_heads: 0 when W0 is shared by the sequences
-    int cgs;                       // column groups of a block: 16 columns of W, two warps each
+    int cgs;                       // column groups of a block: 16 columns of W, four warps each
     int stages;
     Images im;
     float *saveS, *saveX;          // kSave: [slot][H][DK][dv] and [slot][H][64][dv]
@@ -485,35 +480,41 @@ constexpr int scan_stage_bytes() {
     return (MODE == kSave ? 1 : 2) * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 +
            (MODE == kSave ? 0 : MODE == kZ32 ? 2 : 1) * kImg + kScanVecBytes;
 }
-template <bool BF16>
-constexpr int v_tile_bytes() { return BF16 ? C * 32 : C * 20 * 4; }
-// A warp's own area behind the stages: its V tile and what it hands its partner.
-template <bool BF16, int MODE>
-constexpr int warp_bytes() { return v_tile_bytes<BF16>() + (MODE == kSave ? 4096 : 6144); }
+// A column group's own area behind the stages: the four warps' shares of X
+// [to][from][2 tiles], the terms of X [4 blocks][hi, lo], of W^T [DK / 16][hi, (lo)], 1 / their scales.
+template <int DK, int MODE>
+constexpr int scan_group_bytes() {
+    return 16 * 1024 + 4096 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1)) + 512;
+}
 
-// Scan over the chunks. Two warps own 16 columns of W for the whole sequence, as
-// rows of W^T [16][DK] in accumulator registers, half of DK each: accumulator
-// fragments packed pairwise are A fragments, so W^T K^T, X^T M^T and X^T H follow
-// one another in registers, and the only thing the two hand one another is
-// their halves of the sums over DK, once a chunk, through shared memory. Both
-// then form X (the same bits), each writes Z of half the tokens and updates its
-// half of W. Column groups know nothing of one another.
+// Scan over the chunks. Four warps own 16 columns of W for the whole sequence, as
+// the rows of W^T [16][DK] in accumulator registers, a quarter of DK each:
+// accumulator fragments packed pairwise are A fragments, so W^T K^T and X^T H
+// follow one another in registers. Twice a chunk the four meet:
+//   1. each has its quarter's share of W^T K^T for all 64 tokens and hands the
+//      others theirs; warp p then forms X of the 16 tokens of block p, and brings
+//      it into operand form under that block's own row scales;
+//   2. each takes the operand X of all blocks and updates its quarter of W.
+// Z of block p is warp p's too: c D Q W from the operand form of W^T that the four
+// have handed round in step 1 (a quarter's rows under its own scales, so the
+// sums over the quarters are put together in fp32), and M X. Between the meetings
+// column groups and blocks know nothing of one another.
 // The chunk's images come through a ring of shared-memory stages, filled with
 // bulk copies that the first thread issues; V through registers, one chunk ahead.
 template <int DK, bool BF16, int MODE>
-__global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(1024) char ssm[];
     __shared__ uint64_t full[4], empty[4];
     __shared__ int abort_flag;
     constexpr bool ZF = MODE == kZ32, SAVE = MODE == kSave;
     constexpr int STAGE = scan_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
-    constexpr int NT = DK / 16;  // 8-column tiles of this warp's half of W^T
+    constexpr int NT = DK / 32, KK = DK / 64;  // 8-column tiles and 16-deep steps of a quarter
     constexpr int oH = SAVE ? KALL : 2 * KALL, oM = oH + 2 * KIMG;
     const int groups = a.dv / (16 * a.cgs);
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = warp & 1;
+    const int tid = threadIdx.x, lane = tid & 31, cg = tid >> 7, p = (tid >> 5) & 3;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
         abort_flag = 0;
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2 * a.cgs);
+            mbar_init(&empty[s], 4 * a.cgs);
         }
         fence_mbar_init();
     }
@@ -551,32 +552,27 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
         for (int c = 0; c < nchunk && c < a.stages - 1; ++c) fill(c);
 
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = (grp * a.cgs + (warp >> 1)) * 16;
+    const int v0 = (grp * a.cgs + cg) * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *own = ssm + a.stages * STAGE + warp * warp_bytes<BF16, MODE>();
-    char *vt = own;
-    float4 *give = reinterpret_cast<float4 *>(own + v_tile_bytes<BF16>()) + lane;
-    const float4 *take = reinterpret_cast<const float4 *>(
-                             ssm + a.stages * STAGE + (warp ^ 1) * warp_bytes<BF16, MODE>() +
-                             v_tile_bytes<BF16>()) + lane;
-    constexpr int VU = BF16 ? 4 : 8;  // 16-byte units of V per lane
-    uint4 vr[VU];
+    char *area = ssm + a.stages * STAGE + cg * scan_group_bytes<DK, MODE>();
+    float4 *part = reinterpret_cast<float4 *>(area) + lane;               // [to][from][tile][32]
+    uint4 *xfr = reinterpret_cast<uint4 *>(area + 16 * 1024) + lane;      // [block][hi, lo][32]
+    float *iXs = reinterpret_cast<float *>(area + 20 * 1024), *iSs = iXs + 64;  // [block][16], [quarter][16]
+    uint4 *sfr = reinterpret_cast<uint4 *>(area + 20 * 1024 + 512) + lane;  // [step][hi, (lo)][32]
+
+    // V of this lane's places in block p: tokens 16 p + 8 x + 2 q4 + {0, 1}, columns gq, gq + 8
+    float v[2][4];
     auto fetch_v = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < VU; ++i) {
-            const int u = lane + 32 * i, row = BF16 ? u >> 1 : u >> 2, part = BF16 ? u & 1 : u & 3;
-            vr[i] = make_uint4(0, 0, 0, 0);
-            if (c * C + row < len) {
-                const size_t at = (vrow + c * C + row) * a.dv + v0;
-                vr[i] = BF16 ? *reinterpret_cast<const uint4 *>(
-                                   static_cast<const __nv_bfloat16 *>(a.V) + at + 8 * part)
-                             : *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.V) +
-                                                                at + 4 * part);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = c * C + 16 * p + 8 * x + 2 * q4 + (e & 1);
+                v[x][e] = t < len ? load_elem(a.V, (vrow + t) * a.dv + v0 + gq + (e >> 1) * 8, BF16) : 0.f;
             }
-        }
     };
     // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns k0 + 8 nt + 2 q4 + {0, 1}
-    const int k0 = half * (DK / 2);
+    const int k0 = p * (DK / 4);
     float S[NT][4];
     const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
     const float *w0 = a.W0 ? a.W0 + ((size_t)n * a.w_heads + h) * state + mine : nullptr;
@@ -593,16 +589,7 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
         const bool ok = mbar_wait_warp(&full[s], (c / a.stages) & 1, abort, a.status, kScanStatus);
         const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
         const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
-        // both warps are past reading what the other gave for the chunk before;
-        // and leave together when a wait has run out
-        if (named_bar_or(1 + (warp >> 1), 64, !ok)) {
-            // copies in flight land before the block's shared memory goes
-            if (tid == 0)
-                for (int p = c; p < c + a.stages && p < nchunk; ++p)
-                    mbar_drain(&full[p % a.stages], (p / a.stages) & 1);
-            return;
-        }
-        if (SAVE) {
+        if (SAVE && ok) {
             float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -610,16 +597,19 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
                 for (int e = 0; e < 4; ++e)
                     ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
         }
-
-        // X^T = W^T K^T, Z^T = W^T Q^T over this warp's half of DK
-        float X[8][4] = {}, Z[8][4] = {};
-        {
-            float sS[2], iS[2];
+        // W^T K^T over this warp's quarter of DK, W^T's terms handed round for Z
+        if (ok) {
+            float X[8][4] = {}, sS[2], iS[2];
             row_scales<NT>(S, sS, iS);
 #pragma unroll
-            for (int kk = 0; kk < NT / 2; ++kk) {
+            for (int kk = 0; kk < KK; ++kk) {
                 uint32_t hi[4], lo[4], bb[4][4];
                 a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+                if (!SAVE) {
+                    uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (p * KK + kk);
+                    d[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (ZF) d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
 #pragma unroll
                 for (int np = 0; np < 4; ++np) load_b(bb[np], uK, 16 * np, k0 + 16 * kk, lane);
 #pragma unroll
@@ -628,17 +618,6 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
                     mma_f16(X[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                if (!SAVE) {
-#pragma unroll
-                    for (int np = 0; np < 4; ++np) load_b(bb[np], uQ, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-                        mma_f16(Z[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                    if (ZF)
-#pragma unroll
-                        for (int nt = 0; nt < 8; ++nt)
-                            mma_f16(Z[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                }
                 if (!BF16) {
 #pragma unroll
                     for (int np = 0; np < 4; ++np)
@@ -646,149 +625,168 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt)
                         mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                    if (ZF) {
-#pragma unroll
-                        for (int np = 0; np < 4; ++np)
-                            load_b(bb[np], uQ + KIMG, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                        for (int nt = 0; nt < 8; ++nt)
-                            mma_f16(Z[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                    }
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) X[nt][e] *= iS[e >> 1], Z[nt][e] *= iS[e >> 1];
+                part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
+                    iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
+            if (!SAVE && q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
         }
-        // hand over: all of X, and Z of the tokens that the partner writes. The
-        // 16-token blocks 0 and 3 are the first warp's, 1 and 2 the second's, so
-        // that both take the same share of the triangle P.
+        // the first meeting; all leave together when a wait has run out
+        if (named_bar_or(1 + cg, 128, !ok)) {
+            // copies in flight land before the block's shared memory goes
+            if (tid == 0)
+                for (int i = c; i < c + a.stages && i < nchunk; ++i)
+                    mbar_drain(&full[i % a.stages], (i / a.stages) & 1);
+            return;
+        }
+        // X of block p, in operand form
+        {
+            float X[2][4];
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) give[32 * nt] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
-        if (!SAVE) {
+            for (int x = 0; x < 2; ++x) {
+                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
+                float4 o = part[32 * (8 * p + x)];
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float(&zA)[4] = Z[2 * (y ? 2 : 1) + x], (&zB)[4] = Z[2 * (y ? 3 : 0) + x];
-                    give[32 * (8 + 2 * y + x)] =
-                        half ? make_float4(zB[0], zB[1], zB[2], zB[3])
-                             : make_float4(zA[0], zA[1], zA[2], zA[3]);
+                for (int w = 1; w < 4; ++w) {
+                    const float4 u = part[32 * (8 * p + 2 * w + x)];
+                    o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
                 }
-        }
-        // V of this chunk to shared memory, the next chunk's on its way
-#pragma unroll
-        for (int i = 0; i < VU; ++i) {
-            const int u = lane + 32 * i;
-            // bf16: rows of 32 bytes, the halves of every other four rows swapped
-            // (eight rows of an ldmatrix then meet all banks); fp32: 80 bytes
-            const int row = BF16 ? u >> 1 : u >> 2, part = BF16 ? u & 1 : u & 3;
-            char *d = BF16 ? vt + row * 32 + ((part ^ ((row >> 2) & 1)) << 4) : vt + row * 80 + part * 16;
-            *reinterpret_cast<uint4 *>(d) = vr[i];
-        }
-        if (c + 1 < nchunk) fetch_v(c + 1);
-        named_bar(1 + (warp >> 1), 64);
-
-        // X = V - D K W
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            float v[2][4];
-            if (BF16) {
-                uint32_t r[4];  // tokens 16 np + {0..7, 8..15} x columns {0..7, 8..15}
-                const int row = 16 * np + (lane & 7) + ((lane >> 4) << 3), part = (lane >> 3) & 1;
-                ldsm_x4_t(r, smem_u32(vt) + row * 32 + ((part ^ ((row >> 2) & 1)) << 4));
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        v[x][2 * y] = __uint_as_float(r[2 * x + y] << 16);
-                        v[x][2 * y + 1] = __uint_as_float(r[2 * x + y] & 0xFFFF0000u);
-                    }
-            } else {
-                const float *f = reinterpret_cast<const float *>(vt);
+                X[x][0] = v[x][0] - ck.x * o.x;
+                X[x][1] = v[x][1] - ck.y * o.y;
+                X[x][2] = v[x][2] - ck.x * o.z;
+                X[x][3] = v[x][3] - ck.y * o.w;
+            }
+            if (c + 1 < nchunk) fetch_v(c + 1);
+            if (SAVE) {
+                float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + gq;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[x][e] = f[(16 * np + 8 * x + 2 * q4 + (e & 1)) * 20 + gq + (e >> 1) * 8];
+                        wx[(size_t)(8 * x + (e & 1)) * a.dv + (e >> 1) * 8] = X[x][e];
             }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int nt = 2 * np + x;
-                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 8 * nt + 2 * q4);
-                const float4 o = take[32 * nt];
-                // first half plus second half, in both warps
-                X[nt][0] = v[x][0] - ck.x * (X[nt][0] + o.x);
-                X[nt][1] = v[x][1] - ck.y * (X[nt][1] + o.y);
-                X[nt][2] = v[x][2] - ck.x * (X[nt][2] + o.z);
-                X[nt][3] = v[x][3] - ck.y * (X[nt][3] + o.w);
-                m0 = fmaxf(m0, fmaxf(fabsf(X[nt][0]), fabsf(X[nt][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(X[nt][2]), fabsf(X[nt][3])));
-            }
+            float sX[2], iX[2];
+            uint32_t hi[4], lo[4];
+            row_scales<2>(X, sX, iX);
+            a_terms(X[0], X[1], sX, hi, lo);
+            xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
         }
-
-        if (SAVE) {
-            float *wx = a.saveX + ((size_t)(slot0 + c) * a.H + h) * C * a.dv + v0 + gq;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int nt = 4 * half + y;
-                float x[4];  // chosen by value: a pointer into X would send it to memory
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = half ? X[4 + y][e] : X[y][e];
-                float *w = wx + (size_t)(8 * nt + 2 * q4) * a.dv;
-                w[0] = x[0], w[8] = x[2], w[a.dv] = x[1], w[a.dv + 8] = x[3];
-            }
-        }
-        // X's terms, for both products that take it
-        uint32_t hi[4][4], lo[4][4];
-        float sX[2], iX[2];
-        pow2_scale(quad_max(m0), sX[0], iX[0]);
-        pow2_scale(quad_max(m1), sX[1], iX[1]);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) a_terms(X[2 * jj], X[2 * jj + 1], sX, hi[jj], lo[jj]);
-
-        // Z^T += X^T M^T of this warp's tokens
+        // (Q W)^T of block p, quarter by quarter
+        float Z[2][4] = {};
         if (!SAVE) {
-            float Y[4][4] = {};
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                uint32_t bb[2][4];
+            for (int w = 0; w < 4; ++w) {
+                float z[2][4] = {};
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int np = half ? 1 + y : 3 * y;
-                    if (np < jj) continue;  // M_ij is zero for i < j; the same for the whole warp
-                    load_b(bb[y], uM, 16 * np, 16 * jj, lane);
+                for (int kk = 0; kk < KK; ++kk) {
+                    const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
+                    const uint4 fh = d[0];
+                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
+                    uint32_t bb[4];
+                    load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(Y[2 * y + x], hi[jj], bb[y][2 * x], bb[y][2 * x + 1]);
-                        if (ZF) mma_f16(Y[2 * y + x], lo[jj], bb[y][2 * x], bb[y][2 * x + 1]);
-                    }
+                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
                     if (ZF) {
-                        load_b(bb[y], uM + kImg, 16 * np, 16 * jj, lane);
+                        const uint4 fl = d[32];
+                        const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            mma_f16(Y[2 * y + x], hi[jj], bb[y][2 * x], bb[y][2 * x + 1]);
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
+                        if (!BF16) {
+                            load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
+                        }
                     }
                 }
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
+                const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int nt = 2 * (half ? 1 + y : 3 * y) + x;
-                    const float(&zA)[4] = Z[2 * (y ? 2 : 1) + x], (&zB)[4] = Z[2 * (y ? 3 : 0) + x];
-                    const float4 o = take[32 * (8 + 2 * y + x)];
-                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + 8 * nt + 2 * q4);
-                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + 8 * nt + 2 * q4);
-                    const float(&y4)[4] = Y[2 * y + x];
-                    const float z0 = cq.x * ((half ? zA[0] : zB[0]) + o.x) + im.x * (iX[0] * y4[0]);
-                    const float z1 = cq.y * ((half ? zA[1] : zB[1]) + o.y) + im.y * (iX[0] * y4[1]);
-                    const float z2 = cq.x * ((half ? zA[2] : zB[2]) + o.z) + im.x * (iX[1] * y4[2]);
-                    const float z3 = cq.y * ((half ? zA[3] : zB[3]) + o.w) + im.y * (iX[1] * y4[3]);
+                    Z[x][0] = fmaf(i0, z[x][0], Z[x][0]);
+                    Z[x][1] = fmaf(i0, z[x][1], Z[x][1]);
+                    Z[x][2] = fmaf(i1, z[x][2], Z[x][2]);
+                    Z[x][3] = fmaf(i1, z[x][3], Z[x][3]);
+                }
+            }
+        }
+        named_bar(1 + cg, 128);  // the second meeting
+
+        // W'^T = exp(G_C) W^T + X^T H; Z^T += X^T M^T of block p
+        {
+            const float gam = vec[kVs * C];
+            float ZM[2][4] = {};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
+                const float iH = vec[kVs * C + 1 + jj];
+                float U[NT][4] = {};
+                uint32_t bh[KK][4], bl[KK][4];
+#pragma unroll
+                for (int np = 0; np < KK; ++np) {
+                    load_bt(bh[np], uH, 16 * jj, k0 + 16 * np, lane);
+                    load_bt(bl[np], uH + KIMG, 16 * jj, k0 + 16 * np, lane);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], lo, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, bl[nt >> 1][2 * (nt & 1)], bl[nt >> 1][2 * (nt & 1) + 1]);
+                if (!SAVE && jj <= p) {  // M_ij is zero for i < j; the same for the whole warp
+                    float z[2][4] = {};
+                    uint32_t bm[4];
+                    load_b(bm, uM, 16 * p, 16 * jj, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
+                    }
                     if (ZF) {
-                        const int t = c * C + 8 * nt + 2 * q4;
+                        load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        ZM[x][0] = fmaf(i0, z[x][0], ZM[x][0]);
+                        ZM[x][1] = fmaf(i0, z[x][1], ZM[x][1]);
+                        ZM[x][2] = fmaf(i1, z[x][2], ZM[x][2]);
+                        ZM[x][3] = fmaf(i1, z[x][3], ZM[x][3]);
+                    }
+                }
+                const float u0 = i0 * iH, u1 = i1 * iH;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    S[nt][0] = fmaf(u0, U[nt][0], S[nt][0]);
+                    S[nt][1] = fmaf(u0, U[nt][1], S[nt][1]);
+                    S[nt][2] = fmaf(u1, U[nt][2], S[nt][2]);
+                    S[nt][3] = fmaf(u1, U[nt][3], S[nt][3]);
+                }
+            }
+            if (!SAVE) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = 16 * p + 8 * x;
+                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i + 2 * q4);
+                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i + 2 * q4);
+                    const float z0 = cq.x * Z[x][0] + im.x * ZM[x][0];
+                    const float z1 = cq.y * Z[x][1] + im.y * ZM[x][1];
+                    const float z2 = cq.x * Z[x][2] + im.x * ZM[x][2];
+                    const float z3 = cq.y * Z[x][3] + im.y * ZM[x][3];
+                    if (ZF) {
+                        const int t = c * C + i + 2 * q4;
                         float *z = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
                         if (t < len) z[0] = z0, z[8] = z2;
                         if (t + 1 < len) z[a.dv] = z1, z[a.dv + 8] = z3;
@@ -798,7 +796,7 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
                         const __nv_bfloat162 p1 = __floats2bfloat162_rn(z2, z3);
                         const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
                         const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
-                        const int t = c * C + 8 * nt + gq;
+                        const int t = c * C + i + gq;
                         if (t < len) {
                             uint32_t *z = reinterpret_cast<uint32_t *>(
                                 static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
@@ -807,38 +805,6 @@ __global__ void __launch_bounds__(256, 1) delta_scan_kernel(ScanArgs a) {
                         }
                     }
                 }
-        }
-
-        // W'^T = exp(G_C) W^T + X^T H
-        {
-            const float gam = vec[kVs * C], iH = vec[kVs * C + 1];
-            const float iU[2] = {iX[0] * iH, iX[1] * iH};
-#pragma unroll
-            for (int np = 0; np < NT / 2; np += 2) {  // two 16-column blocks: four chains
-                float U[4][4] = {};
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    uint32_t bb[2][4], bl[2][4];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        load_bt(bb[y], uH, 16 * jj, k0 + 16 * (np + y), lane);
-                        load_bt(bl[y], uH + KIMG, 16 * jj, k0 + 16 * (np + y), lane);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_f16(U[x], hi[jj], bb[x >> 1][2 * (x & 1)], bb[x >> 1][2 * (x & 1) + 1]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_f16(U[x], lo[jj], bb[x >> 1][2 * (x & 1)], bb[x >> 1][2 * (x & 1) + 1]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_f16(U[x], hi[jj], bl[x >> 1][2 * (x & 1)], bl[x >> 1][2 * (x & 1) + 1]);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        S[2 * np + x][e] = fmaf(iU[e >> 1], U[x][e], gam * S[2 * np + x][e]);
             }
         }
         __syncwarp();
@@ -869,9 +835,9 @@ cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
 
 template <int DK, bool BF16, int MODE>
 cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
-    r.cgs = scan_groups((long long)N * r.H, r.dv);
+    r.cgs = scan_groups((long long)N * r.H, DK, r.dv);
     constexpr int stage = scan_stage_bytes<DK, BF16, MODE>();
-    const int wbytes = 2 * r.cgs * warp_bytes<BF16, MODE>();
+    const int wbytes = r.cgs * scan_group_bytes<DK, MODE>();
     r.stages = (226 * 1024 - wbytes) / stage;
     r.stages = r.stages > 3 ? 3 : r.stages;
     const int smem = r.stages * stage + wbytes;
@@ -879,7 +845,7 @@ cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
-    delta_scan_kernel<DK, BF16, MODE><<<grid, 64 * r.cgs, smem, s>>>(r);
+    delta_scan_kernel<DK, BF16, MODE><<<grid, 128 * r.cgs, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
@@ -907,15 +873,16 @@ cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cud
     return a.bf16 ? prep_inst<128, true>(r, blocks, s) : prep_inst<128, false>(r, blocks, s);
 }
 
-// Column groups of a block (one block per SM): one or two leave each warp a
-// scheduler of its own, four share them. The fewest rounds of blocks over the 148
-// SMs win, a round of four-group blocks counted 1.6 times.
-int scan_groups(long long heads, int dv) {
+// Column groups of a block (one block per SM): the fewest rounds of blocks over
+// the 148 SMs win. A chunk of a block of two groups takes 1.2 times that of one, of
+// four 2 times (their warps share the schedulers).
+int scan_groups(long long heads, int dk, int dv) {
     int best = 1;
     double least = 1e30;
-    for (int cgs = 1; cgs <= 4; cgs *= 2) {
-        const double rounds = (double)((heads * (dv / (16 * cgs)) + 147) / 148) * (cgs == 4 ? 1.6 : 1.0);
-        if (rounds <= least) least = rounds, best = cgs;
+    for (int cgs = 1; cgs <= (dk == 64 ? 4 : 2); cgs *= 2) {
+        const double rounds = (double)((heads * (dv / (16 * cgs)) + 147) / 148) *
+                              (cgs == 4 ? 2.0 : cgs == 2 ? 1.2 : 1.0);
+        if (rounds < least) least = rounds, best = cgs;
     }
     return best;
 }

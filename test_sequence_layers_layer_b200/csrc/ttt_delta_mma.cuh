@@ -30,7 +30,7 @@ enum Vec {
     kVk,   // exp(G_j) / sK_j
     kVq,   // c exp(G_i) / sQ_i
     kVm,   // 1 / sM_i
-    kVs,   // [0] exp(G_C), [1] 1 / sH (one scale for the image of H)
+    kVs,   // [0] exp(G_C), [1 + b] 1 / sH of the 16 rows of block b (one scale for them)
     kVik,  // 1 / sK_j
     kViq,  // 1 / sQ_i
     kVgh,  // G_j as the sum of two floats
@@ -213,7 +213,7 @@ struct ChunkSearch {
 // The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
 Images images_at(const Plan &p, void *workspace, bool bwd);
-int scan_groups(long long heads, int dv);
+int scan_groups(long long heads, int dk, int dv);
 cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
                         cudaStream_t s);
 
