@@ -688,82 +688,86 @@ def affine_prefix(M, N, W0, W_in, W_end=None, *, S, H, nseg, seq_stride, seg_str
 # The calls below read their shapes off the tensors, check every tensor
 # (device, type, shape, contiguous) and run on the tensors' own device, on
 # `stream` or that device's current stream; what they allocate belongs to the
-# stream that uses it.
+# stream that uses it. They are written for calls of a few microseconds: plain
+# attribute reads and one C call, no context managers unless the device differs.
 
-def _tensors(fn, device, **want):
+def _tensors(fn, index, **want):
     """want: name=(tensor or None, dtypes, shape). Raises ValueError on the first that is off."""
     for name, (t, dtypes, shape) in want.items():
-        if t is None:
+        if t is None or (t.get_device() == index and t.dtype in dtypes and t.shape == shape
+                         and t.is_contiguous()):
             continue
-        if t.device != device:
-            raise ValueError(f"{fn}: {name} is on {t.device}, expected {device}")
+        if t.get_device() != index:
+            raise ValueError(f"{fn}: {name} is on {t.device}, expected cuda:{index}")
         if t.dtype not in dtypes:
             raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} is not contiguous")
+        raise ValueError(f"{fn}: {name} is not contiguous")
 
 
 class _On:
-    """The device and the stream of a call; empty() allocates for that stream."""
+    """The device and the stream of a call: empty() allocates for it, run() makes it."""
+
+    __slots__ = ("fn", "index", "device", "handle", "side", "torch")
 
     def __init__(self, fn, first, stream):
         import torch
         if not first.is_cuda:
             raise ValueError(f"{fn}: tensors must be on a CUDA device, got {first.device}")
-        self.device = first.device
-        self._guard = torch.cuda.device(first.device)
+        self.torch, self.fn, self.device, self.side = torch, fn, first.device, None
+        self.index = index = first.get_device()
+        current = torch.cuda.current_stream(index)
+        self.handle = current.cuda_stream
+        if stream is None:
+            return
         if isinstance(stream, int):
             # 0 is the legacy default stream, which torch knows as its default stream
             stream = torch.cuda.ExternalStream(stream, device=first.device) if stream else \
                 torch.cuda.default_stream(first.device)
-        if stream is not None and stream.device != first.device:
+        if stream.device != first.device:
             raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {first.device}")
-        self._stream = stream
-
-    def __enter__(self):
-        import torch
-        self._guard.__enter__()
-        if self._stream is None:
-            self._stream = torch.cuda.current_stream()
-        self._other = self._stream != torch.cuda.current_stream()
-        self.handle = self._stream.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+        if stream != current:
+            self.handle, self.side = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
-        import torch
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self._other:
+        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if self.side is not None:
             # memory the current stream may still be using: the call waits for
             # that, and the block is not handed out again before the call is done
-            self._stream.wait_stream(torch.cuda.current_stream())
-            t.record_stream(self._stream)
+            self.side.wait_stream(self.torch.cuda.current_stream(self.index))
+            t.record_stream(self.side)
         return t
 
-    def workspace(self, fn, given, need):
-        import torch
+    def workspace(self, given, need):
+        """A workspace of `need` bytes (a given one is checked): its address and size."""
         if given is None:
-            return self.empty(max(need, 256), torch.uint8) if need else None
-        if given.device != self.device or not given.is_contiguous():
-            raise ValueError(f"{fn}: workspace must be contiguous and on {self.device}")
-        return given
+            return self.empty(max(need, 256), self.torch.uint8).data_ptr(), max(need, 256)
+        if given.get_device() != self.index or not given.is_contiguous():
+            raise ValueError(f"{self.fn}: workspace must be contiguous and on cuda:{self.index}")
+        return given.data_ptr(), given.numel() * given.element_size()
+
+    def run(self, name, f, *args):
+        if self.torch.cuda.current_device() == self.index:
+            rc = f(*args, self.handle)
+        else:
+            with self.torch.cuda.device(self.index):
+                rc = f(*args, self.handle)
+        if rc != TTT_OK:
+            raise TTTError(name, rc)
 
 
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
-def _delta_shapes(fn, dev, Q, K, V, eta, g, W0, w0_per_seq, seq_start):
-    """Checks the inputs of the gated delta rule; returns B, Hk, H, T, dk, dv, n_seq, N."""
+def _delta_shapes(fn, index, Q, K, V, eta, g, W0, w0_per_seq, seq_start):
+    """Checks the inputs of the gated delta rule; returns B, Hk, H, T, dk, dv, n_seq, N, dtype code."""
     import torch
     if Q.dim() != 4 or V.dim() != 4:
         raise ValueError(f"{fn}: Q, K, V must be [B, heads, T, d]")
     B, Hk, T, dk = Q.shape
-    H, dv = V.shape[1], V.shape[3]
+    _, H, _, dv = V.shape
     n_seq = 0
     if seq_start is not None:
         if seq_start.dim() != 1 or seq_start.numel() < 2:
@@ -772,13 +776,13 @@ def _delta_shapes(fn, dev, Q, K, V, eta, g, W0, w0_per_seq, seq_start):
             raise ValueError(f"{fn}: packed sequences need B = 1, got {B}")
         n_seq = seq_start.numel() - 1
     N = n_seq or B
+    code = _dtype_code(Q)
     f32, same = (torch.float32,), (Q.dtype,)
-    _dtype_code(Q)
-    _tensors(fn, dev, Q=(Q, same, (B, Hk, T, dk)), K=(K, same, (B, Hk, T, dk)),
+    _tensors(fn, index, Q=(Q, same, (B, Hk, T, dk)), K=(K, same, (B, Hk, T, dk)),
              V=(V, same, (B, H, T, dv)), eta=(eta, f32, (B, H, T)), g=(g, f32, (B, H, T)),
              W0=(W0, f32, (N, H, dk, dv) if w0_per_seq else (H, dk, dv)),
              seq_start=(seq_start, (torch.int32,), (n_seq + 1,)))
-    return B, Hk, H, T, dk, dv, n_seq, N
+    return B, Hk, H, T, dk, dv, n_seq, N, code
 
 
 def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None, q_scale=1.0,
@@ -789,19 +793,22 @@ def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None
     T (B = 1). Returns (Z [B, H, T, dv], W_out [N, H, dk, dv] or None). Z may be given; its rows
     outside every sequence are left as they are (in a new Z they are undefined)."""
     import torch
-    with _On("delta_fwd", Q, stream) as on:
-        B, Hk, H, T, dk, dv, n_seq, N = _delta_shapes("delta_fwd", on.device, Q, K, V, eta, g, W0,
-                                                      w0_per_seq, seq_start)
-        zt = torch.bfloat16 if z_bf16 else torch.float32
-        if Z is None:
-            Z = on.empty((B, H, T, dv), zt)
-        _tensors("delta_fwd", on.device, Z=(Z, (zt,), (B, H, T, dv)))
-        W_out = on.empty((N, H, dk, dv), torch.float32) if want_w else None
-        need = ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, _dtype_code(Q))
-        workspace = on.workspace("delta_fwd", workspace, need)
-        flags = (TTT_F_W0_PER_SEQ if w0_per_seq else 0) | (TTT_F_Z_BF16 if z_bf16 else 0)
-        ttt_delta_fwd(Q, K, V, eta, g, W0, Z, W_out, seq_start, n_seq, q_scale, B, Hk, H, T, dk,
-                      dv, _dtype_code(Q), flags, workspace, _nbytes(workspace), on.handle)
+    on = _On("delta_fwd", Q, stream)
+    B, Hk, H, T, dk, dv, n_seq, N, code = _delta_shapes("delta_fwd", on.index, Q, K, V, eta, g, W0,
+                                                        w0_per_seq, seq_start)
+    zt = torch.bfloat16 if z_bf16 else torch.float32
+    if Z is None:
+        Z = on.empty((B, H, T, dv), zt)
+    else:
+        _tensors("delta_fwd", on.index, Z=(Z, (zt,), (B, H, T, dv)))
+    W_out = on.empty((N, H, dk, dv), torch.float32) if want_w else None
+    L = lib()
+    ws, nbytes = on.workspace(workspace,
+                              L.ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, code))
+    on.run("ttt_delta_fwd", L.ttt_delta_fwd, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+           eta.data_ptr(), _p(g), _p(W0), Z.data_ptr(), _p(W_out), _p(seq_start), n_seq, q_scale,
+           B, Hk, H, T, dk, dv, code,
+           (TTT_F_W0_PER_SEQ if w0_per_seq else 0) | (TTT_F_Z_BF16 if z_bf16 else 0), ws, nbytes)
     return Z, W_out
 
 
@@ -811,20 +818,22 @@ def delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out=None, *, w0_per_seq=False, seq_sta
     for delta_fwd's inputs, as a dict of fp32 tensors Q, K, V, eta and, for what was given, g and
     W0. dZ [B, H, T, dv] and dW_out [N, H, dk, dv] (or None) are fp32."""
     import torch
-    with _On("delta_bwd", Q, stream) as on:
-        B, Hk, H, T, dk, dv, n_seq, N = _delta_shapes("delta_bwd", on.device, Q, K, V, eta, g, W0,
-                                                      w0_per_seq, seq_start)
-        f32 = torch.float32
-        _tensors("delta_bwd", on.device, dZ=(dZ, (f32,), (B, H, T, dv)),
-                 dW_out=(dW_out, (f32,), (N, H, dk, dv)))
-        grads = {n: on.empty(t.shape, f32) for n, t in
-                 dict(Q=Q, K=K, V=V, eta=eta, g=g, W0=W0).items() if t is not None}
-        need = ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, _dtype_code(Q))
-        workspace = on.workspace("delta_bwd", workspace, need or 256)
-        ttt_delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out, grads["Q"], grads["K"], grads["V"],
-                      grads["eta"], grads.get("g"), grads.get("W0"), seq_start, n_seq, q_scale, B,
-                      Hk, H, T, dk, dv, _dtype_code(Q), TTT_F_W0_PER_SEQ if w0_per_seq else 0,
-                      workspace, _nbytes(workspace), on.handle)
+    on = _On("delta_bwd", Q, stream)
+    B, Hk, H, T, dk, dv, n_seq, N, code = _delta_shapes("delta_bwd", on.index, Q, K, V, eta, g, W0,
+                                                        w0_per_seq, seq_start)
+    f32 = torch.float32
+    _tensors("delta_bwd", on.index, dZ=(dZ, (f32,), (B, H, T, dv)),
+             dW_out=(dW_out, (f32,), (N, H, dk, dv)))
+    grads = {n: on.empty(t.shape, f32) for n, t in
+             dict(Q=Q, K=K, V=V, eta=eta, g=g, W0=W0).items() if t is not None}
+    L = lib()
+    ws, nbytes = on.workspace(workspace,
+                              L.ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, code))
+    on.run("ttt_delta_bwd", L.ttt_delta_bwd, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+           eta.data_ptr(), _p(g), _p(W0), dZ.data_ptr(), _p(dW_out), grads["Q"].data_ptr(),
+           grads["K"].data_ptr(), grads["V"].data_ptr(), grads["eta"].data_ptr(),
+           _p(grads.get("g")), _p(grads.get("W0")), _p(seq_start), n_seq, q_scale, B, Hk, H, T, dk,
+           dv, code, TTT_F_W0_PER_SEQ if w0_per_seq else 0, ws, nbytes)
     return grads
 
 
@@ -836,19 +845,22 @@ def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_
     Rows whose index is outside the pool are padding: their Z is left as it is (undefined in a
     new Z). The other rows' indices must be distinct. Returns Z [B, H, n, dv]."""
     import torch
-    with _On("delta_decode", Q, stream) as on:
-        B, Hk, H, n, dk, dv, _, _ = _delta_shapes("delta_decode", on.device, Q, K, V, eta, g, None,
-                                                  False, None)
-        zt = torch.bfloat16 if z_bf16 else torch.float32
-        if W.dim() != 4:
-            raise ValueError("delta_decode: W must be [slots, H, dk, dv]")
-        if Z is None:
-            Z = on.empty((B, H, n, dv), zt)
-        _tensors("delta_decode", on.device, Z=(Z, (zt,), (B, H, n, dv)),
-                 W=(W, (torch.float32,), (W.shape[0], H, dk, dv)),
-                 state_index=(state_index, (torch.int32,), (B,)))
-        ttt_delta_decode(Q, K, V, eta, g, W, Z, state_index, W.shape[0], q_scale, B, Hk, H, n, dk,
-                         dv, _dtype_code(Q), TTT_F_Z_BF16 if z_bf16 else 0, on.handle)
+    on = _On("delta_decode", Q, stream)
+    B, Hk, H, n, dk, dv, _, _, code = _delta_shapes("delta_decode", on.index, Q, K, V, eta, g, None,
+                                                    False, None)
+    zt = torch.bfloat16 if z_bf16 else torch.float32
+    if W.dim() != 4:
+        raise ValueError("delta_decode: W must be [slots, H, dk, dv]")
+    slots = W.shape[0]
+    if Z is None:
+        Z = on.empty((B, H, n, dv), zt)
+    else:
+        _tensors("delta_decode", on.index, Z=(Z, (zt,), (B, H, n, dv)))
+    _tensors("delta_decode", on.index, W=(W, (torch.float32,), (slots, H, dk, dv)),
+             state_index=(state_index, (torch.int32,), (B,)))
+    on.run("ttt_delta_decode", lib().ttt_delta_decode, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+           eta.data_ptr(), _p(g), W.data_ptr(), Z.data_ptr(), _p(state_index), slots, q_scale, B,
+           Hk, H, n, dk, dv, code, TTT_F_Z_BF16 if z_bf16 else 0)
     return Z
 
 
@@ -865,8 +877,9 @@ def delta_decode(q, k, v, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=Fa
 _ACTS = {"silu": 0, "sigmoid": TTT_F_GATE_SIGMOID}
 
 
-def _join_shapes(fn, dev, X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, rms, act):
-    """Checks the inputs of the join; returns B, H, T, d, flags and the parameters' shapes."""
+def _join_shapes(fn, index, X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, rms,
+                 act):
+    """Checks the inputs of the join; returns B, H, T, d, the flags and the dtype code."""
     import torch
     if X.dim() != 3 or (Z is not None and Z.dim() != 4):
         raise ValueError(f"{fn}: expected [B, T, D] and Z [B, H, T, d]")
@@ -876,19 +889,17 @@ def _join_shapes(fn, dev, X, Z, gate, scale, post_gamma, post_beta, pre_gamma, p
     H, d = (1, D) if Z is None else (Z.shape[1], Z.shape[3])
     if H * d != D:
         raise ValueError(f"{fn}: H * d = {H * d} is not D = {D}")
-    _dtype_code(X)
+    code = _dtype_code(X)
     same, f32 = (X.dtype,), (torch.float32,)
-    params = dict(scale=scale, post_gamma=post_gamma, post_beta=post_beta, pre_gamma=pre_gamma,
-                  pre_beta=pre_beta)
-    for name, p in params.items():
-        if p is not None:
-            _tensors(fn, dev, **{name: (p, f32, (H, d) if tuple(p.shape) == (H, d) else (D,))})
-    _tensors(fn, dev, X=(X, same, (B, T, D)), gate=(gate, same, (B, T, D)),
-             Z=(Z, (torch.float32, torch.bfloat16), (B, H, T, d)))
+    flat = lambda p: (p, f32, (D,) if p is None or p.dim() == 1 else (H, d))  # noqa: E731
+    _tensors(fn, index, X=(X, same, (B, T, D)), gate=(gate, same, (B, T, D)),
+             Z=(Z, (torch.float32, torch.bfloat16), (B, H, T, d)), scale=flat(scale),
+             post_gamma=flat(post_gamma), post_beta=flat(post_beta), pre_gamma=flat(pre_gamma),
+             pre_beta=flat(pre_beta))
     flags = (TTT_F_RMS if rms else 0) | _ACTS[act]
     if Z is not None and Z.dtype == torch.bfloat16:
         flags |= TTT_F_Z_BF16
-    return B, H, T, d, flags
+    return B, H, T, d, flags, code
 
 
 def join_fwd(X, Z, gate=None, scale=None, post_gamma=None, post_beta=None, pre_gamma=None,
@@ -898,13 +909,14 @@ def join_fwd(X, Z, gate=None, scale=None, post_gamma=None, post_beta=None, pre_g
     [B, H, T, d] (fp32 or bf16; its norm is per head), the parameters [D] or [H, d] fp32, each
     optional. Returns (R, Hn); Hn is None without want_h. With Z None only Hn = Norm(X) is
     computed, and R is X."""
-    with _On("join_fwd", X, stream) as on:
-        B, H, T, d, flags = _join_shapes("join_fwd", on.device, X, Z, gate, scale, post_gamma,
-                                         post_beta, pre_gamma, pre_beta, rms, act)
-        R = None if Z is None else on.empty(X.shape, X.dtype)
-        Hn = on.empty(X.shape, X.dtype) if want_h else None
-        ttt_join_fwd(X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn, eps, B,
-                     H, T, d, _dtype_code(X), flags, on.handle)
+    on = _On("join_fwd", X, stream)
+    B, H, T, d, flags, code = _join_shapes("join_fwd", on.index, X, Z, gate, scale, post_gamma,
+                                           post_beta, pre_gamma, pre_beta, rms, act)
+    R = None if Z is None else on.empty(X.shape, X.dtype)
+    Hn = on.empty(X.shape, X.dtype) if want_h else None
+    on.run("ttt_join_fwd", lib().ttt_join_fwd, X.data_ptr(), _p(Z), _p(gate), _p(scale),
+           _p(post_gamma), _p(post_beta), _p(pre_gamma), _p(pre_beta), _p(R), _p(Hn), eps, B, H, T,
+           d, code, flags)
     return (X if Z is None else R), Hn
 
 
@@ -915,19 +927,20 @@ def join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, dR, 
     for what was given Z, gate, scale, gamma1, beta1 (post_*), gamma2, beta2 (pre_*; not without
     dH)."""
     import torch
-    with _On("join_bwd", R, stream) as on:
-        B, H, T, d, flags = _join_shapes("join_bwd", on.device, R, Z, gate, scale, post_gamma,
-                                         post_beta, pre_gamma, pre_beta, rms, act)
-        f32 = torch.float32
-        _tensors("join_bwd", on.device, dR=(dR, (f32,), R.shape), dH=(dH, (f32,), R.shape))
-        want = dict(X=R, Z=Z, gate=gate, scale=scale, gamma1=post_gamma, beta1=post_beta)
-        if dH is not None:
-            want.update(gamma2=pre_gamma, beta2=pre_beta)
-        g = {n: on.empty(t.shape, f32) for n, t in want.items() if t is not None}
-        need = ttt_join_bwd_workspace_bytes(B, H, T, d)
-        workspace = on.workspace("join_bwd", workspace, need or 256)
-        ttt_join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, g["X"],
-                     g.get("Z"), g.get("gate"), g.get("scale"), g.get("gamma1"), g.get("beta1"),
-                     g.get("gamma2"), g.get("beta2"), eps, B, H, T, d, _dtype_code(R), flags,
-                     workspace, _nbytes(workspace), on.handle)
+    on = _On("join_bwd", R, stream)
+    B, H, T, d, flags, code = _join_shapes("join_bwd", on.index, R, Z, gate, scale, post_gamma,
+                                           post_beta, pre_gamma, pre_beta, rms, act)
+    f32 = torch.float32
+    _tensors("join_bwd", on.index, dR=(dR, (f32,), R.shape), dH=(dH, (f32,), R.shape))
+    want = dict(X=R, Z=Z, gate=gate, scale=scale, gamma1=post_gamma, beta1=post_beta)
+    if dH is not None:
+        want.update(gamma2=pre_gamma, beta2=pre_beta)
+    g = {n: on.empty(t.shape, f32) for n, t in want.items() if t is not None}
+    L = lib()
+    ws, nbytes = on.workspace(workspace, L.ttt_join_bwd_workspace_bytes(B, H, T, d))
+    at = lambda n: _p(g.get(n))  # noqa: E731
+    on.run("ttt_join_bwd", L.ttt_join_bwd, R.data_ptr(), _p(Z), _p(gate), _p(scale),
+           _p(post_gamma), _p(post_beta), _p(pre_gamma), _p(dR), _p(dH), at("X"), at("Z"),
+           at("gate"), at("scale"), at("gamma1"), at("beta1"), at("gamma2"), at("beta2"), eps, B,
+           H, T, d, code, flags, ws, nbytes)
     return g

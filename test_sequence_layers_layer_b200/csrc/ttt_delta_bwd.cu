@@ -929,8 +929,8 @@ cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
     r.stages = (226 * 1024 - wbytes) / stage;
     r.stages = r.stages > 3 ? 3 : r.stages;
     const int smem = r.stages * stage + wbytes;
-    cudaError_t e = cudaFuncSetAttribute(delta_rev_kernel<DK, BF16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once;
+    cudaError_t e = once.allow(delta_rev_kernel<DK, BF16>, 227 * 1024 - 1024);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
     delta_rev_kernel<DK, BF16><<<grid, 128 * r.cgs, smem, s>>>(r);
@@ -943,8 +943,8 @@ template <int DK, int DV, bool BF16>
 cudaError_t grad_inst(const GradArgs &r, int blocks, cudaStream_t s) {
     constexpr int smem = GradSmem<DK, DV, BF16>::bytes;
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<DK, DV, BF16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once;
+    cudaError_t e = once.allow(delta_grad_kernel<DK, DV, BF16>, smem);
     if (e != cudaSuccess) return e;
     delta_grad_kernel<DK, DV, BF16><<<blocks, kGradThreads, smem, s>>>(r);
     e = cudaGetLastError();

@@ -561,16 +561,22 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
     uint4 *sfr = reinterpret_cast<uint4 *>(area + 20 * 1024 + 512) + lane;  // [step][hi, (lo)][32]
 
     // V of this lane's places in block p: tokens 16 p + 8 x + 2 q4 + {0, 1}, columns gq, gq + 8
-    float v[2][4];
+    // kept as loaded: a conversion here would wait for the load
+    uint32_t v[2][4];
     auto fetch_v = [&](int c) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int t = c * C + 16 * p + 8 * x + 2 * q4 + (e & 1);
-                v[x][e] = t < len ? load_elem(a.V, (vrow + t) * a.dv + v0 + gq + (e >> 1) * 8, BF16) : 0.f;
+                const size_t at = (vrow + t) * a.dv + v0 + gq + (e >> 1) * 8;
+                v[x][e] = 0;
+                if (t < len)
+                    v[x][e] = BF16 ? (uint32_t)static_cast<const uint16_t *>(a.V)[at]
+                                   : static_cast<const uint32_t *>(a.V)[at];
             }
     };
+    auto v_at = [&](int x, int e) { return __uint_as_float(BF16 ? v[x][e] << 16 : v[x][e]); };
     // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns k0 + 8 nt + 2 q4 + {0, 1}
     const int k0 = p * (DK / 4);
     float S[NT][4];
@@ -653,10 +659,10 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
                     const float4 u = part[32 * (8 * p + 2 * w + x)];
                     o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
                 }
-                X[x][0] = v[x][0] - ck.x * o.x;
-                X[x][1] = v[x][1] - ck.y * o.y;
-                X[x][2] = v[x][2] - ck.x * o.z;
-                X[x][3] = v[x][3] - ck.y * o.w;
+                X[x][0] = v_at(x, 0) - ck.x * o.x;
+                X[x][1] = v_at(x, 1) - ck.y * o.y;
+                X[x][2] = v_at(x, 2) - ck.x * o.z;
+                X[x][3] = v_at(x, 3) - ck.y * o.w;
             }
             if (c + 1 < nchunk) fetch_v(c + 1);
             if (SAVE) {
@@ -824,8 +830,8 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
 template <int DK, bool BF16>
 cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
     constexpr int smem = prep_smem<DK, BF16>();
-    cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<DK, BF16>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once;
+    cudaError_t e = once.allow(delta_prep_kernel<DK, BF16>, smem);
     if (e != cudaSuccess) return e;
     delta_prep_kernel<DK, BF16><<<blocks, kPrepThreads, smem, s>>>(r);
     e = cudaGetLastError();
@@ -841,8 +847,8 @@ cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
     r.stages = (226 * 1024 - wbytes) / stage;
     r.stages = r.stages > 3 ? 3 : r.stages;
     const int smem = r.stages * stage + wbytes;
-    cudaError_t e = cudaFuncSetAttribute(delta_scan_kernel<DK, BF16, MODE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOnce once;
+    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, 227 * 1024 - 1024);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
     delta_scan_kernel<DK, BF16, MODE><<<grid, 128 * r.cgs, smem, s>>>(r);

@@ -16,6 +16,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 namespace ttt {
 namespace delta {
 
@@ -207,6 +209,22 @@ struct ChunkSearch {
         len -= c * C;
         len = len < C ? len : C;
         return len > 0;
+    }
+};
+
+// Lets a kernel take `bytes` of dynamic shared memory, asked of the runtime once
+// per device (the request costs about a microsecond). Two threads may both ask.
+struct SmemOnce {
+    std::atomic<bool> done[64] = {};
+    template <class K>
+    cudaError_t allow(K *kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+        return e;
     }
 };
 
