@@ -739,6 +739,12 @@ class _On:
             t.record_stream(self.side)
         return t
 
+    def like(self, t, dtype):
+        """An uninitialised tensor of t's (contiguous) shape."""
+        if self.side is not None:
+            return self.empty(t.shape, dtype)
+        return self.torch.empty_like(t, dtype=dtype)
+
     def workspace(self, given, need):
         """A workspace of `need` bytes (a given one is checked): its address and size."""
         if given is None:
@@ -798,7 +804,7 @@ def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None
                                                         w0_per_seq, seq_start)
     zt = torch.bfloat16 if z_bf16 else torch.float32
     if Z is None:
-        Z = on.empty((B, H, T, dv), zt)
+        Z = on.like(V, zt)
     else:
         _tensors("delta_fwd", on.index, Z=(Z, (zt,), (B, H, T, dv)))
     W_out = on.empty((N, H, dk, dv), torch.float32) if want_w else None
@@ -824,7 +830,7 @@ def delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out=None, *, w0_per_seq=False, seq_sta
     f32 = torch.float32
     _tensors("delta_bwd", on.index, dZ=(dZ, (f32,), (B, H, T, dv)),
              dW_out=(dW_out, (f32,), (N, H, dk, dv)))
-    grads = {n: on.empty(t.shape, f32) for n, t in
+    grads = {n: on.like(t, f32) for n, t in
              dict(Q=Q, K=K, V=V, eta=eta, g=g, W0=W0).items() if t is not None}
     L = lib()
     ws, nbytes = on.workspace(workspace,
@@ -853,7 +859,7 @@ def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_
         raise ValueError("delta_decode: W must be [slots, H, dk, dv]")
     slots = W.shape[0]
     if Z is None:
-        Z = on.empty((B, H, n, dv), zt)
+        Z = on.like(V, zt)
     else:
         _tensors("delta_decode", on.index, Z=(Z, (zt,), (B, H, n, dv)))
     _tensors("delta_decode", on.index, W=(W, (torch.float32,), (slots, H, dk, dv)),
@@ -912,8 +918,8 @@ def join_fwd(X, Z, gate=None, scale=None, post_gamma=None, post_beta=None, pre_g
     on = _On("join_fwd", X, stream)
     B, H, T, d, flags, code = _join_shapes("join_fwd", on.index, X, Z, gate, scale, post_gamma,
                                            post_beta, pre_gamma, pre_beta, rms, act)
-    R = None if Z is None else on.empty(X.shape, X.dtype)
-    Hn = on.empty(X.shape, X.dtype) if want_h else None
+    R = None if Z is None else on.like(X, X.dtype)
+    Hn = on.like(X, X.dtype) if want_h else None
     on.run("ttt_join_fwd", lib().ttt_join_fwd, X.data_ptr(), _p(Z), _p(gate), _p(scale),
            _p(post_gamma), _p(post_beta), _p(pre_gamma), _p(pre_beta), _p(R), _p(Hn), eps, B, H, T,
            d, code, flags)
@@ -935,7 +941,7 @@ def join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, dR, 
     want = dict(X=R, Z=Z, gate=gate, scale=scale, gamma1=post_gamma, beta1=post_beta)
     if dH is not None:
         want.update(gamma2=pre_gamma, beta2=pre_beta)
-    g = {n: on.empty(t.shape, f32) for n, t in want.items() if t is not None}
+    g = {n: on.like(t, f32) for n, t in want.items() if t is not None}
     L = lib()
     ws, nbytes = on.workspace(workspace, L.ttt_join_bwd_workspace_bytes(B, H, T, d))
     at = lambda n: _p(g.get(n))  # noqa: E731

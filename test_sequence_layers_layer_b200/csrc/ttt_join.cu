@@ -23,81 +23,109 @@
 namespace ttt {
 namespace {
 
-constexpr int kJoinMaxThreads = 512;  // D <= 4096
+// Blocks of up to 128 threads (rows of up to 1024 channels) may take 168 registers a
+// thread and keep the parameters in them; blocks of up to 512 (D <= 4096) have 128.
+constexpr int kJoinThreads = 128, kJoinMaxThreads = 512;
 constexpr int kJoinParams = 5;        // scale, gamma1, beta1, gamma2, beta2
 
-// Eight consecutive elements, 16-byte loads and stores.
+constexpr int V = 8;  // channels of a thread
+
+// Eight consecutive elements as 4-byte words, as loaded (16 bytes at a time) and as floats.
 template <bool BF16>
-__device__ __forceinline__ void load8(float (&x)[8], const void *p, size_t i) {
-    if (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+    static constexpr int N = BF16 ? V / 2 : V;
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const void *p, size_t i) {
+        const char *q = static_cast<const char *>(p) + i * (BF16 ? 2 : 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int j = 0; j < N; j += 4) {
+            const uint4 u = reinterpret_cast<const uint4 *>(q)[j / 4];
+            w[j] = u.x, w[j + 1] = u.y, w[j + 2] = u.z, w[j + 3] = u.w;
         }
-    } else {
-        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = 0;
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t u = w[BF16 ? j / 2 : j];
+            x[j] = __uint_as_float(!BF16 ? u : (j & 1) ? u & 0xFFFF0000u : u << 16);
+        }
+    }
+};
 // Stores x and leaves in x the values as they were stored.
 template <bool BF16>
-__device__ __forceinline__ void store8(void *p, size_t i, float (&x)[8]) {
+__device__ __forceinline__ void store_v(void *p, size_t i, float (&x)[V]) {
     if (BF16) {
-        uint32_t w[4];
+        uint32_t w[V / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < V / 2; ++j) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
             w[j] = *reinterpret_cast<const uint32_t *>(&b);
             x[2 * j] = __uint_as_float(w[j] << 16);
             x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
         }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(p) + i;
+        *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
         float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int j = 0; j < V; j += 4) f[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
     }
 }
-__device__ __forceinline__ void param8(float (&x)[8], const float *p, int i, bool live, float dflt) {
+__device__ __forceinline__ void param_v(float (&x)[V], const float *p, int i, bool live, float dflt) {
     if (p && live) {
-        load8<false>(x, p, i);
+        Raw<false> r;
+        r.load(p, i);
+        r.get(x);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = dflt;
+        for (int j = 0; j < V; ++j) x[j] = dflt;
     }
 }
 
-// Sum over the block; `slots` holds a float per warp. The first barrier lets
-// the readers of the sum before finish with the slots.
-__device__ __forceinline__ float block_sum(float v, float *slots) {
-    v = warp_sum(v);
-    const int nw = blockDim.x >> 5;
-    if (nw == 1) return v;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < nw; ++w) s += slots[w];
-    return s;
-}
-__device__ __forceinline__ float head_sum(float v, int lanes, float *slots) {
-    if (lanes == 0) return block_sum(v, slots);  // one head: the whole row
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-__device__ __forceinline__ float sum8(const float (&x)[8]) {
+// Sums over the block and over a head. Two sets of 16 slots in turn: a thread that
+// writes the sum after next has passed the next one's barrier, behind which this
+// one's slots are read. Slots of warps that are not there stay zero.
+struct Sums {
+    float *slots;  // 32 floats, zeroed before the first use
+    int nw, lanes; // warps; threads of a head (0: one head, the whole row)
+    int turn;
+    __device__ __forceinline__ float block(float v) {
+        v = warp_sum(v);
+        if (nw == 1) return v;
+        float *p = slots + turn;
+        turn ^= 16;
+        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const float4 *q = reinterpret_cast<const float4 *>(p);
+        float4 s = q[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            if (4 * i >= nw) break;
+            const float4 u = q[i];
+            s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+        }
+        return (s.x + s.y) + (s.z + s.w);
+    }
+    __device__ __forceinline__ float head(float v) {
+        if (lanes == 0) return block(v);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        return v;
+    }
+};
+__device__ __forceinline__ float sum_v(const float (&x)[V]) {
     return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
-__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+__device__ __forceinline__ float dot_v(const float (&x)[V], const float (&y)[V]) {
     float s = x[0] * y[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) s = fmaf(x[j], y[j], s);
+    for (int j = 1; j < V; ++j) s = fmaf(x[j], y[j], s);
     return s;
 }
 
@@ -105,52 +133,94 @@ __device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) 
 // over the norm's n channels; a thread without channels holds zeros and
 // passes live = false (its centred values must not count).
 template <class Sum>
-__device__ __forceinline__ float norm8(float (&x)[8], float inv_n, float eps, bool rms, bool live,
+__device__ __forceinline__ float norm_v(float (&x)[V], float inv_n, float eps, bool rms, bool live,
                                        Sum sum) {
     if (!rms) {
-        const float m = sum(sum8(x)) * inv_n;
+        const float m = sum(sum_v(x)) * inv_n;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = live ? x[j] - m : 0.f;
+        for (int j = 0; j < V; ++j) x[j] = live ? x[j] - m : 0.f;
     }
-    // divided, not rsqrtf (2 ulp): one division per row costs nothing here
-    const float i = 1.f / sqrtf(sum(dot8(x, x)) * inv_n + eps);
+    // the fast root and one Newton step: within an ulp of the exact quotient
+    const float q = sum(dot_v(x, x)) * inv_n + eps, y = rsqrtf(q);
+    const float i = y * fmaf(-0.5f * q * y, y, 1.5f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= i;
+    for (int j = 0; j < V; ++j) x[j] *= i;
     return i;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// The fast exponential and reciprocal: off by 2^-22 + |x| 2^-24 and 2^-23 of the value,
+// a tenth of what the sums over a row lose. The exact forms cost four times the
+// instructions, which at 12 bytes a channel bound the forward.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-template <bool BF16, bool ZBF16>
-__global__ void __launch_bounds__(kJoinMaxThreads) join_fwd_kernel(JoinArgs a) {
-    __shared__ float slots[kJoinMaxThreads / 32];
-    const int D = a.H * a.d, c = threadIdx.x * 8;
+// A block's rows are blockIdx.x, + gridDim.x, ...; a row's loads are on their way
+// while the row before it is computed.
+// Batch row and token of a block's rows, one after the other without divisions.
+struct Rows {
+    long long row, end;
+    int b, t, T, db, dt;
+    __device__ __forceinline__ Rows(long long rows, int T_) : row(blockIdx.x), end(rows), T(T_) {
+        b = (int)(blockIdx.x / (unsigned)T);
+        t = (int)(blockIdx.x - (unsigned)b * T);
+        db = (int)(gridDim.x / (unsigned)T);
+        dt = (int)(gridDim.x - (unsigned)db * T);
+    }
+    __device__ __forceinline__ bool live() const { return row < end; }
+    __device__ __forceinline__ void next() {
+        row += gridDim.x;
+        b += db;
+        t += dt;
+        if (t >= T) t -= T, ++b;
+    }
+    // element of a head-major [B][H][T][d] array
+    __device__ __forceinline__ size_t head_major(int H, int h, int d) const {
+        return (((size_t)b * H + h) * T + t) * d;
+    }
+};
+
+template <int NT, bool BF16, bool ZBF16>
+__global__ void __launch_bounds__(NT, 512 / NT) join_fwd_kernel(JoinArgs a) {
+    __shared__ __align__(16) float slots[32];
+    const int D = a.H * a.d, c = threadIdx.x * V;
     const bool live = c < D;
     const int h = c / a.d, cd = c - h * a.d;
-    const int lanes = a.H == 1 ? 0 : a.d >> 3;
+    if (threadIdx.x < 32) slots[threadIdx.x] = 0.f;
+    __syncthreads();
+    Sums sums{slots, (int)(blockDim.x >> 5), a.H == 1 ? 0 : a.d / V, 0};
     const float inv_d = 1.f / (float)a.d, inv_D = 1.f / (float)D;
-    float s[8], g1[8], b1[8], g2[8], b2[8];
-    param8(s, a.scale, c, live, 1.f);
-    param8(g1, a.gamma1, c, live, 1.f);
-    param8(b1, a.beta1, c, live, 0.f);
-    param8(g2, a.gamma2, c, live, 1.f);
-    param8(b2, a.beta2, c, live, 0.f);
-    auto hsum = [&](float v) { return head_sum(v, lanes, slots); };
-    auto rsum = [&](float v) { return block_sum(v, slots); };
+    float s[V], g1[V], b1[V], g2[V], b2[V];
+    param_v(s, a.scale, c, live, 1.f);
+    param_v(g1, a.gamma1, c, live, 1.f);
+    param_v(b1, a.beta1, c, live, 0.f);
+    param_v(g2, a.gamma2, c, live, 1.f);
+    param_v(b2, a.beta2, c, live, 0.f);
+    auto hsum = [&](float v) { return sums.head(v); };
+    auto rsum = [&](float v) { return sums.block(v); };
     const long long rows = (long long)a.B * a.T;
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-        const size_t at = (size_t)row * D + c;
-        float r[8] = {}, z[8] = {}, g[8] = {};
-        if (live) load8<BF16>(r, a.X, at);
+    Raw<BF16> xr, gr;
+    Raw<ZBF16> zr;
+    xr.zero(), gr.zero(), zr.zero();
+    auto fetch = [&](const Rows &at) {
+        if (!live) return;
+        const size_t i = (size_t)at.row * D + c;
+        xr.load(a.X, i);
         if (a.Z) {
-            const long long b = row / a.T, t = row - b * a.T;
-            if (live) {
-                load8<ZBF16>(z, a.Z, ((size_t)(b * a.H + h) * a.T + t) * a.d + cd);
-                if (a.gate) load8<BF16>(g, a.gate, at);
-            }
-            norm8(z, inv_d, a.eps, a.rms, live, hsum);
+            zr.load(a.Z, at.head_major(a.H, h, a.d) + cd);
+            if (a.gate) gr.load(a.gate, i);
+        }
+    };
+    Rows now(rows, a.T), ahead = now;
+    if (ahead.live()) fetch(ahead);
+    for (; now.live(); now.next()) {
+        const size_t at = (size_t)now.row * D + c;
+        float r[V], z[V], g[V];
+        xr.get(r), zr.get(z), gr.get(g);
+        ahead.next();
+        if (ahead.live()) fetch(ahead);
+        if (a.Z) {
+            norm_v(z, inv_d, a.eps, a.rms, live, hsum);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < V; ++j) {
                 float y = s[j] * fmaf(z[j], g1[j], b1[j]);
                 if (a.gate) {
                     const float sg = sigmoid(g[j]);
@@ -158,76 +228,99 @@ __global__ void __launch_bounds__(kJoinMaxThreads) join_fwd_kernel(JoinArgs a) {
                 }
                 r[j] += y;
             }
-            if (live) store8<BF16>(a.R, at, r);
+            if (live) store_v<BF16>(a.R, at, r);
         }
         if (a.Hn) {
             if (!live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = 0.f;
+                for (int j = 0; j < V; ++j) r[j] = 0.f;
             }
-            norm8(r, inv_D, a.eps, a.rms, live, rsum);
+            norm_v(r, inv_D, a.eps, a.rms, live, rsum);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = fmaf(r[j], g2[j], b2[j]);
-            if (live) store8<BF16>(a.Hn, at, r);
+            for (int j = 0; j < V; ++j) r[j] = fmaf(r[j], g2[j], b2[j]);
+            if (live) store_v<BF16>(a.Hn, at, r);
         }
     }
 }
 
-template <bool BF16, bool ZBF16>
-__global__ void __launch_bounds__(kJoinMaxThreads) join_bwd_kernel(JoinBwdArgs a) {
-    __shared__ float slots[kJoinMaxThreads / 32];
-    const int D = a.H * a.d, c = threadIdx.x * 8;
+template <int NT, bool BF16, bool ZBF16>
+__global__ void __launch_bounds__(NT, NT == kJoinThreads ? 3 : 1) join_bwd_kernel(JoinBwdArgs a) {
+    __shared__ __align__(16) float slots[32];
+    const int D = a.H * a.d, c = threadIdx.x * V;
     const bool live = c < D;
     const int h = c / a.d, cd = c - h * a.d;
-    const int lanes = a.H == 1 ? 0 : a.d >> 3;
+    if (threadIdx.x < 32) slots[threadIdx.x] = 0.f;
+    __syncthreads();
+    Sums sums{slots, (int)(blockDim.x >> 5), a.H == 1 ? 0 : a.d / V, 0};
     const float inv_d = 1.f / (float)a.d, inv_D = 1.f / (float)D;
-    float s[8], g1[8], b1[8], g2[8];
-    param8(s, a.scale, c, live, 1.f);
-    param8(g1, a.gamma1, c, live, 1.f);
-    param8(b1, a.beta1, c, live, 0.f);
-    param8(g2, a.gamma2, c, live, 1.f);
-    float acc[kJoinParams][8] = {};
-    auto hsum = [&](float v) { return head_sum(v, lanes, slots); };
-    auto rsum = [&](float v) { return block_sum(v, slots); };
+    constexpr bool KEEP = NT == kJoinThreads;  // else the parameters are read again for each row
+    float ks[V], kg1[V], kb1[V], kg2[V];
+    if (KEEP) {
+        param_v(ks, a.scale, c, live, 1.f);
+        param_v(kg1, a.gamma1, c, live, 1.f);
+        param_v(kb1, a.beta1, c, live, 0.f);
+        param_v(kg2, a.gamma2, c, live, 1.f);
+    }
+    float acc[kJoinParams][V] = {};
+    auto hsum = [&](float v) { return sums.head(v); };
+    auto rsum = [&](float v) { return sums.block(v); };
     const long long rows = (long long)a.B * a.T;
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
-        const size_t at = (size_t)row * D + c;
-        float dx[8] = {};
-        if (a.dR && live) load8<false>(dx, a.dR, at);
+    Raw<BF16> rr, gr;
+    Raw<ZBF16> zr;
+    Raw<false> dr, hr;
+    rr.zero(), gr.zero(), zr.zero(), dr.zero(), hr.zero();
+    auto fetch = [&](const Rows &at) {
+        if (!live) return;
+        const size_t i = (size_t)at.row * D + c;
         if (a.dH) {
-            float r[8] = {}, dy[8] = {};
-            if (live) {
-                load8<BF16>(r, a.R, at);
-                load8<false>(dy, a.dH, at);
-            }
-            const float i = norm8(r, inv_D, a.eps, a.rms, live, rsum);
+            rr.load(a.R, i);
+            hr.load(a.dH, i);
+        }
+        if (a.dR) dr.load(a.dR, i);
+        if (a.Z) {
+            zr.load(a.Z, at.head_major(a.H, h, a.d) + cd);
+            if (a.gate) gr.load(a.gate, i);
+        }
+    };
+    Rows now(rows, a.T), ahead = now;
+    if (ahead.live()) fetch(ahead);
+    for (; now.live(); now.next()) {
+        const size_t at = (size_t)now.row * D + c;
+        float dx[V], z[V], g[V], r[V], dy[V];
+        dr.get(dx), rr.get(r), hr.get(dy), zr.get(z), gr.get(g);
+        ahead.next();
+        if (ahead.live()) fetch(ahead);
+        if (a.dH) {
+            if (!KEEP) param_v(kg2, a.gamma2, c, live, 1.f);
+            const float i = norm_v(r, inv_D, a.eps, a.rms, live, rsum);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < V; ++j) {
                 acc[3][j] = fmaf(dy[j], r[j], acc[3][j]);
                 acc[4][j] += dy[j];
-                dy[j] *= g2[j];
+                dy[j] *= kg2[j];
             }
-            const float m1 = a.rms ? 0.f : rsum(sum8(dy)) * inv_D;
-            const float m2 = rsum(dot8(dy, r)) * inv_D;
+            const float m1 = a.rms ? 0.f : rsum(sum_v(dy)) * inv_D;
+            const float m2 = rsum(dot_v(dy, r)) * inv_D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dx[j] += i * (dy[j] - m1 - r[j] * m2);
+            for (int j = 0; j < V; ++j) dx[j] += i * (dy[j] - m1 - r[j] * m2);
         }
-        if (live) store8<false>(a.dX, at, dx);
+        if (live) store_v<false>(a.dX, at, dx);
         if (a.Z) {
-            const long long b = row / a.T, t = row - b * a.T;
-            const size_t zat = ((size_t)(b * a.H + h) * a.T + t) * a.d + cd;
-            float z[8] = {}, g[8] = {}, dg[8];
-            if (live) {
-                load8<ZBF16>(z, a.Z, zat);
-                if (a.gate) load8<BF16>(g, a.gate, at);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dx[j] = 0.f;
+            const size_t zat = now.head_major(a.H, h, a.d) + cd;
+            float dg[V];
+            if (!KEEP) {
+                param_v(ks, a.scale, c, live, 1.f);
+                param_v(kg1, a.gamma1, c, live, 1.f);
+                param_v(kb1, a.beta1, c, live, 0.f);
             }
-            const float i = norm8(z, inv_d, a.eps, a.rms, live, hsum);
+            if (!live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = fmaf(z[j], g1[j], b1[j]);
+                for (int j = 0; j < V; ++j) dx[j] = 0.f;
+            }
+            const float i = norm_v(z, inv_d, a.eps, a.rms, live, hsum);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float n = fmaf(z[j], kg1[j], kb1[j]);
                 float act = 1.f, dact = 0.f;
                 if (a.gate) {
                     const float sg = sigmoid(g[j]);
@@ -235,46 +328,45 @@ __global__ void __launch_bounds__(kJoinMaxThreads) join_bwd_kernel(JoinBwdArgs a
                     dact = a.silu ? sg * fmaf(g[j], 1.f - sg, 1.f) : sg * (1.f - sg);
                 }
                 acc[0][j] = fmaf(dx[j] * act, n, acc[0][j]);
-                const float ds = dx[j] * s[j];
+                const float ds = dx[j] * ks[j];
                 dg[j] = ds * n * dact;
                 const float dn = ds * act;
                 acc[1][j] = fmaf(dn, z[j], acc[1][j]);
                 acc[2][j] += dn;
-                dx[j] = dn * g1[j];
+                dx[j] = dn * kg1[j];
             }
-            if (a.gate && live) store8<false>(a.dGate, at, dg);
-            const float m1 = a.rms ? 0.f : hsum(sum8(dx)) * inv_d;
-            const float m2 = hsum(dot8(dx, z)) * inv_d;
+            if (a.gate && live) store_v<false>(a.dGate, at, dg);
+            const float m1 = a.rms ? 0.f : hsum(sum_v(dx)) * inv_d;
+            const float m2 = hsum(dot_v(dx, z)) * inv_d;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dx[j] = i * (dx[j] - m1 - z[j] * m2);
-            if (live) store8<false>(a.dZ, zat, dx);
+            for (int j = 0; j < V; ++j) dx[j] = i * (dx[j] - m1 - z[j] * m2);
+            if (live) store_v<false>(a.dZ, zat, dx);
         }
     }
     if (live) {
 #pragma unroll
         for (int p = 0; p < kJoinParams; ++p)
-            store8<false>(a.partials, ((size_t)blockIdx.x * kJoinParams + p) * D + c, acc[p]);
+            store_v<false>(a.partials, ((size_t)blockIdx.x * kJoinParams + p) * D + c, acc[p]);
     }
 }
 
-// Adds the blocks' partial rows. Block: 32 channels x 8 threads, thread row y
-// takes the partial rows y, y + 8, ... in order; the eight sums are added in order.
+// Adds the blocks' partial rows. Block: 8 channels x 32 threads, thread row y
+// takes the partial rows y, y + 32, ... in order; the 32 sums are added in order.
 __global__ void __launch_bounds__(256) join_params_kernel(const float *partials, int nblocks, int D,
                                                           float *out0, float *out1, float *out2,
                                                           float *out3, float *out4) {
-    __shared__ float sums[256];
-    float *const outs[kJoinParams] = {out0, out1, out2, out3, out4};
-    float *out = outs[blockIdx.y];
+    __shared__ float sums[32][9];
+    const int p = blockIdx.y;
+    float *out = p == 0 ? out0 : p == 1 ? out1 : p == 2 ? out2 : p == 3 ? out3 : out4;
     if (!out) return;
-    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
     float v = 0.f;
-    if (c < D)
-        for (int i = y; i < nblocks; i += 8)
-            v += partials[((size_t)i * kJoinParams + blockIdx.y) * D + c];
-    sums[threadIdx.x] = v;
+#pragma unroll 4
+    for (int i = y; i < nblocks; i += 32) v += partials[((size_t)i * kJoinParams + p) * D + c];
+    sums[y][x] = v;
     __syncthreads();
-    if (y == 0 && c < D) {
-        for (int i = 1; i < 8; ++i) v += sums[i * 32 + lane];
+    if (y == 0) {
+        for (int i = 1; i < 32; ++i) v += sums[i][x];
         out[c] = v;
     }
 }
@@ -291,34 +383,51 @@ bool join_supported(int H, int d) {
 }
 
 namespace {
-int join_threads(int H, int d) { return (H * d / 8 + 31) / 32 * 32; }
-// Blocks of the persistent backward: as many as are resident at 128 registers a
-// thread (its accumulators), at most one per row. The count depends on the
-// shape alone, so the order of the parameter sums is the same in every call.
-int join_bwd_blocks(long long rows, int H, int d) {
-    int per_sm = 512 / join_threads(H, d);
+int join_threads(int H, int d) { return (H * d / V + 31) / 32 * 32; }
+// Blocks of the persistent kernels: as many as are resident at 128 registers a
+// thread (the backward's narrow blocks: three), at most one per row. The
+// count depends on the shape alone, so the order of the parameter sums is the
+// same in every call.
+int join_blocks(long long rows, int nt, bool bwd) {
+    int per_sm = 512 / nt;
     if (per_sm > 8) per_sm = 8;
+    if (bwd && nt > 64 && nt <= kJoinThreads) per_sm = 3;
     const long long n = 148LL * (per_sm < 1 ? 1 : per_sm);
     return (int)(rows < n ? rows : n);
+}
+
+template <int NT>
+void run_fwd(const JoinArgs &a, unsigned grid, int nt, cudaStream_t s) {
+    if (a.bf16) {
+        if (a.z_bf16) join_fwd_kernel<NT, true, true><<<grid, nt, 0, s>>>(a);
+        else join_fwd_kernel<NT, true, false><<<grid, nt, 0, s>>>(a);
+    } else {
+        if (a.z_bf16) join_fwd_kernel<NT, false, true><<<grid, nt, 0, s>>>(a);
+        else join_fwd_kernel<NT, false, false><<<grid, nt, 0, s>>>(a);
+    }
+}
+template <int NT>
+void run_bwd(const JoinBwdArgs &a, unsigned grid, int nt, cudaStream_t s) {
+    if (a.bf16) {
+        if (a.z_bf16) join_bwd_kernel<NT, true, true><<<grid, nt, 0, s>>>(a);
+        else join_bwd_kernel<NT, true, false><<<grid, nt, 0, s>>>(a);
+    } else {
+        if (a.z_bf16) join_bwd_kernel<NT, false, true><<<grid, nt, 0, s>>>(a);
+        else join_bwd_kernel<NT, false, false><<<grid, nt, 0, s>>>(a);
+    }
 }
 }  // namespace
 
 size_t join_bwd_workspace_bytes(int B, int H, int T, int d) {
-    return sizeof(float) * kJoinParams * (size_t)H * d * join_bwd_blocks((long long)B * T, H, d);
+    return sizeof(float) * kJoinParams * (size_t)H * d * join_blocks((long long)B * T, join_threads(H, d), true);
 }
 
 cudaError_t launch_join_fwd(const JoinArgs &a, cudaStream_t s) {
     const int nt = join_threads(a.H, a.d);
     const long long rows = (long long)a.B * a.T;
-    const long long most = 148LL * (2048 / nt);
-    const unsigned grid = (unsigned)(rows < most ? rows : most);
-    if (a.bf16) {
-        if (a.z_bf16) join_fwd_kernel<true, true><<<grid, nt, 0, s>>>(a);
-        else join_fwd_kernel<true, false><<<grid, nt, 0, s>>>(a);
-    } else {
-        if (a.z_bf16) join_fwd_kernel<false, true><<<grid, nt, 0, s>>>(a);
-        else join_fwd_kernel<false, false><<<grid, nt, 0, s>>>(a);
-    }
+    const int grid = join_blocks(rows, nt, false);
+    if (nt <= kJoinThreads) run_fwd<kJoinThreads>(a, grid, nt, s);
+    else run_fwd<kJoinMaxThreads>(a, grid, nt, s);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
@@ -326,19 +435,14 @@ cudaError_t launch_join_fwd(const JoinArgs &a, cudaStream_t s) {
 
 cudaError_t launch_join_bwd(const JoinBwdArgs &a, cudaStream_t s) {
     const int nt = join_threads(a.H, a.d), D = a.H * a.d;
-    const int grid = join_bwd_blocks((long long)a.B * a.T, a.H, a.d);
-    if (a.bf16) {
-        if (a.z_bf16) join_bwd_kernel<true, true><<<grid, nt, 0, s>>>(a);
-        else join_bwd_kernel<true, false><<<grid, nt, 0, s>>>(a);
-    } else {
-        if (a.z_bf16) join_bwd_kernel<false, true><<<grid, nt, 0, s>>>(a);
-        else join_bwd_kernel<false, false><<<grid, nt, 0, s>>>(a);
-    }
+    const int grid = join_blocks((long long)a.B * a.T, nt, true);
+    if (nt <= kJoinThreads) run_bwd<kJoinThreads>(a, grid, nt, s);
+    else run_bwd<kJoinMaxThreads>(a, grid, nt, s);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launch(s);
     if (!a.dscale && !a.dgamma1 && !a.dbeta1 && !a.dgamma2 && !a.dbeta2) return e;
-    join_params_kernel<<<dim3((D + 31) / 32, kJoinParams), 256, 0, s>>>(
+    join_params_kernel<<<dim3(D / 8, kJoinParams), 256, 0, s>>>(
         a.partials, grid, D, a.dscale, a.dgamma1, a.dbeta1, a.dgamma2, a.dbeta2);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
