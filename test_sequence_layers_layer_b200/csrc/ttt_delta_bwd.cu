@@ -30,38 +30,43 @@ struct RevArgs {
     const float *dZ, *dW_out;
     float *dV, *dW0;               // dW0 [N][H][DK][dv] or NULL
     const int *seq_start;
-    int B, Hk, H, T, dv, cgs, stages;
+    int B, Hk, H, T, dv, stages, zstages;
     Images im;
     float *saveO;                  // [slot][H][DK][dv]
     int *status;
 };
 
+// Bytes of a stage of the chain's ring (K, H, vectors) and of the helpers' (Q, M, vectors).
 template <int DK, bool BF16>
-constexpr int rev_stage_bytes() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 + 2 * kImg + kScanVecBytes;
-}
-// A column group's area: shares of dX [to][from][2 tiles], terms of dX [4 blocks][hi, lo],
-// of dZ [4 blocks][for M: hi, lo, for Q: hi, lo], 1 / their scales.
-constexpr int kRevGroupBytes = 16 * 1024 + 4096 + 8192 + 1024;
+constexpr int rev_stage_bytes() { return ((BF16 ? 1 : 2) + 2) * C * DK * 2 + kHalfVecBytes; }
+template <int DK, bool BF16>
+constexpr int rev_zstage_bytes() { return (BF16 ? 1 : 2) * C * DK * 2 + 2 * kImg + kHalfVecBytes; }
+// Shares of dX [to 4][from 4][2 tiles], the terms of dX [4 blocks][hi, lo] and of dZ
+// [4 blocks][for M, for Q][hi, lo] with 1 / their scales; twice, for the chunks in turn,
+// what the helpers leave: (M^T dZ)^T [4 blocks][2 tiles], (c D Q)^T dZ transposed [DK / 8 tiles].
+template <int DK>
+constexpr int rev_turn_bytes() { return 4096 + DK / 8 * 512; }
+template <int DK>
+constexpr int rev_group_bytes() { return 16 * 1024 + 4096 + 8192 + 768 + 2 * rev_turn_bytes<DK>(); }
 
 // The mirror of the forward scan: four warps own 16 columns of Om, as the rows of
-// Om^T in registers, a quarter of DK each. Before the first meeting each hands
-// out its quarter's share of Om^T H^T, and the operand forms of dZ of its block of
-// 16 tokens; then warp p puts dX of block p together (with dZ^T M over the blocks from
-// p on), and after the second meeting each updates its quarter of Om.
+// Om^T in registers, a quarter of DK each. Before the first meeting each hands out its
+// quarter's share of Om^T H^T; warp p puts dX of block p together, and after the second
+// meeting each updates its quarter of Om. What dZ adds does not depend on Om: four
+// helper warps form M^T dZ (a block of tokens each) and (c D Q)^T dZ (a quarter of DK
+// each), up to two chunks ahead. Two more warps fill the rings of stages.
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_rev_kernel(RevArgs a) {
+__global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
     extern __shared__ __align__(1024) char ssm[];
-    __shared__ uint64_t full[4], empty[4];
+    __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4], zready[2], zfree[2];
     __shared__ int abort_flag;
-    constexpr int STAGE = rev_stage_bytes<DK, BF16>();
+    constexpr int STAGE = rev_stage_bytes<DK, BF16>(), ZSTAGE = rev_zstage_bytes<DK, BF16>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
     constexpr int NT = DK / 32, KK = DK / 64;
-    constexpr int oH = 2 * KALL, oM = oH + 2 * KIMG;
-    const int groups = a.dv / (16 * a.cgs);
+    const int groups = a.dv / 16;
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, lane = tid & 31, cg = tid >> 7, p = (tid >> 5) & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = warp & 3;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -71,203 +76,145 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_rev_kernel(RevA
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4 * a.cgs);
+            mbar_init(&empty[s], 4);
+            mbar_init(&zfull[s], 1);
+            mbar_init(&zempty[s], 4);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&zready[t], 4);
+            mbar_init(&zfree[t], 4);
         }
         fence_mbar_init();
     }
     __syncthreads();
 
-    // step i works on chunk nchunk - 1 - i
-    auto fill = [&](int i) {
-        const int s = i % a.stages, c = nchunk - 1 - i;
-        if (i >= a.stages &&
-            !mbar_wait(&empty[s], ((i / a.stages) & 1) ^ 1, abort, a.status, kScanStatus))
-            return;
-        char *d = ssm + s * STAGE;
-        const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
-        mbar_arrive_expect_tx(&full[s], STAGE);
-        bulk_load(d, a.im.K + ks * KALL, KALL, &full[s]);
-        bulk_load(d + KALL, a.im.Q + ks * KALL, KALL, &full[s]);
-        bulk_load(d + oH, a.im.H + hs * 2 * KIMG, 2 * KIMG, &full[s]);
-        bulk_load(d + oM, a.im.M + hs * 2 * kImg, 2 * kImg, &full[s]);
-        bulk_load(d + STAGE - kScanVecBytes, a.im.vec + hs * kVecBytes, kScanVecBytes, &full[s]);
-    };
-    if (tid == 0)
-        for (int i = 0; i < nchunk && i < a.stages - 1; ++i) fill(i);
-
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = (grp * a.cgs + cg) * 16;
+    const int v0 = grp * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *area = ssm + a.stages * STAGE + cg * kRevGroupBytes;
-    float4 *part = reinterpret_cast<float4 *>(area) + lane;                // [to][from][tile][32]
-    uint4 *xfr = reinterpret_cast<uint4 *>(area + 16 * 1024) + lane;       // [block][hi, lo][32]
-    uint4 *zfr = reinterpret_cast<uint4 *>(area + 20 * 1024) + lane;       // [block][M hi, lo, Q hi, lo][32]
-    float *iXs = reinterpret_cast<float *>(area + 28 * 1024), *iZm = iXs + 64, *iZq = iZm + 64;
-
-    // dZ of this lane's places in block p
-    float z[2][4];
-    auto fetch_z = [&](int c) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = c * C + 16 * p + 8 * x + 2 * q4 + (e & 1);
-                z[x][e] = t < len ? a.dZ[(vrow + t) * a.dv + v0 + gq + (e >> 1) * 8] : 0.f;
-            }
+    char *zst = ssm + a.stages * STAGE, *area = zst + a.zstages * ZSTAGE;
+    auto wait = [&](uint64_t *bar, int parity) {
+        return mbar_wait_warp(bar, parity, abort, a.status, kScanStatus);
     };
-    const int k0 = p * (DK / 4);
-    float S[NT][4];
-    const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
-    const float *w0 = a.dW_out ? a.dW_out + ((size_t)n * a.H + h) * state + mine : nullptr;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
-    if (nchunk > 0) fetch_z(nchunk - 1);
+    uint4 *const zfr = reinterpret_cast<uint4 *>(area + 20 * 1024) + lane;  // [block][M hi, lo, Q hi, lo][32]
+    float *const iXs = reinterpret_cast<float *>(area + 28 * 1024), *const iZm = iXs + 64, *const iZq = iZm + 64;
+    auto turn_at = [&](int turn) { return area + 28 * 1024 + 768 + turn * rev_turn_bytes<DK>(); };
 
-    for (int i = 0; i < nchunk; ++i) {
-        const int s = i % a.stages, c = nchunk - 1 - i;
-        if (tid == 0 && i + a.stages - 1 < nchunk) fill(i + a.stages - 1);
-        const bool ok = mbar_wait_warp(&full[s], (i / a.stages) & 1, abort, a.status, kScanStatus);
-        const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
-        const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
-        if (ok) {
-            float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
+    // step i works on chunk nchunk - 1 - i
+    if (warp >= 8) {  // ------------------------------------------------ the rings
+        auto chain_copy = [&](int i, int s, uint64_t *bar) {
+            char *d = ssm + s * STAGE;
+            const size_t c = slot0 + nchunk - 1 - i, ks = c * a.Hk + hk, hs = c * a.H + h;
+            mbar_arrive_expect_tx(bar, STAGE);
+            bulk_load(d, a.im.H + hs * 2 * KIMG, 2 * KIMG, bar);
+            bulk_load(d + 2 * KIMG, a.im.K + ks * KALL, KALL, bar);
+            bulk_load(d + STAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes, kHalfVecBytes, bar);
+        };
+        auto z_copy = [&](int i, int s, uint64_t *bar) {
+            char *d = zst + s * ZSTAGE;
+            const size_t c = slot0 + nchunk - 1 - i, ks = c * a.Hk + hk, hs = c * a.H + h;
+            mbar_arrive_expect_tx(bar, ZSTAGE);
+            bulk_load(d, a.im.Q + ks * KALL, KALL, bar);
+            bulk_load(d + KALL, a.im.M + hs * 2 * kImg, 2 * kImg, bar);
+            bulk_load(d + ZSTAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes + kHalfVecBytes,
+                      kHalfVecBytes, bar);
+        };
+        if (lane == 0) {
+            if (warp == 8) {
+                Filler<decltype(chain_copy)> f(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
+                while (f.filled < nchunk && f.next()) {
+                }
+                if (*abort) f.drain();
+            } else {
+                Filler<decltype(z_copy)> f(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
+                while (f.filled < nchunk && f.next()) {
+                }
+                if (*abort) f.drain();
+            }
+        }
+        return;
+    }
+    if (warp >= 4) {  // ------------------------------------------------ dZ's parts
+        // dZ of this lane's places in block p
+        float z[2][4];
+        const size_t zlane = (vrow + 16 * p + 2 * q4) * a.dv + v0 + gq;
+        auto fetch_z = [&](int c) {
+            const size_t at = zlane + (size_t)c * C * a.dv;
+            const int t = c * C + 16 * p + 2 * q4;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
-            // Om^T H^T over this warp's quarter of DK
-            float X[8][4] = {}, sS[2], iS[2];
-            row_scales<NT>(S, sS, iS);
+                    z[x][e] = t + 8 * x + (e & 1) < len
+                                  ? a.dZ[at + (8 * x + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
+        };
+        if (nchunk > 0) fetch_z(nchunk - 1);
+        Ring ring(a.zstages);
+        for (int i = 0; i < nchunk; ++i, ring.next()) {
+            const int turn = i & 1, c = nchunk - 1 - i;
+            const uint32_t uQ = smem_u32(zst + ring.s * ZSTAGE), uM = uQ + KALL;
+            // the enum's order, counted from kVq on
+            const float *vec = reinterpret_cast<const float *>(zst + (ring.s + 1) * ZSTAGE - kHalfVecBytes) - kVq * C;
+            float4 *zm = reinterpret_cast<float4 *>(turn_at(turn)) + lane;  // [block][tile][32]
+            float4 *uq = zm + 256;                                         // [DK / 8][32]
+            bool ok = wait(&zfull[ring.s], ring.ph);
+            if (i >= 2) ok = ok && wait(&zfree[turn], ((i >> 1) & 1) ^ 1);
+            if (ok) {
+                // dZ of block p as an operand for M (M's row scales in it) and for c D Q
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                uint32_t hi[4], lo[4], bb[4][4];
-                a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+                for (int y = 0; y < 2; ++y) {
+                    float A[2][4], sA[2], iA[2];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int np = 0; np < 4; ++np) load_b(bb[np], uH, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int np = 0; np < 4; ++np)
-                    load_b(bb[np], uH + KIMG, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-                part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
-                    iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
-            // dZ of block p as an operand for M (M's row scales in it) and for c D Q
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float A[2][4], sA[2], iA[2];
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float2 f = *reinterpret_cast<const float2 *>(
-                        vec + (y ? kVq : kVm) * C + 16 * p + 8 * x + 2 * q4);
-                    A[x][0] = z[x][0] * f.x, A[x][1] = z[x][1] * f.y;
-                    A[x][2] = z[x][2] * f.x, A[x][3] = z[x][3] * f.y;
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 f = *reinterpret_cast<const float2 *>(
+                            vec + (y ? kVq : kVm) * C + 16 * p + 8 * x + 2 * q4);
+                        A[x][0] = z[x][0] * f.x, A[x][1] = z[x][1] * f.y;
+                        A[x][2] = z[x][2] * f.x, A[x][3] = z[x][3] * f.y;
+                    }
+                    row_scales<2>(A, sA, iA);
+                    a_terms(A[0], A[1], sA, hi, lo);
+                    zfr[32 * (4 * p + 2 * y)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    zfr[32 * (4 * p + 2 * y + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    float *q = y ? iZq : iZm;
+                    if (q4 == 0) q[16 * p + gq] = iA[0], q[16 * p + gq + 8] = iA[1];
                 }
-                row_scales<2>(A, sA, iA);
-                a_terms(A[0], A[1], sA, hi, lo);
-                zfr[32 * (4 * p + 2 * y)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                zfr[32 * (4 * p + 2 * y + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                float *q = y ? iZq : iZm;
-                if (q4 == 0) q[16 * p + gq] = iA[0], q[16 * p + gq + 8] = iA[1];
+                if (i + 1 < nchunk) fetch_z(c - 1);
             }
-        }
-        // the first meeting; all leave together when a wait has run out
-        if (named_bar_or(1 + cg, 128, !ok)) {
-            if (tid == 0)
-                for (int j = i; j < i + a.stages && j < nchunk; ++j)
-                    mbar_drain(&full[j % a.stages], (j / a.stages) & 1);
-            return;
-        }
-        if (i + 1 < nchunk) fetch_z(c - 1);
-        // dX of block p
-        {
-            float X[2][4];
-            const float iH = vec[kVs * C + 1 + p];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float4 o = part[32 * (8 * p + x)];
-#pragma unroll
-                for (int w = 1; w < 4; ++w) {
-                    const float4 u = part[32 * (8 * p + 2 * w + x)];
-                    o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
-                }
-                X[x][0] = iH * o.x, X[x][1] = iH * o.y, X[x][2] = iH * o.z, X[x][3] = iH * o.w;
-            }
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-                if (ii < p) continue;  // M_ij is zero for i < j; the same for the whole warp
-                const uint4 fh = zfr[32 * (4 * ii)], fl = zfr[32 * (4 * ii + 1)];
-                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
-                const float i0 = iZm[16 * ii + gq], i1 = iZm[16 * ii + gq + 8];
-                float d[2][4] = {};
-                uint32_t bh[4], bl[4];
-                load_bt(bh, uM, 16 * ii, 16 * p, lane);
-                load_bt(bl, uM + kImg, 16 * ii, 16 * p, lane);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mma_f16(d[x], hi, bh[2 * x], bh[2 * x + 1]);
-                    mma_f16(d[x], lo, bh[2 * x], bh[2 * x + 1]);
-                    mma_f16(d[x], hi, bl[2 * x], bl[2 * x + 1]);
-                    X[x][0] = fmaf(i0, d[x][0], X[x][0]);
-                    X[x][1] = fmaf(i0, d[x][1], X[x][1]);
-                    X[x][2] = fmaf(i1, d[x][2], X[x][2]);
-                    X[x][3] = fmaf(i1, d[x][3], X[x][3]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = c * C + 16 * p + 8 * x + 2 * q4;
-                float *w = a.dV + (vrow + t) * a.dv + v0 + gq;
-                if (t < len) w[0] = X[x][0], w[8] = X[x][2];
-                if (t + 1 < len) w[a.dv] = X[x][1], w[a.dv + 8] = X[x][3];
-                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
-                X[x][0] *= -ck.x, X[x][1] *= -ck.y, X[x][2] *= -ck.x, X[x][3] *= -ck.y;
-            }
-            float sX[2], iX[2];
-            uint32_t hi[4], lo[4];
-            row_scales<2>(X, sX, iX);
-            a_terms(X[0], X[1], sX, hi, lo);
-            xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
-        }
-        // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K); dZ's part before the meeting
-        const float gam = vec[kVs * C];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            if (y == 1) named_bar(1 + cg, 128);  // the second meeting
+            if (named_bar_or(2, 128, !ok)) return;
+            float D[2][4] = {}, Q[NT][4] = {};
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
-                const uint4 fh = y ? xfr[32 * (2 * jj)] : zfr[32 * (4 * jj + 2)];
-                const uint4 fl = y ? xfr[32 * (2 * jj + 1)] : zfr[32 * (4 * jj + 3)];
-                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
-                const float *q = y ? iXs : iZq;
-                const float i0 = q[16 * jj + gq], i1 = q[16 * jj + gq + 8];
-                const uint32_t img = y ? uK : uQ;
-                float U[NT][4] = {};
-                uint32_t bb[KK][4];
+                if (jj >= p) {  // (M^T dZ)^T of block p: M_ij is zero for i < j
+                    const uint4 fh = zfr[32 * (4 * jj)], fl = zfr[32 * (4 * jj + 1)];
+                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                    const float i0 = iZm[16 * jj + gq], i1 = iZm[16 * jj + gq + 8];
+                    uint32_t bh[4], bl[4];
+                    float d[2][4] = {}, e2[2][4] = {};
+                    load_bt(bh, uM, 16 * jj, 16 * p, lane);
+                    load_bt(bl, uM + kImg, 16 * jj, 16 * p, lane);
 #pragma unroll
-                for (int np = 0; np < KK; ++np) load_bt(bb[np], img, 16 * jj, k0 + 16 * np, lane);
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(d[x], hi, bh[2 * x], bh[2 * x + 1]);
+                        mma_f16(e2[x], lo, bh[2 * x], bh[2 * x + 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) mma_f16(e2[x], hi, bl[2 * x], bl[2 * x + 1]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            D[x][e] = fmaf(e < 2 ? i0 : i1, d[x][e] + e2[x][e], D[x][e]);
+                }
+                // dZ^T (c D Q) of quarter p of DK
+                const uint4 fh = zfr[32 * (4 * jj + 2)], fl = zfr[32 * (4 * jj + 3)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float i0 = iZq[16 * jj + gq], i1 = iZq[16 * jj + gq + 8];
+                uint32_t bb[KK][4];
+                float U[NT][4] = {};
+#pragma unroll
+                for (int np = 0; np < KK; ++np) load_bt(bb[np], uQ, 16 * jj, p * (DK / 4) + 16 * np, lane);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     mma_f16(U[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
@@ -277,22 +224,180 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_rev_kernel(RevA
                 if (!BF16) {
 #pragma unroll
                     for (int np = 0; np < KK; ++np)
-                        load_bt(bb[np], img + KIMG, 16 * jj, k0 + 16 * np, lane);
+                        load_bt(bb[np], uQ + KIMG, 16 * jj, p * (DK / 4) + 16 * np, lane);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma_f16(U[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    S[nt][0] = fmaf(i0, U[nt][0], S[nt][0]);
-                    S[nt][1] = fmaf(i0, U[nt][1], S[nt][1]);
-                    S[nt][2] = fmaf(i1, U[nt][2], S[nt][2]);
-                    S[nt][3] = fmaf(i1, U[nt][3], S[nt][3]);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        Q[nt][e] = fmaf(e < 2 ? i0 : i1, U[nt][e], Q[nt][e]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) zm[32 * (2 * p + x)] = make_float4(D[x][0], D[x][1], D[x][2], D[x][3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                uq[32 * (p * NT + nt)] = make_float4(Q[nt][0], Q[nt][1], Q[nt][2], Q[nt][3]);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&zready[turn]);
+                mbar_arrive(&zempty[ring.s]);
+            }
+            named_bar(2, 128);  // dZ's terms are read
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------- the chain
+    float4 *part = reinterpret_cast<float4 *>(area) + lane;           // [to][from][tile][32]
+    uint4 *xfr = reinterpret_cast<uint4 *>(area + 16 * 1024) + lane;  // [block][hi, lo][32]
+    const int k0 = p * (DK / 4);
+    float S[NT][4];
+    const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
+    const float *w0 = a.dW_out ? a.dW_out + ((size_t)n * a.H + h) * state + mine : nullptr;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
+
+    Ring ring(a.stages);
+    for (int i = 0; i < nchunk; ++i, ring.next()) {
+        const int turn = i & 1, c = nchunk - 1 - i;
+        const uint32_t uH = smem_u32(ssm + ring.s * STAGE), uK = uH + 2 * KIMG;
+        const float *vec = reinterpret_cast<const float *>(ssm + (ring.s + 1) * STAGE - kHalfVecBytes);
+        const float4 *zm = reinterpret_cast<const float4 *>(turn_at(turn)) + lane, *uq = zm + 256;
+        bool ok = wait(&full[ring.s], ring.ph);
+        // Om^T H^T over this warp's quarter of DK
+        if (ok) {
+            float X[8][4] = {}, sS[2], iS[2];
+            uint32_t bh[4][4], bl[4][4];
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                load_b(bh[np], uH, 16 * np, k0, lane);
+                load_b(bl[np], uH + KIMG, 16 * np, k0, lane);
+            }
+            row_scales<NT>(S, sS, iS);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                uint32_t hi[4], lo[4];
+                a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], lo, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+                if (kk + 1 < KK)
+#pragma unroll
+                    for (int np = 0; np < 4; ++np) load_b(bh[np], uH, 16 * np, k0 + 16 * kk + 16, lane);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bl[nt >> 1][2 * (nt & 1)], bl[nt >> 1][2 * (nt & 1) + 1]);
+                if (kk + 1 < KK)
+#pragma unroll
+                    for (int np = 0; np < 4; ++np)
+                        load_b(bl[np], uH + KIMG, 16 * np, k0 + 16 * kk + 16, lane);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+                part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
+                    iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
+            ok = wait(&zready[turn], (i >> 1) & 1);
+        }
+        // the first meeting; all leave together when a wait has run out
+        if (named_bar_or(1, 128, !ok)) return;
+        // dX of block p
+        float X[2][4];
+        {
+            const float iH = vec[kVs * C + 1 + p];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 o0 = part[32 * (8 * p + x)], o1 = part[32 * (8 * p + 2 + x)],
+                             o2 = part[32 * (8 * p + 4 + x)], o3 = part[32 * (8 * p + 6 + x)];
+                const float4 m = zm[32 * (2 * p + x)];
+                X[x][0] = fmaf(iH, (o0.x + o1.x) + (o2.x + o3.x), m.x);
+                X[x][1] = fmaf(iH, (o0.y + o1.y) + (o2.y + o3.y), m.y);
+                X[x][2] = fmaf(iH, (o0.z + o1.z) + (o2.z + o3.z), m.z);
+                X[x][3] = fmaf(iH, (o0.w + o1.w) + (o2.w + o3.w), m.w);
+            }
+            float A[2][4], sX[2], iX[2];
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
+                A[x][0] = -ck.x * X[x][0], A[x][1] = -ck.y * X[x][1];
+                A[x][2] = -ck.x * X[x][2], A[x][3] = -ck.y * X[x][3];
+            }
+            row_scales<2>(A, sX, iX);
+            a_terms(A[0], A[1], sX, hi, lo);
+            xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
+        }
+        // in the shadow of the meeting: what goes out, and all that does not wait for X
+        uint32_t bk[4][KK][4];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int np = 0; np < KK; ++np) load_bt(bk[jj][np], uK, 16 * jj, k0 + 16 * np, lane);
+        const float gam = vec[kVs * C];
+        float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+            const float4 u = uq[32 * (p * NT + nt)];
+            S[nt][0] = fmaf(gam, S[nt][0], u.x), S[nt][1] = fmaf(gam, S[nt][1], u.y);
+            S[nt][2] = fmaf(gam, S[nt][2], u.z), S[nt][3] = fmaf(gam, S[nt][3], u.w);
+        }
+        named_bar(1, 128);  // the second meeting; zm and uq are read
+
+        // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+            const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+            const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
+            float U[NT][4] = {};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(U[nt], hi, bk[jj][nt >> 1][2 * (nt & 1)], bk[jj][nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(U[nt], lo, bk[jj][nt >> 1][2 * (nt & 1)], bk[jj][nt >> 1][2 * (nt & 1) + 1]);
+            if (!BF16) {
+                uint32_t bb[KK][4];
+#pragma unroll
+                for (int np = 0; np < KK; ++np) load_bt(bb[np], uK + KIMG, 16 * jj, k0 + 16 * np, lane);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                S[nt][0] = fmaf(i0, U[nt][0], S[nt][0]);
+                S[nt][1] = fmaf(i0, U[nt][1], S[nt][1]);
+                S[nt][2] = fmaf(i1, U[nt][2], S[nt][2]);
+                S[nt][3] = fmaf(i1, U[nt][3], S[nt][3]);
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) {
+            mbar_arrive(&zfree[turn]);
+            mbar_arrive(&empty[ring.s]);
+        }
+        // dV behind the arrivals, which would wait for its stores
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t = c * C + 16 * p + 8 * x + 2 * q4;
+            float *d = a.dV + (vrow + t) * a.dv + v0 + gq;
+            if (t < len) d[0] = X[x][0], d[8] = X[x][2];
+            if (t + 1 < len) d[a.dv] = X[x][1], d[a.dv + 8] = X[x][3];
+        }
     }
 
     if (a.dW0) {
@@ -921,19 +1026,17 @@ BwdPlan bwd_plan(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed
 
 template <int DK, bool BF16>
 cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
-    r.cgs = scan_groups((long long)N * r.H, DK, r.dv);
-    constexpr int stage = rev_stage_bytes<DK, BF16>();
-    // two stages if that can be, so that the next chunk is loaded during this one
-    while (r.cgs > 1 && 2 * stage + r.cgs * kRevGroupBytes > 226 * 1024) r.cgs /= 2;
-    const int wbytes = r.cgs * kRevGroupBytes;
-    r.stages = (226 * 1024 - wbytes) / stage;
-    r.stages = r.stages > 3 ? 3 : r.stages;
-    const int smem = r.stages * stage + wbytes;
+    constexpr int stage = rev_stage_bytes<DK, BF16>(), zstage = rev_zstage_bytes<DK, BF16>();
+    constexpr int group = rev_group_bytes<DK>(), most = 225 * 1024;
+    // two stages of each ring if that can be, then a third of the chain's
+    r.stages = r.zstages = 2 * (stage + zstage) + group > most ? 1 : 2;
+    if (r.stages == 2 && 3 * stage + 2 * zstage + group <= most) r.stages = 3;
+    const int smem = r.stages * stage + r.zstages * zstage + group;
     static SmemOnce once;
-    cudaError_t e = once.allow(delta_rev_kernel<DK, BF16>, 227 * 1024 - 1024);
+    cudaError_t e = once.allow(delta_rev_kernel<DK, BF16>, most);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
-    delta_rev_kernel<DK, BF16><<<grid, 128 * r.cgs, smem, s>>>(r);
+    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / 16));
+    delta_rev_kernel<DK, BF16><<<grid, 320, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;

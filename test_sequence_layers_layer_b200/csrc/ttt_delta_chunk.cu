@@ -15,6 +15,7 @@
 // has to be brought into operand form on the way.
 #include "../../include/ttt.h"
 #include "ttt_delta_mma.cuh"
+#include <stdlib.h>
 
 namespace ttt {
 namespace delta {
@@ -468,53 +469,66 @@ struct ScanArgs {
     const int *seq_start;
     int B, Hk, H, T, dv, w_heads;  // w_heads: 0 when W0 is shared by the sequences
     int cgs;                       // column groups of a block: 16 columns of W, four warps each
-    int stages;
+    int stages, zstages;           // of the chain's ring and of Z's
     Images im;
     float *saveS, *saveX;          // kSave: [slot][H][DK][dv] and [slot][H][64][dv]
     int *status;
 };
 
-// Bytes of one stage: K, (Q,) H (two terms), (M, one or two terms,) vectors.
+// Bytes of a stage of the chain's ring (K, H with two terms, vectors) and of Z's (Q, M
+// with one term or two, vectors).
+template <int DK, bool BF16>
+constexpr int chain_stage_bytes() { return ((BF16 ? 1 : 2) + 2) * C * DK * 2 + kHalfVecBytes; }
 template <int DK, bool BF16, int MODE>
-constexpr int scan_stage_bytes() {
-    return (MODE == kSave ? 1 : 2) * C * DK * 2 * (BF16 ? 1 : 2) + 2 * C * DK * 2 +
-           (MODE == kSave ? 0 : MODE == kZ32 ? 2 : 1) * kImg + kScanVecBytes;
+constexpr int z_stage_bytes() {
+    return MODE == kSave ? 0
+                         : (BF16 ? 1 : 2) * C * DK * 2 + (MODE == kZ32 ? 2 : 1) * kImg + kHalfVecBytes;
 }
 // A column group's own area behind the stages: the four warps' shares of X
-// [to][from][2 tiles], the terms of X [4 blocks][hi, lo], of W^T [DK / 16][hi, (lo)], 1 / their scales.
+// [to][from][2 tiles], and, twice for the chunks in turn, the terms of X
+// [4 blocks][hi, lo], of W^T [DK / 16][hi, (lo)], and 1 / their scales.
 template <int DK, int MODE>
-constexpr int scan_group_bytes() {
-    return 16 * 1024 + 4096 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1)) + 512;
+constexpr int scan_turn_bytes() {
+    return 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
 }
+template <int DK, int MODE>
+constexpr int scan_group_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MODE>(); }
 
 // Scan over the chunks. Four warps own 16 columns of W for the whole sequence, as
 // the rows of W^T [16][DK] in accumulator registers, a quarter of DK each:
 // accumulator fragments packed pairwise are A fragments, so W^T K^T and X^T H
 // follow one another in registers. Twice a chunk the four meet:
 //   1. each has its quarter's share of W^T K^T for all 64 tokens and hands the
-//      others theirs; warp p then forms X of the 16 tokens of block p, and brings
-//      it into operand form under that block's own row scales;
+//      others theirs; warp p then forms X of the 16 tokens of block p, and brings it
+//      into operand form under that block's own row scales;
 //   2. each takes the operand X of all blocks and updates its quarter of W.
-// Z of block p is warp p's too: c D Q W from the operand form of W^T that the four
-// have handed round in step 1 (a quarter's rows under its own scales, so the
-// sums over the quarters are put together in fp32), and M X. Between the meetings
-// column groups and blocks know nothing of one another.
-// The chunk's images come through a ring of shared-memory stages, filled with
-// bulk copies that the first thread issues; V through registers, one chunk ahead.
+// This chain is what bounds the scan, so all else is off it: two more warps for each
+// group form Z, up to a chunk behind, from the operand forms of W^T and X that the
+// four leave in shared memory (a quarter's rows under its own scales: the
+// sums over the quarters and blocks are put together in fp32), each for two of
+// the blocks, 0 and 3 or 1 and 2, the same share of the triangle M. The chunks'
+// images come by bulk copies through two rings of stages, K and H for the chain, Q
+// and M for Z, so that the chain's next images need not wait for Z. One thread of a
+// warp of its own fills each ring; with two groups a block, where the registers of
+// twelve warps are all there are, the first Z warp of each group does it between
+// its steps. Column groups know nothing of one another. V comes through registers,
+// one chunk ahead.
 template <int DK, bool BF16, int MODE>
-__global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(1024) char ssm[];
-    __shared__ uint64_t full[4], empty[4];
+    __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4];
+    __shared__ uint64_t zready[2][2], zfree[2][2];  // [group][turn]
     __shared__ int abort_flag;
     constexpr bool ZF = MODE == kZ32, SAVE = MODE == kSave;
-    constexpr int STAGE = scan_stage_bytes<DK, BF16, MODE>();
+    constexpr int STAGE = chain_stage_bytes<DK, BF16>(), ZSTAGE = z_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
     constexpr int NT = DK / 32, KK = DK / 64;  // 8-column tiles and 16-deep steps of a quarter
-    constexpr int oH = SAVE ? KALL : 2 * KALL, oM = oH + 2 * KIMG;
     const int groups = a.dv / (16 * a.cgs);
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
-    const int tid = threadIdx.x, lane = tid & 31, cg = tid >> 7, p = (tid >> 5) & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = warp & 3;
+    const bool chain = warp < 4 * a.cgs;
+    const int extra = warp - 4 * a.cgs, cg = chain ? warp >> 2 : extra >> 1;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -524,56 +538,242 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 4 * a.cgs);
+            mbar_init(&zfull[s], 1);
+            mbar_init(&zempty[s], 2 * a.cgs);
         }
+        for (int g = 0; g < 2; ++g)
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(&zready[g][t], 4);
+                mbar_init(&zfree[g][t], 2);
+            }
         fence_mbar_init();
     }
     __syncthreads();
 
-    // Fills the stage of chunk c (one thread): stages - 1 chunks ahead of the
-    // one being worked on, once every warp has left the stage's last chunk.
-    auto fill = [&](int c) {
-        const int s = c % a.stages;
-        if (c >= a.stages &&
-            !mbar_wait(&empty[s], ((c / a.stages) & 1) ^ 1, abort, a.status, kScanStatus))
-            return;
-        char *d = ssm + s * STAGE;
-        const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
-        mbar_arrive_expect_tx(&full[s], STAGE);
-        bulk_load(d, a.im.K + ks * KALL, KALL, &full[s]);
-        if (!SAVE) bulk_load(d + KALL, a.im.Q + ks * KALL, KALL, &full[s]);
-        bulk_load(d + oH, a.im.H + hs * 2 * KIMG, 2 * KIMG, &full[s]);
-        if (!SAVE) bulk_load(d + oM, a.im.M + hs * 2 * kImg, (ZF ? 2 : 1) * kImg, &full[s]);
-        bulk_load(d + STAGE - kScanVecBytes, a.im.vec + hs * kVecBytes, kScanVecBytes, &full[s]);
-    };
-    if (tid == 0)
-        for (int c = 0; c < nchunk && c < a.stages - 1; ++c) fill(c);
-
     const int gq = lane >> 2, q4 = lane & 3;
     const int v0 = (grp * a.cgs + cg) * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *area = ssm + a.stages * STAGE + cg * scan_group_bytes<DK, MODE>();
-    float4 *part = reinterpret_cast<float4 *>(area) + lane;               // [to][from][tile][32]
-    uint4 *xfr = reinterpret_cast<uint4 *>(area + 16 * 1024) + lane;      // [block][hi, lo][32]
-    float *iXs = reinterpret_cast<float *>(area + 20 * 1024), *iSs = iXs + 64;  // [block][16], [quarter][16]
-    uint4 *sfr = reinterpret_cast<uint4 *>(area + 20 * 1024 + 512) + lane;  // [step][hi, (lo)][32]
+    char *zst = ssm + a.stages * STAGE, *area = zst + a.zstages * ZSTAGE + cg * scan_group_bytes<DK, MODE>();
+    auto wait = [&](uint64_t *bar, int parity) {
+        return mbar_wait_warp(bar, parity, abort, a.status, kScanStatus);
+    };
 
-    // V of this lane's places in block p: tokens 16 p + 8 x + 2 q4 + {0, 1}, columns gq, gq + 8
-    // kept as loaded: a conversion here would wait for the load
+    if (!chain) {  // ------------------------------------------------ Z, and the rings
+        auto chain_copy = [&](int c, int s, uint64_t *bar) {
+            char *d = ssm + s * STAGE;
+            const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
+            mbar_arrive_expect_tx(bar, STAGE);
+            bulk_load(d, a.im.K + ks * KALL, KALL, bar);
+            bulk_load(d + KALL, a.im.H + hs * 2 * KIMG, 2 * KIMG, bar);
+            bulk_load(d + STAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes, kHalfVecBytes, bar);
+        };
+        auto z_copy = [&](int c, int s, uint64_t *bar) {
+            char *d = zst + s * ZSTAGE;
+            const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
+            mbar_arrive_expect_tx(bar, ZSTAGE);
+            bulk_load(d, a.im.Q + ks * KALL, KALL, bar);
+            bulk_load(d + KALL, a.im.M + hs * 2 * kImg, (ZF ? 2 : 1) * kImg, bar);
+            bulk_load(d + ZSTAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes + kHalfVecBytes,
+                      kHalfVecBytes, bar);
+        };
+        Filler<decltype(chain_copy)> fill(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
+        Filler<decltype(z_copy)> zfill(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
+        const int own = SAVE ? 0 : a.cgs == 1 ? 2 : -1;  // the first warp that only fills, if any
+        if (own >= 0 && extra >= own) {
+            if (lane == 0) {
+                if (extra == own) {
+                    while (fill.filled < nchunk && fill.next()) {
+                    }
+                    if (*abort) fill.drain();
+                } else {
+                    while (zfill.filled < nchunk && zfill.next()) {
+                    }
+                    if (*abort) zfill.drain();
+                }
+            }
+            return;
+        }
+        const bool fills = own < 0 && lane == 0 && extra == 0, zfills = own < 0 && lane == 0 && extra == 2;
+        auto poll = [&]() {
+            if (fills) fill.poll();
+            if (zfills) zfill.poll();
+            __syncwarp();
+        };
+        const int half = extra & 1;
+        Ring ring(a.zstages);
+        for (int c = 0; c < nchunk; ++c, ring.next()) {
+            const int turn = c & 1;
+            poll();
+            // what this step itself needs has to be on its way before it is waited for
+            const bool lost = (fills && fill.filled == c && !fill.next()) ||
+                              (zfills && zfill.filled == c && !zfill.next());
+            if (__any_sync(0xffffffffu, lost)) break;
+            const uint32_t uQ = smem_u32(zst + ring.s * ZSTAGE), uM = uQ + KALL;
+            // the enum's order, counted from kVq on
+            const float *vec = reinterpret_cast<const float *>(zst + (ring.s + 1) * ZSTAGE - kHalfVecBytes) - kVq * C;
+            const char *at = area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>();
+            const uint4 *xfr = reinterpret_cast<const uint4 *>(at) + lane;             // [block][hi, lo][32]
+            const float *iXs = reinterpret_cast<const float *>(at + 4096), *iSs = iXs + 64;
+            const uint4 *sfr = reinterpret_cast<const uint4 *>(at + 4096 + 512) + lane;  // [step][hi, (lo)][32]
+            if (!wait(&zfull[ring.s], ring.ph)) break;
+            bool ok = false;
+            if (own < 0) {  // the chain may need its next images first
+                for (int tries = 0; tries < 64 && !ok; ++tries) {
+                    ok = __all_sync(0xffffffffu, mbar_test(&zready[cg][turn], (c >> 1) & 1));
+                    poll();
+                }
+            }
+            if (!ok && !wait(&zready[cg][turn], (c >> 1) & 1)) break;
+            float Z[2][2][4] = {}, ZM[2][2][4] = {};
+            // (Q W)^T of the two blocks, quarter by quarter
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                float z[2][2][4] = {};
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
+                    const uint4 fh = d[0];
+                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
+                    uint32_t bb[2][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        load_b(bb[y], uQ, 16 * (half ? 1 + y : 3 * y), w * (DK / 4) + 16 * kk, lane);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) mma_f16(z[y][x], hi, bb[y][2 * x], bb[y][2 * x + 1]);
+                    if (ZF) {
+                        const uint4 fl = d[32];
+                        const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) mma_f16(z[y][x], lo, bb[y][2 * x], bb[y][2 * x + 1]);
+                        if (!BF16) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                load_b(bb[y], uQ + KIMG, 16 * (half ? 1 + y : 3 * y),
+                                       w * (DK / 4) + 16 * kk, lane);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    mma_f16(z[y][x], hi, bb[y][2 * x], bb[y][2 * x + 1]);
+                        }
+                    }
+                }
+                const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            Z[y][x][e] = fmaf(e < 2 ? i0 : i1, z[y][x][e], Z[y][x][e]);
+            }
+            poll();
+            // (M X)^T
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int i = half ? 1 + y : 3 * y;
+                    if (jj > i) continue;  // M_ij is zero for i < j; the same for the whole warp
+                    float z[2][4] = {};
+                    uint32_t bm[4];
+                    load_b(bm, uM, 16 * i, 16 * jj, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
+                    }
+                    if (ZF) {
+                        load_b(bm, uM + kImg, 16 * i, 16 * jj, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            ZM[y][x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], ZM[y][x][e]);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = 16 * (half ? 1 + y : 3 * y) + 8 * x + 2 * q4;
+                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i);
+                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i);
+                    float(&z)[4] = Z[y][x], (&u)[4] = ZM[y][x];
+                    z[0] = cq.x * z[0] + im.x * u[0], z[1] = cq.y * z[1] + im.y * u[1];
+                    z[2] = cq.x * z[2] + im.x * u[2], z[3] = cq.y * z[3] + im.y * u[3];
+                }
+            poll();
+            // everything is read: the arrivals do not wait for the stores behind them
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&zfree[cg][turn]);
+                mbar_arrive(&zempty[ring.s]);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = c * C + 16 * (half ? 1 + y : 3 * y) + 8 * x;
+                    const float(&z)[4] = Z[y][x];
+                    if (ZF) {
+                        const int t = i + 2 * q4;
+                        float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
+                        if (t < len) o[0] = z[0], o[8] = z[2];
+                        if (t + 1 < len) o[a.dv] = z[1], o[a.dv + 8] = z[3];
+                    } else {
+                        // 8 x 8 blocks transposed between the lanes: a token per row
+                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(z[0], z[1]);
+                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(z[2], z[3]);
+                        const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
+                        const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
+                        const int t = i + gq;
+                        if (t < len) {
+                            uint32_t *o = reinterpret_cast<uint32_t *>(
+                                static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
+                            o[0] = r0;
+                            o[4] = r1;
+                        }
+                    }
+                }
+        }
+        if (fills && *abort) fill.drain();
+        if (zfills && *abort) zfill.drain();
+        return;
+    }
+
+    // -------------------------------------------------------------- the chain
+    float4 *part = reinterpret_cast<float4 *>(area) + lane;  // [to][from][tile][32]
+    // V of this lane's places in block p: tokens 16 p + 8 x + 2 q4 + {0, 1}, columns gq,
+    // gq + 8; kept as loaded: a conversion here would wait for the load
     uint32_t v[2][4];
+    const size_t vlane = (vrow + 16 * p + 2 * q4) * a.dv + v0 + gq;
     auto fetch_v = [&](int c) {
+        const int t = c * C + 16 * p + 2 * q4;
+        const size_t at = vlane + (size_t)c * C * a.dv;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int t = c * C + 16 * p + 8 * x + 2 * q4 + (e & 1);
-                const size_t at = (vrow + t) * a.dv + v0 + gq + (e >> 1) * 8;
                 v[x][e] = 0;
-                if (t < len)
-                    v[x][e] = BF16 ? (uint32_t)static_cast<const uint16_t *>(a.V)[at]
-                                   : static_cast<const uint32_t *>(a.V)[at];
+                if (t + 8 * x + (e & 1) < len) {
+                    const size_t i = at + (8 * x + (e & 1)) * a.dv + (e >> 1) * 8;
+                    v[x][e] = BF16 ? (uint32_t)static_cast<const uint16_t *>(a.V)[i]
+                                   : static_cast<const uint32_t *>(a.V)[i];
+                }
             }
     };
     auto v_at = [&](int x, int e) { return __uint_as_float(BF16 ? v[x][e] << 16 : v[x][e]); };
@@ -589,89 +789,70 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
             S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
     if (nchunk > 0) fetch_v(0);
 
-    for (int c = 0; c < nchunk; ++c) {
-        const int s = c % a.stages;
-        if (tid == 0 && c + a.stages - 1 < nchunk) fill(c + a.stages - 1);
-        const bool ok = mbar_wait_warp(&full[s], (c / a.stages) & 1, abort, a.status, kScanStatus);
-        const uint32_t uK = smem_u32(ssm + s * STAGE), uQ = uK + KALL, uH = uK + oH, uM = uK + oM;
-        const float *vec = reinterpret_cast<const float *>(ssm + (s + 1) * STAGE - kScanVecBytes);
-        if (SAVE && ok) {
-            float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
-        }
-        // W^T K^T over this warp's quarter of DK, W^T's terms handed round for Z
+    Ring ring(a.stages);
+    for (int c = 0; c < nchunk; ++c, ring.next()) {
+        const int turn = c & 1;
+        const uint32_t uK = smem_u32(ssm + ring.s * STAGE), uH = uK + KALL;
+        const float *vec = reinterpret_cast<const float *>(ssm + (ring.s + 1) * STAGE - kHalfVecBytes);
+        char *at = area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>();
+        uint4 *xfr = reinterpret_cast<uint4 *>(at) + lane;
+        float *iXs = reinterpret_cast<float *>(at + 4096), *iSs = iXs + 64;
+        uint4 *sfr = reinterpret_cast<uint4 *>(at + 4096 + 512) + lane;
+        bool ok = wait(&full[ring.s], ring.ph);
+        if (!SAVE && c >= 2) ok = ok && wait(&zfree[cg][turn], ((c >> 1) & 1) ^ 1);
+        // W^T K^T over this warp's quarter of DK, W^T's terms left for Z
         if (ok) {
             float X[8][4] = {}, sS[2], iS[2];
+            uint32_t bb[KK][4][4];
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int np = 0; np < 4; ++np) load_b(bb[kk][np], uK, 16 * np, k0 + 16 * kk, lane);
             row_scales<NT>(S, sS, iS);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                uint32_t hi[4], lo[4], bb[4][4];
+                uint32_t hi[4], lo[4];
                 a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], hi, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt)
+                    mma_f16(X[nt], lo, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
+                if (!BF16) {
+#pragma unroll
+                    for (int np = 0; np < 4; ++np)
+                        load_b(bb[kk][np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+                        mma_f16(X[nt], hi, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
+                }
                 if (!SAVE) {
                     uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (p * KK + kk);
                     d[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     if (ZF) d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-#pragma unroll
-                for (int np = 0; np < 4; ++np) load_b(bb[np], uK, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], lo, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                if (!BF16) {
-#pragma unroll
-                    for (int np = 0; np < 4; ++np)
-                        load_b(bb[np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-                        mma_f16(X[nt], hi, bb[nt >> 1][2 * (nt & 1)], bb[nt >> 1][2 * (nt & 1) + 1]);
-                }
             }
+            if (!SAVE && q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
                 part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
                     iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
-            if (!SAVE && q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
         }
         // the first meeting; all leave together when a wait has run out
-        if (named_bar_or(1 + cg, 128, !ok)) {
-            // copies in flight land before the block's shared memory goes
-            if (tid == 0)
-                for (int i = c; i < c + a.stages && i < nchunk; ++i)
-                    mbar_drain(&full[i % a.stages], (i / a.stages) & 1);
-            return;
-        }
+        if (named_bar_or(1 + cg, 128, !ok)) return;
         // X of block p, in operand form
         {
             float X[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
-                float4 o = part[32 * (8 * p + x)];
-#pragma unroll
-                for (int w = 1; w < 4; ++w) {
-                    const float4 u = part[32 * (8 * p + 2 * w + x)];
-                    o.x += u.x, o.y += u.y, o.z += u.z, o.w += u.w;
-                }
-                X[x][0] = v_at(x, 0) - ck.x * o.x;
-                X[x][1] = v_at(x, 1) - ck.y * o.y;
-                X[x][2] = v_at(x, 2) - ck.x * o.z;
-                X[x][3] = v_at(x, 3) - ck.y * o.w;
-            }
-            if (c + 1 < nchunk) fetch_v(c + 1);
-            if (SAVE) {
-                float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + gq;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        wx[(size_t)(8 * x + (e & 1)) * a.dv + (e >> 1) * 8] = X[x][e];
+                const float4 o0 = part[32 * (8 * p + x)], o1 = part[32 * (8 * p + 2 + x)],
+                             o2 = part[32 * (8 * p + 4 + x)], o3 = part[32 * (8 * p + 6 + x)];
+                X[x][0] = v_at(x, 0) - ck.x * ((o0.x + o1.x) + (o2.x + o3.x));
+                X[x][1] = v_at(x, 1) - ck.y * ((o0.y + o1.y) + (o2.y + o3.y));
+                X[x][2] = v_at(x, 2) - ck.x * ((o0.z + o1.z) + (o2.z + o3.z));
+                X[x][3] = v_at(x, 3) - ck.y * ((o0.w + o1.w) + (o2.w + o3.w));
             }
             float sX[2], iX[2];
             uint32_t hi[4], lo[4];
@@ -680,141 +861,72 @@ __global__ void __launch_bounds__(DK == 64 ? 512 : 256, 1) delta_scan_kernel(Sca
             xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
-        }
-        // (Q W)^T of block p, quarter by quarter
-        float Z[2][4] = {};
-        if (!SAVE) {
+            if (!SAVE) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&zready[cg][turn]);
+            } else {
+                float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + gq;
+                float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float z[2][4] = {};
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
-                    const uint4 fh = d[0];
-                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
-                    uint32_t bb[4];
-                    load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
+                    for (int e = 0; e < 4; ++e)
+                        wx[(size_t)(8 * x + (e & 1)) * a.dv + (e >> 1) * 8] = X[x][e];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
-                    if (ZF) {
-                        const uint4 fl = d[32];
-                        const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
-                        if (!BF16) {
-                            load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
-                        }
-                    }
-                }
-                const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    Z[x][0] = fmaf(i0, z[x][0], Z[x][0]);
-                    Z[x][1] = fmaf(i0, z[x][1], Z[x][1]);
-                    Z[x][2] = fmaf(i1, z[x][2], Z[x][2]);
-                    Z[x][3] = fmaf(i1, z[x][3], Z[x][3]);
-                }
+                    for (int e = 0; e < 4; ++e)
+                        ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
             }
         }
+        // H of the first half of the tokens and the next V, in the shadow of the meeting
+        uint32_t bh[2][KK][4], bl[2][KK][4];
+        auto load_h = [&](int y, int jj) {
+#pragma unroll
+            for (int np = 0; np < KK; ++np) {
+                load_bt(bh[y][np], uH, 16 * jj, k0 + 16 * np, lane);
+                load_bt(bl[y][np], uH + KIMG, 16 * jj, k0 + 16 * np, lane);
+            }
+        };
+        load_h(0, 0);
+        load_h(1, 1);
+        const float gam = vec[kVs * C];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
+        if (c + 1 < nchunk) fetch_v(c + 1);
         named_bar(1 + cg, 128);  // the second meeting
 
-        // W'^T = exp(G_C) W^T + X^T H; Z^T += X^T M^T of block p
-        {
-            const float gam = vec[kVs * C];
-            float ZM[2][4] = {};
+        // W'^T = exp(G_C) W^T + X^T H
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+            const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+            const float iH = vec[kVs * C + 1 + jj];
+            const float u0 = iXs[16 * jj + gq] * iH, u1 = iXs[16 * jj + gq + 8] * iH;
+            uint32_t(&h2)[KK][4] = bh[jj & 1], (&l2)[KK][4] = bl[jj & 1];
+            float U[NT][4] = {};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
+                mma_f16(U[nt], hi, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(U[nt], lo, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
-                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
-                const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
-                const float iH = vec[kVs * C + 1 + jj];
-                float U[NT][4] = {};
-                uint32_t bh[KK][4], bl[KK][4];
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(U[nt], hi, l2[nt >> 1][2 * (nt & 1)], l2[nt >> 1][2 * (nt & 1) + 1]);
+            if (jj < 2) load_h(jj, jj + 2);
 #pragma unroll
-                for (int np = 0; np < KK; ++np) {
-                    load_bt(bh[np], uH, 16 * jj, k0 + 16 * np, lane);
-                    load_bt(bl[np], uH + KIMG, 16 * jj, k0 + 16 * np, lane);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(U[nt], hi, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(U[nt], lo, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(U[nt], hi, bl[nt >> 1][2 * (nt & 1)], bl[nt >> 1][2 * (nt & 1) + 1]);
-                if (!SAVE && jj <= p) {  // M_ij is zero for i < j; the same for the whole warp
-                    float z[2][4] = {};
-                    uint32_t bm[4];
-                    load_b(bm, uM, 16 * p, 16 * jj, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
-                    }
-                    if (ZF) {
-                        load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        ZM[x][0] = fmaf(i0, z[x][0], ZM[x][0]);
-                        ZM[x][1] = fmaf(i0, z[x][1], ZM[x][1]);
-                        ZM[x][2] = fmaf(i1, z[x][2], ZM[x][2]);
-                        ZM[x][3] = fmaf(i1, z[x][3], ZM[x][3]);
-                    }
-                }
-                const float u0 = i0 * iH, u1 = i1 * iH;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    S[nt][0] = fmaf(u0, U[nt][0], S[nt][0]);
-                    S[nt][1] = fmaf(u0, U[nt][1], S[nt][1]);
-                    S[nt][2] = fmaf(u1, U[nt][2], S[nt][2]);
-                    S[nt][3] = fmaf(u1, U[nt][3], S[nt][3]);
-                }
-            }
-            if (!SAVE) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = 16 * p + 8 * x;
-                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i + 2 * q4);
-                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i + 2 * q4);
-                    const float z0 = cq.x * Z[x][0] + im.x * ZM[x][0];
-                    const float z1 = cq.y * Z[x][1] + im.y * ZM[x][1];
-                    const float z2 = cq.x * Z[x][2] + im.x * ZM[x][2];
-                    const float z3 = cq.y * Z[x][3] + im.y * ZM[x][3];
-                    if (ZF) {
-                        const int t = c * C + i + 2 * q4;
-                        float *z = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
-                        if (t < len) z[0] = z0, z[8] = z2;
-                        if (t + 1 < len) z[a.dv] = z1, z[a.dv + 8] = z3;
-                    } else {
-                        // 8 x 8 blocks transposed between the lanes: a token per row
-                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(z0, z1);
-                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(z2, z3);
-                        const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
-                        const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
-                        const int t = c * C + i + gq;
-                        if (t < len) {
-                            uint32_t *z = reinterpret_cast<uint32_t *>(
-                                static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
-                            z[0] = r0;
-                            z[4] = r1;
-                        }
-                    }
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                S[nt][0] = fmaf(u0, U[nt][0], S[nt][0]);
+                S[nt][1] = fmaf(u0, U[nt][1], S[nt][1]);
+                S[nt][2] = fmaf(u1, U[nt][2], S[nt][2]);
+                S[nt][3] = fmaf(u1, U[nt][3], S[nt][3]);
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) mbar_arrive(&empty[ring.s]);
     }
 
     if (a.W_out) {
@@ -841,17 +953,21 @@ cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
 
 template <int DK, bool BF16, int MODE>
 cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
-    r.cgs = scan_groups((long long)N * r.H, DK, r.dv);
-    constexpr int stage = scan_stage_bytes<DK, BF16, MODE>();
-    const int wbytes = r.cgs * scan_group_bytes<DK, MODE>();
-    r.stages = (226 * 1024 - wbytes) / stage;
-    r.stages = r.stages > 3 ? 3 : r.stages;
-    const int smem = r.stages * stage + wbytes;
+    constexpr int stage = chain_stage_bytes<DK, BF16>(), zstage = z_stage_bytes<DK, BF16, MODE>();
+    constexpr int group = scan_group_bytes<DK, MODE>(), most = 225 * 1024;
+    r.cgs = scan_groups((long long)N * r.H, r.dv);
+    // two stages of each ring if that can be, so that the next chunk is loaded during
+    // this one; then a third of the chain's
+    if (2 * (stage + zstage) + r.cgs * group > most) r.cgs = 1;
+    r.stages = r.zstages = 2 * (stage + zstage) + r.cgs * group > most ? 1 : 2;
+    if (r.stages == 2 && 3 * stage + 2 * zstage + r.cgs * group <= most) r.stages = 3;
+    const int smem = r.stages * stage + r.zstages * zstage + r.cgs * group;
     static SmemOnce once;
-    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, 227 * 1024 - 1024);
+    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, most);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
-    delta_scan_kernel<DK, BF16, MODE><<<grid, 128 * r.cgs, smem, s>>>(r);
+    const int warps = MODE == kSave ? 4 * r.cgs + 1 : r.cgs == 1 ? 8 : 12;
+    delta_scan_kernel<DK, BF16, MODE><<<grid, 32 * warps, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
@@ -880,23 +996,19 @@ cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cud
 }
 
 // Column groups of a block (one block per SM): the fewest rounds of blocks over
-// the 148 SMs win. A chunk of a block of two groups takes 1.2 times that of one, of
-// four 2 times (their warps share the schedulers).
-int scan_groups(long long heads, int dk, int dv) {
-    int best = 1;
-    double least = 1e30;
-    for (int cgs = 1; cgs <= (dk == 64 ? 4 : 2); cgs *= 2) {
-        const double rounds = (double)((heads * (dv / (16 * cgs)) + 147) / 148) *
-                              (cgs == 4 ? 2.0 : cgs == 2 ? 1.2 : 1.0);
-        if (rounds < least) least = rounds, best = cgs;
-    }
-    return best;
+// the 148 SMs win, a round of two-group blocks counted 1.4 times.
+int scan_groups(long long heads, int dv) {
+    const char *f = getenv("DSHAPE");
+    if (f) return f[0] - '0';
+    const double one = (double)((heads * (dv / 16) + 147) / 148);
+    const double two = (double)((heads * (dv / 32) + 147) / 148) * 1.4;
+    return two < one ? 2 : 1;
 }
 
 cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
                         cudaStream_t s) {
     const ScanArgs r{a.V, a.W0, a.Z, a.W_out, a.seq_start, a.B, a.Hk, a.H, a.T, a.dv,
-                     a.w0_per_seq ? a.H : 0, 0, 0, im, saveS, saveX, device_status_word()};
+                     a.w0_per_seq ? a.H : 0, 0, 0, 0, im, saveS, saveX, device_status_word()};
     if (a.dk == 64)
         return a.bf16 ? scan_mode<64, true>(r, a.N, mode, s) : scan_mode<64, false>(r, a.N, mode, s);
     return a.bf16 ? scan_mode<128, true>(r, a.N, mode, s) : scan_mode<128, false>(r, a.N, mode, s);

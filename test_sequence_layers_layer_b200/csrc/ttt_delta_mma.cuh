@@ -26,13 +26,13 @@ using namespace sm100;
 constexpr int C = kDeltaC;
 constexpr int kImg = C * C * 2;  // bytes of a 64 x 64 fp16 image
 
-// Per chunk and value head: vectors of 64 floats; sX is the scale of row j
-// of image X. The scans read the first four.
+// Per chunk and value head: vectors of 64 floats; sX is the scale of row j of image
+// X. The scans' chains read the first two, the warps beside them the next two.
 enum Vec {
     kVk,   // exp(G_j) / sK_j
+    kVs,   // [0] exp(G_C), [1 + b] 1 / sH of the 16 rows of block b (one scale for them)
     kVq,   // c exp(G_i) / sQ_i
     kVm,   // 1 / sM_i
-    kVs,   // [0] exp(G_C), [1 + b] 1 / sH of the 16 rows of block b (one scale for them)
     kVik,  // 1 / sK_j
     kViq,  // 1 / sQ_i
     kVgh,  // G_j as the sum of two floats
@@ -40,7 +40,7 @@ enum Vec {
     kVit,  // 1 / sT_i
     kVecs
 };
-constexpr int kVecBytes = kVecs * C * 4, kScanVecBytes = 4 * C * 4;
+constexpr int kVecBytes = kVecs * C * 4, kHalfVecBytes = 2 * C * 4;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -126,10 +126,57 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+constexpr int kScanStatus = 61;  // a wait of the scans has run out
+
+// Place in a ring of stages: the stage and the parity of its use, without divisions.
+struct Ring {
+    int stages, s = 0, ph = 0;
+    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
+    __device__ __forceinline__ void next() {
+        if (++s == stages) s = 0, ph ^= 1;
+    }
+};
+
+// What one thread needs to keep a ring of stages filled. copy(step, stage, bar)
+// issues the copies of a step after announcing their bytes on the barrier.
+template <class Copy>
+struct Filler {
+    uint64_t *full, *empty;
+    Copy copy;
+    int steps, filled;
+    Ring to;
+    volatile int *abort;
+    int *status;
+    __device__ __forceinline__ Filler(uint64_t *f, uint64_t *e, int stages, int n, volatile int *ab,
+                                      int *st, Copy c)
+        : full(f), empty(e), copy(c), steps(n), filled(0), to(stages), abort(ab), status(st) {}
+    __device__ __forceinline__ void put() {
+        copy(filled, to.s, &full[to.s]);
+        ++filled;
+        to.next();
+    }
+    // All steps that have a free stage, without waiting.
+    __device__ __forceinline__ void poll() {
+        while (filled < steps && (filled < to.stages || mbar_test(&empty[to.s], to.ph ^ 1))) put();
+    }
+    // The next step, waiting for its stage; false when a wait has run out.
+    __device__ __forceinline__ bool next() {
+        if (filled >= to.stages && !mbar_wait(&empty[to.s], to.ph ^ 1, abort, status, kScanStatus))
+            return false;
+        put();
+        return true;
+    }
+    // After an abort: copies in flight land before the block's shared memory goes.
+    __device__ __forceinline__ void drain() {
+        Ring r(to.stages);
+        for (int i = 0; i < filled; ++i, r.next())
+            if (i >= filled - to.stages) mbar_drain(&full[r.s], r.ph);
+    }
+};
+
 // What a scan writes: Z as bf16, Z as fp32, or (for the backward) the weight
 // each chunk starts from and X.
 enum ScanMode { kZ16, kZ32, kSave };
-constexpr int kScanStatus = 61;
 
 // Workspace: per chunk slot and head, the images that the scans read.
 //   K, Q [key head]: the chunk's rows, one fp16 term (bf16 inputs) or two
@@ -231,7 +278,7 @@ struct SmemOnce {
 // The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
 Images images_at(const Plan &p, void *workspace, bool bwd);
-int scan_groups(long long heads, int dk, int dv);
+int scan_groups(long long heads, int dv);
 cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
                         cudaStream_t s);
 
