@@ -46,23 +46,29 @@ constexpr int rev_zstage_bytes() { return (BF16 ? 1 : 2) * C * DK * 2 + 2 * kImg
 // what the helpers leave: (M^T dZ)^T [4 blocks][2 tiles], (c D Q)^T dZ transposed [DK / 8 tiles].
 template <int DK>
 constexpr int rev_turn_bytes() { return 4096 + DK / 8 * 512; }
-template <int DK>
-constexpr int rev_group_bytes() { return 16 * 1024 + 4096 + 8192 + 768 + 2 * rev_turn_bytes<DK>(); }
+// Two turns, so that the helpers may run ahead; one where shared memory is short.
+template <int DK, bool BF16>
+constexpr int rev_turns() { return DK == 128 && !BF16 ? 1 : 2; }
+template <int DK, bool BF16>
+constexpr int rev_area_bytes() {
+    return 16 * 1024 + 4096 + 8192 + 768 + rev_turns<DK, BF16>() * rev_turn_bytes<DK>();
+}
 
 // The mirror of the forward scan: four warps own 16 columns of Om, as the rows of
 // Om^T in registers, a quarter of DK each. Before the first meeting each hands out its
 // quarter's share of Om^T H^T; warp p puts dX of block p together, and after the second
 // meeting each updates its quarter of Om. What dZ adds does not depend on Om: four
 // helper warps form M^T dZ (a block of tokens each) and (c D Q)^T dZ (a quarter of DK
-// each), up to two chunks ahead. Two more warps fill the rings of stages.
+// each), up to two chunks ahead. Two more warps fill the rings of stages, and one, the
+// gate, does the chain's waiting.
 template <int DK, bool BF16>
-__global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
-    extern __shared__ __align__(1024) char ssm[];
+__global__ void __launch_bounds__(352, 1) delta_rev_kernel(RevArgs a) {
+    extern __shared__ __align__(128) char ssm[];
     __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4], zready[2], zfree[2];
     __shared__ int abort_flag;
     constexpr int STAGE = rev_stage_bytes<DK, BF16>(), ZSTAGE = rev_zstage_bytes<DK, BF16>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
-    constexpr int NT = DK / 32, KK = DK / 64;
+    constexpr int NT = DK / 32, KK = DK / 64, TURNS = rev_turns<DK, BF16>();
     const int groups = a.dv / 16;
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
@@ -78,13 +84,13 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
         abort_flag = 0;
         for (int s = 0; s < 4; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4);
+            mbar_init(&empty[s], 1);
             mbar_init(&zfull[s], 1);
             mbar_init(&zempty[s], 4);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&zready[t], 4);
-            mbar_init(&zfree[t], 4);
+            mbar_init(&zfree[t], 1);
         }
         fence_mbar_init();
     }
@@ -102,6 +108,22 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
     auto turn_at = [&](int turn) { return area + 28 * 1024 + 768 + turn * rev_turn_bytes<DK>(); };
 
     // step i works on chunk nchunk - 1 - i
+    if (warp == 10) {  // ------------------------------------------------ the gate
+        // Waits for all that a step needs and then meets the chain, which so waits on
+        // nothing but barriers; at the next meeting the chain is done with what it had.
+        Ring ring(a.stages);
+        int last = 0;
+        for (int i = 0; i < nchunk; ++i, ring.next()) {
+            const bool ok = wait(&full[ring.s], ring.ph) && wait(&zready[i % TURNS], (i / TURNS) & 1);
+            if (named_bar_or(3, 160, !ok)) return;
+            if (i > 0 && lane == 0) {
+                mbar_arrive(&empty[last]);
+                if (TURNS == 2) mbar_arrive(&zfree[(i - 1) % TURNS]);
+            }
+            last = ring.s;
+        }
+        return;
+    }
     if (warp >= 8) {  // ------------------------------------------------ the rings
         auto chain_copy = [&](int i, int s, uint64_t *bar) {
             char *d = ssm + s * STAGE;
@@ -152,14 +174,14 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
         if (nchunk > 0) fetch_z(nchunk - 1);
         Ring ring(a.zstages);
         for (int i = 0; i < nchunk; ++i, ring.next()) {
-            const int turn = i & 1, c = nchunk - 1 - i;
+            const int turn = i % TURNS, c = nchunk - 1 - i;
             const uint32_t uQ = smem_u32(zst + ring.s * ZSTAGE), uM = uQ + KALL;
             // the enum's order, counted from kVq on
             const float *vec = reinterpret_cast<const float *>(zst + (ring.s + 1) * ZSTAGE - kHalfVecBytes) - kVq * C;
             float4 *zm = reinterpret_cast<float4 *>(turn_at(turn)) + lane;  // [block][tile][32]
             float4 *uq = zm + 256;                                         // [DK / 8][32]
             bool ok = wait(&zfull[ring.s], ring.ph);
-            if (i >= 2) ok = ok && wait(&zfree[turn], ((i >> 1) & 1) ^ 1);
+            if (i >= TURNS) ok = ok && wait(&zfree[turn], ((i / TURNS) & 1) ^ 1);
             if (ok) {
                 // dZ of block p as an operand for M (M's row scales in it) and for c D Q
 #pragma unroll
@@ -263,22 +285,35 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
         for (int e = 0; e < 4; ++e)
             S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
 
+    // Om at the end of chunk c
+    auto save = [&](int c) {
+        float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+    };
+    if (nchunk > 0) save(nchunk - 1);
+
     Ring ring(a.stages);
     for (int i = 0; i < nchunk; ++i, ring.next()) {
-        const int turn = i & 1, c = nchunk - 1 - i;
+        const int turn = i % TURNS, c = nchunk - 1 - i;
         const uint32_t uH = smem_u32(ssm + ring.s * STAGE), uK = uH + 2 * KIMG;
         const float *vec = reinterpret_cast<const float *>(ssm + (ring.s + 1) * STAGE - kHalfVecBytes);
         const float4 *zm = reinterpret_cast<const float4 *>(turn_at(turn)) + lane, *uq = zm + 256;
-        bool ok = wait(&full[ring.s], ring.ph);
+        if (named_bar_or(3, 160, false)) return;  // with the gate; it says when a wait has run out
         // Om^T H^T over this warp's quarter of DK
-        if (ok) {
+        {
             float X[8][4] = {}, sS[2], iS[2];
-            uint32_t bh[4][4], bl[4][4];
+            uint32_t bh[KK][4][4], bl[KK][4][4];
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                load_b(bh[np], uH, 16 * np, k0, lane);
-                load_b(bl[np], uH + KIMG, 16 * np, k0, lane);
-            }
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    load_b(bh[kk][np], uH, 16 * np, k0 + 16 * kk, lane);
+                    load_b(bl[kk][np], uH + KIMG, 16 * np, k0 + 16 * kk, lane);
+                }
             row_scales<NT>(S, sS, iS);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
@@ -286,29 +321,20 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
                 a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
+                    mma_f16(X[nt], hi, bh[kk][nt >> 1][2 * (nt & 1)], bh[kk][nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], lo, bh[nt >> 1][2 * (nt & 1)], bh[nt >> 1][2 * (nt & 1) + 1]);
-                if (kk + 1 < KK)
-#pragma unroll
-                    for (int np = 0; np < 4; ++np) load_b(bh[np], uH, 16 * np, k0 + 16 * kk + 16, lane);
+                    mma_f16(X[nt], lo, bh[kk][nt >> 1][2 * (nt & 1)], bh[kk][nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bl[nt >> 1][2 * (nt & 1)], bl[nt >> 1][2 * (nt & 1) + 1]);
-                if (kk + 1 < KK)
-#pragma unroll
-                    for (int np = 0; np < 4; ++np)
-                        load_b(bl[np], uH + KIMG, 16 * np, k0 + 16 * kk + 16, lane);
+                    mma_f16(X[nt], hi, bl[kk][nt >> 1][2 * (nt & 1)], bl[kk][nt >> 1][2 * (nt & 1) + 1]);
             }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
                 part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
                     iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
-            ok = wait(&zready[turn], (i >> 1) & 1);
         }
-        // the first meeting; all leave together when a wait has run out
-        if (named_bar_or(1, 128, !ok)) return;
+        named_bar(1, 128);  // the first meeting
         // dX of block p
         float X[2][4];
         {
@@ -344,17 +370,15 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
 #pragma unroll
             for (int np = 0; np < KK; ++np) load_bt(bk[jj][np], uK, 16 * jj, k0 + 16 * np, lane);
         const float gam = vec[kVs * C];
-        float *ws = a.saveO + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
             const float4 u = uq[32 * (p * NT + nt)];
             S[nt][0] = fmaf(gam, S[nt][0], u.x), S[nt][1] = fmaf(gam, S[nt][1], u.y);
             S[nt][2] = fmaf(gam, S[nt][2], u.z), S[nt][3] = fmaf(gam, S[nt][3], u.w);
         }
-        named_bar(1, 128);  // the second meeting; zm and uq are read
+        named_bar(1, 128);  // the second meeting
+        // with one turn the gate cannot give it back: it waits for the next step's
+        if (TURNS == 1 && tid == 0) mbar_arrive(&zfree[0]);
 
         // Om^T <- exp(G_C) Om^T + dZ^T (c D Q) - dX^T (D K)
 #pragma unroll
@@ -385,12 +409,7 @@ __global__ void __launch_bounds__(320, 1) delta_rev_kernel(RevArgs a) {
                 S[nt][3] = fmaf(i1, U[nt][3], S[nt][3]);
             }
         }
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&zfree[turn]);
-            mbar_arrive(&empty[ring.s]);
-        }
-        // dV behind the arrivals, which would wait for its stores
+        if (c > 0) save(c - 1);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = c * C + 16 * p + 8 * x + 2 * q4;
@@ -490,7 +509,7 @@ struct RowFrags {
 // holds the rows of tokens 16 mt .. 16 mt + 15 and half of the columns.
 template <int DK, int DV, bool BF16>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a) {
-    extern __shared__ __align__(1024) char gsm[];
+    extern __shared__ __align__(128) char gsm[];
     using SM = GradSmem<DK, DV, BF16>;
     constexpr int IMG = SM::IMG, KIMG = C * DK * 2;
     constexpr int NK = DK / 16;  // 8-column tiles of half of DK
@@ -1027,16 +1046,19 @@ BwdPlan bwd_plan(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed
 template <int DK, bool BF16>
 cudaError_t rev_inst(RevArgs r, int N, cudaStream_t s) {
     constexpr int stage = rev_stage_bytes<DK, BF16>(), zstage = rev_zstage_bytes<DK, BF16>();
-    constexpr int group = rev_group_bytes<DK>(), most = 225 * 1024;
-    // two stages of each ring if that can be, then a third of the chain's
-    r.stages = r.zstages = 2 * (stage + zstage) + group > most ? 1 : 2;
-    if (r.stages == 2 && 3 * stage + 2 * zstage + group <= most) r.stages = 3;
-    const int smem = r.stages * stage + r.zstages * zstage + group;
+    constexpr int area = rev_area_bytes<DK, BF16>();
+    // two stages of the chain's ring at least (the gate frees one when the chain has
+    // met it for the next), two of the helpers' or a third of the chain's where there is room
+    static_assert(2 * stage + zstage + area <= kScanSmem, "shared memory");
+    r.stages = 2;
+    r.zstages = 2 * (stage + zstage) + area <= kScanSmem ? 2 : 1;
+    if (3 * stage + 2 * zstage + area <= kScanSmem) r.stages = 3;
+    const int smem = r.stages * stage + r.zstages * zstage + area;
     static SmemOnce once;
-    cudaError_t e = once.allow(delta_rev_kernel<DK, BF16>, most);
+    cudaError_t e = once.allow(delta_rev_kernel<DK, BF16>, kScanSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / 16));
-    delta_rev_kernel<DK, BF16><<<grid, 320, smem, s>>>(r);
+    delta_rev_kernel<DK, BF16><<<grid, 352, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;

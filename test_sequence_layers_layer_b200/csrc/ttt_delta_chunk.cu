@@ -15,7 +15,6 @@
 // has to be brought into operand form on the way.
 #include "../../include/ttt.h"
 #include "ttt_delta_mma.cuh"
-#include <stdlib.h>
 
 namespace ttt {
 namespace delta {
@@ -174,7 +173,7 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
 // each; the inverse between them takes all.
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a) {
-    extern __shared__ __align__(1024) char psm[];
+    extern __shared__ __align__(128) char psm[];
     constexpr int KIMG = C * DK * 2, IMG = KIMG * (BF16 ? 1 : 2);
     char *sK = psm, *sQ = sK + IMG;
     float *L = reinterpret_cast<float *>(sQ + IMG);  // A of the chunk, row-major
@@ -468,7 +467,6 @@ struct ScanArgs {
     float *W_out;
     const int *seq_start;
     int B, Hk, H, T, dv, w_heads;  // w_heads: 0 when W0 is shared by the sequences
-    int cgs;                       // column groups of a block: 16 columns of W, four warps each
     int stages, zstages;           // of the chain's ring and of Z's
     Images im;
     float *saveS, *saveX;          // kSave: [slot][H][DK][dv] and [slot][H][64][dv]
@@ -484,15 +482,48 @@ constexpr int z_stage_bytes() {
     return MODE == kSave ? 0
                          : (BF16 ? 1 : 2) * C * DK * 2 + (MODE == kZ32 ? 2 : 1) * kImg + kHalfVecBytes;
 }
-// A column group's own area behind the stages: the four warps' shares of X
-// [to][from][2 tiles], and, twice for the chunks in turn, the terms of X
-// [4 blocks][hi, lo], of W^T [DK / 16][hi, (lo)], and 1 / their scales.
+// Where the 16-byte unit `part` of a token's 16 columns of V stands: rows of 32 bytes
+// (bf16) with the halves of every other four swapped, so that the eight rows of an
+// ldmatrix meet all banks, or of 64 (fp32) with the quarters turned by row pairs.
+template <bool BF16>
+__device__ __forceinline__ uint32_t v_off(int row, int part) {
+    return BF16 ? row * 32 + ((part ^ ((row >> 2) & 1)) << 4)
+                : row * 64 + ((part ^ ((row >> 1) & 3)) << 4);
+}
+// V of a block of 16 tokens as two tiles of V^T: columns gq (x, y) and gq + 8 (z, w) of
+// tokens 8 x + 2 q4 + {0, 1}.
+template <bool BF16>
+__device__ __forceinline__ void load_v(float4 (&v)[2], const char *vt, int row0, int lane) {
+    if (BF16) {
+        uint32_t r[4];
+        ldsm_x4_t(r, smem_u32(vt) + v_off<BF16>(row0 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            v[x] = make_float4(__uint_as_float(r[2 * x] << 16), __uint_as_float(r[2 * x] & 0xFFFF0000u),
+                               __uint_as_float(r[2 * x + 1] << 16),
+                               __uint_as_float(r[2 * x + 1] & 0xFFFF0000u));
+    } else {
+        const int gq = lane >> 2, q4 = lane & 3;
+        auto at = [&](int row, int col) {
+            return *reinterpret_cast<const float *>(vt + v_off<BF16>(row, col >> 2) + (col & 3) * 4);
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t = row0 + 8 * x + 2 * q4;
+            v[x] = make_float4(at(t, gq), at(t + 1, gq), at(t, gq + 8), at(t + 1, gq + 8));
+        }
+    }
+}
+
+// Behind the stages: the four warps' shares of X [to][from][2 tiles], and, twice for
+// the chunks in turn, V [64][16], the terms of X [4 blocks][hi, lo], 1 / their
+// scales and those of W^T, the terms of W^T [DK / 16][hi, (lo)].
 template <int DK, int MODE>
 constexpr int scan_turn_bytes() {
-    return 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
+    return 4096 + 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
 }
 template <int DK, int MODE>
-constexpr int scan_group_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MODE>(); }
+constexpr int scan_area_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MODE>(); }
 
 // Scan over the chunks. Four warps own 16 columns of W for the whole sequence, as
 // the rows of W^T [16][DK] in accumulator registers, a quarter of DK each:
@@ -502,33 +533,29 @@ constexpr int scan_group_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MO
 //      others theirs; warp p then forms X of the 16 tokens of block p, and brings it
 //      into operand form under that block's own row scales;
 //   2. each takes the operand X of all blocks and updates its quarter of W.
-// This chain is what bounds the scan, so all else is off it: two more warps for each
-// group form Z, up to a chunk behind, from the operand forms of W^T and X that the
-// four leave in shared memory (a quarter's rows under its own scales: the
-// sums over the quarters and blocks are put together in fp32), each for two of
-// the blocks, 0 and 3 or 1 and 2, the same share of the triangle M. The chunks'
-// images come by bulk copies through two rings of stages, K and H for the chain, Q
-// and M for Z, so that the chain's next images need not wait for Z. One thread of a
-// warp of its own fills each ring; with two groups a block, where the registers of
-// twelve warps are all there are, the first Z warp of each group does it between
-// its steps. Column groups know nothing of one another. V comes through registers,
-// one chunk ahead.
+// This chain is what bounds the scan, so all else is off it. Four more warps, a block
+// of tokens each, form Z up to two chunks behind, from the operand forms of W^T and
+// X that the chain leaves in shared memory (a quarter's rows under its own scales:
+// the sums over the quarters and blocks are put together in fp32). One brings V to
+// shared memory up to two chunks ahead. The chunks' images come by bulk copies
+// through two rings of stages, K and H for the chain, Q and M for Z, so that the
+// chain's next images need not wait for Z; one thread of a warp of its own fills
+// each ring. The last warp, the gate, does the chain's waiting: a wait on an
+// mbarrier costs a warp about 150 cycles even when nothing is waited for.
 template <int DK, bool BF16, int MODE>
 __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
-    extern __shared__ __align__(1024) char ssm[];
+    extern __shared__ __align__(128) char ssm[];
     __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4];
-    __shared__ uint64_t zready[2][2], zfree[2][2];  // [group][turn]
+    __shared__ uint64_t tready[2], zready[2];  // for the chunks in turn
     __shared__ int abort_flag;
     constexpr bool ZF = MODE == kZ32, SAVE = MODE == kSave;
     constexpr int STAGE = chain_stage_bytes<DK, BF16>(), ZSTAGE = z_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
     constexpr int NT = DK / 32, KK = DK / 64;  // 8-column tiles and 16-deep steps of a quarter
-    const int groups = a.dv / (16 * a.cgs);
+    const int groups = a.dv / 16;
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = warp & 3;
-    const bool chain = warp < 4 * a.cgs;
-    const int extra = warp - 4 * a.cgs, cg = chain ? warp >> 2 : extra >> 1;
     int t0, len;
     delta_span(a.seq_start, n, a.T, t0, len);
     const int nchunk = (len + C - 1) / C;
@@ -540,28 +567,65 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
         abort_flag = 0;
         for (int s = 0; s < 4; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4 * a.cgs);
+            mbar_init(&empty[s], 1);
             mbar_init(&zfull[s], 1);
-            mbar_init(&zempty[s], 2 * a.cgs);
+            mbar_init(&zempty[s], 4);
         }
-        for (int g = 0; g < 2; ++g)
-            for (int t = 0; t < 2; ++t) {
-                mbar_init(&zready[g][t], 4);
-                mbar_init(&zfree[g][t], 2);
-            }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&tready[t], SAVE ? 32 : 36);  // V is there (a warp), the four Z warps are done
+            mbar_init(&zready[t], 4);
+        }
         fence_mbar_init();
     }
     __syncthreads();
 
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = (grp * a.cgs + cg) * 16;
+    const int v0 = grp * 16;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
-    char *zst = ssm + a.stages * STAGE, *area = zst + a.zstages * ZSTAGE + cg * scan_group_bytes<DK, MODE>();
+    char *zst = ssm + a.stages * STAGE, *area = zst + a.zstages * ZSTAGE;
     auto wait = [&](uint64_t *bar, int parity) {
         return mbar_wait_warp(bar, parity, abort, a.status, kScanStatus);
     };
 
-    if (!chain) {  // ------------------------------------------------ Z, and the rings
+    // what the chunks in turn keep: V, X's terms, 1 / scales, W^T's terms
+    auto turn_at = [&](int turn) { return area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>(); };
+
+    if (warp == 11) {  // ------------------------------------------------ the gate
+        // Waits for all that a chunk needs and then meets the chain, which so waits on
+        // nothing but barriers; at the next meeting the chain is done with the stage.
+        Ring ring(a.stages);
+        int last = 0;
+        for (int c = 0; c < nchunk; ++c, ring.next()) {
+            const bool ok = wait(&full[ring.s], ring.ph) && wait(&tready[c & 1], (c >> 1) & 1);
+            if (named_bar_or(2, 160, !ok)) return;
+            if (c > 0 && lane == 0) mbar_arrive(&empty[last]);
+            last = ring.s;
+        }
+        return;
+    }
+    if (warp == 10) {  // ------------------------------------------------ V ahead
+        // Rows of 16 columns by 16-byte asynchronous copies, zeros behind the sequence;
+        // each lane's arrival follows its copies.
+        constexpr int U = BF16 ? 4 : 8, PER = BF16 ? 2 : 4;  // units of a lane, of a row
+        const size_t v_at = (vrow * a.dv + v0) * (BF16 ? 2 : 4);
+        const char *src = static_cast<const char *>(a.V) + v_at;
+        const size_t ld = (size_t)a.dv * (BF16 ? 2 : 4);
+        for (int c = 0; c < nchunk; ++c) {
+            // X of the chunk two before is formed: its V has been read
+            if (c >= 2 && !wait(&zready[c & 1], ((c >> 1) & 1) ^ 1)) break;
+            const uint32_t d = smem_u32(turn_at(c & 1));
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int u = lane + 32 * i, row = u / PER, part = u % PER, t = c * C + row;
+                const bool in = t < len;
+                cp_async16(d + v_off<BF16>(row, part), src + (in ? t * ld : 0) + part * 16, in);
+            }
+            cp_async_arrive(&tready[c & 1]);
+        }
+        cp_async_wait_all();
+        return;
+    }
+    if (warp >= 8) {  // ------------------------------------------------ the rings
         auto chain_copy = [&](int c, int s, uint64_t *bar) {
             char *d = ssm + s * STAGE;
             const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
@@ -579,204 +643,137 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             bulk_load(d + ZSTAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes + kHalfVecBytes,
                       kHalfVecBytes, bar);
         };
-        Filler<decltype(chain_copy)> fill(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
-        Filler<decltype(z_copy)> zfill(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
-        const int own = SAVE ? 0 : a.cgs == 1 ? 2 : -1;  // the first warp that only fills, if any
-        if (own >= 0 && extra >= own) {
-            if (lane == 0) {
-                if (extra == own) {
-                    while (fill.filled < nchunk && fill.next()) {
-                    }
-                    if (*abort) fill.drain();
-                } else {
-                    while (zfill.filled < nchunk && zfill.next()) {
-                    }
-                    if (*abort) zfill.drain();
-                }
+        if (lane == 0 && warp == 8) {
+            Filler<decltype(chain_copy)> f(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
+            while (f.filled < nchunk && f.next()) {
             }
-            return;
+            if (*abort) f.drain();
         }
-        const bool fills = own < 0 && lane == 0 && extra == 0, zfills = own < 0 && lane == 0 && extra == 2;
-        auto poll = [&]() {
-            if (fills) fill.poll();
-            if (zfills) zfill.poll();
-            __syncwarp();
-        };
-        const int half = extra & 1;
+        if (lane == 0 && warp == 9 && !SAVE) {
+            Filler<decltype(z_copy)> f(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
+            while (f.filled < nchunk && f.next()) {
+            }
+            if (*abort) f.drain();
+        }
+        return;
+    }
+
+    if (warp >= 4) {  // ------------------------------------------------ Z behind
+        if (SAVE) return;
+        if (lane == 0) mbar_arrive(&tready[0]), mbar_arrive(&tready[1]);  // nothing to be done with yet
         Ring ring(a.zstages);
         for (int c = 0; c < nchunk; ++c, ring.next()) {
             const int turn = c & 1;
-            poll();
-            // what this step itself needs has to be on its way before it is waited for
-            const bool lost = (fills && fill.filled == c && !fill.next()) ||
-                              (zfills && zfill.filled == c && !zfill.next());
-            if (__any_sync(0xffffffffu, lost)) break;
             const uint32_t uQ = smem_u32(zst + ring.s * ZSTAGE), uM = uQ + KALL;
             // the enum's order, counted from kVq on
             const float *vec = reinterpret_cast<const float *>(zst + (ring.s + 1) * ZSTAGE - kHalfVecBytes) - kVq * C;
-            const char *at = area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>();
-            const uint4 *xfr = reinterpret_cast<const uint4 *>(at) + lane;             // [block][hi, lo][32]
-            const float *iXs = reinterpret_cast<const float *>(at + 4096), *iSs = iXs + 64;
-            const uint4 *sfr = reinterpret_cast<const uint4 *>(at + 4096 + 512) + lane;  // [step][hi, (lo)][32]
-            if (!wait(&zfull[ring.s], ring.ph)) break;
-            bool ok = false;
-            if (own < 0) {  // the chain may need its next images first
-                for (int tries = 0; tries < 64 && !ok; ++tries) {
-                    ok = __all_sync(0xffffffffu, mbar_test(&zready[cg][turn], (c >> 1) & 1));
-                    poll();
-                }
-            }
-            if (!ok && !wait(&zready[cg][turn], (c >> 1) & 1)) break;
-            float Z[2][2][4] = {}, ZM[2][2][4] = {};
-            // (Q W)^T of the two blocks, quarter by quarter
+            const char *at = turn_at(turn);
+            const uint4 *xfr = reinterpret_cast<const uint4 *>(at + 4096) + lane;        // [block][hi, lo][32]
+            const float *iXs = reinterpret_cast<const float *>(at + 8192), *iSs = iXs + 64;
+            const uint4 *sfr = reinterpret_cast<const uint4 *>(at + 8192 + 512) + lane;  // [step][hi, (lo)][32]
+            if (!wait(&zfull[ring.s], ring.ph) || !wait(&zready[turn], (c >> 1) & 1)) return;
+            float Z[2][4] = {}, ZM[2][4] = {};
+            // (Q W)^T of block p, quarter by quarter
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                float z[2][2][4] = {};
+                float z[2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
                     const uint4 fh = d[0];
                     const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
-                    uint32_t bb[2][4];
+                    uint32_t bb[4];
+                    load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        load_b(bb[y], uQ, 16 * (half ? 1 + y : 3 * y), w * (DK / 4) + 16 * kk, lane);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[y][x], hi, bb[y][2 * x], bb[y][2 * x + 1]);
+                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
                     if (ZF) {
                         const uint4 fl = d[32];
                         const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) mma_f16(z[y][x], lo, bb[y][2 * x], bb[y][2 * x + 1]);
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
                         if (!BF16) {
+                            load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                load_b(bb[y], uQ + KIMG, 16 * (half ? 1 + y : 3 * y),
-                                       w * (DK / 4) + 16 * kk, lane);
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    mma_f16(z[y][x], hi, bb[y][2 * x], bb[y][2 * x + 1]);
+                            for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
                         }
                     }
                 }
                 const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            Z[y][x][e] = fmaf(e < 2 ? i0 : i1, z[y][x][e], Z[y][x][e]);
+                    for (int e = 0; e < 4; ++e) Z[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], Z[x][e]);
             }
-            poll();
             // (M X)^T
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
+                if (jj > p) continue;  // M_ij is zero for i < j; the same for the whole warp
                 const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
                 const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
                 const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int i = half ? 1 + y : 3 * y;
-                    if (jj > i) continue;  // M_ij is zero for i < j; the same for the whole warp
-                    float z[2][4] = {};
-                    uint32_t bm[4];
-                    load_b(bm, uM, 16 * i, 16 * jj, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
-                    }
-                    if (ZF) {
-                        load_b(bm, uM + kImg, 16 * i, 16 * jj, lane);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            ZM[y][x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], ZM[y][x][e]);
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
+                float z[2][4] = {};
+                uint32_t bm[4];
+                load_b(bm, uM, 16 * p, 16 * jj, lane);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int i = 16 * (half ? 1 + y : 3 * y) + 8 * x + 2 * q4;
-                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i);
-                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i);
-                    float(&z)[4] = Z[y][x], (&u)[4] = ZM[y][x];
-                    z[0] = cq.x * z[0] + im.x * u[0], z[1] = cq.y * z[1] + im.y * u[1];
-                    z[2] = cq.x * z[2] + im.x * u[2], z[3] = cq.y * z[3] + im.y * u[3];
+                    mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                    if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
                 }
-            poll();
+                if (ZF) {
+                    load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ZM[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], ZM[x][e]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = 16 * p + 8 * x + 2 * q4;
+                const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i);
+                const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i);
+                float(&z)[4] = Z[x], (&u)[4] = ZM[x];
+                z[0] = cq.x * z[0] + im.x * u[0], z[1] = cq.y * z[1] + im.y * u[1];
+                z[2] = cq.x * z[2] + im.x * u[2], z[3] = cq.y * z[3] + im.y * u[3];
+            }
             // everything is read: the arrivals do not wait for the stores behind them
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&zfree[cg][turn]);
+                mbar_arrive(&tready[turn]);
                 mbar_arrive(&zempty[ring.s]);
             }
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = c * C + 16 * (half ? 1 + y : 3 * y) + 8 * x;
-                    const float(&z)[4] = Z[y][x];
-                    if (ZF) {
-                        const int t = i + 2 * q4;
-                        float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
-                        if (t < len) o[0] = z[0], o[8] = z[2];
-                        if (t + 1 < len) o[a.dv] = z[1], o[a.dv + 8] = z[3];
-                    } else {
-                        // 8 x 8 blocks transposed between the lanes: a token per row
-                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(z[0], z[1]);
-                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(z[2], z[3]);
-                        const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
-                        const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
-                        const int t = i + gq;
-                        if (t < len) {
-                            uint32_t *o = reinterpret_cast<uint32_t *>(
-                                static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
-                            o[0] = r0;
-                            o[4] = r1;
-                        }
+            for (int x = 0; x < 2; ++x) {
+                const int i = c * C + 16 * p + 8 * x;
+                const float(&z)[4] = Z[x];
+                if (ZF) {
+                    const int t = i + 2 * q4;
+                    float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
+                    if (t < len) o[0] = z[0], o[8] = z[2];
+                    if (t + 1 < len) o[a.dv] = z[1], o[a.dv + 8] = z[3];
+                } else {
+                    // 8 x 8 blocks transposed between the lanes: a token per row
+                    const __nv_bfloat162 p0 = __floats2bfloat162_rn(z[0], z[1]);
+                    const __nv_bfloat162 p1 = __floats2bfloat162_rn(z[2], z[3]);
+                    const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
+                    const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
+                    const int t = i + gq;
+                    if (t < len) {
+                        uint32_t *o = reinterpret_cast<uint32_t *>(
+                            static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
+                        o[0] = r0;
+                        o[4] = r1;
                     }
                 }
+            }
         }
-        if (fills && *abort) fill.drain();
-        if (zfills && *abort) zfill.drain();
         return;
     }
 
     // -------------------------------------------------------------- the chain
     float4 *part = reinterpret_cast<float4 *>(area) + lane;  // [to][from][tile][32]
-    // V of this lane's places in block p: tokens 16 p + 8 x + 2 q4 + {0, 1}, columns gq,
-    // gq + 8; kept as loaded: a conversion here would wait for the load
-    uint32_t v[2][4];
-    const size_t vlane = (vrow + 16 * p + 2 * q4) * a.dv + v0 + gq;
-    auto fetch_v = [&](int c) {
-        const int t = c * C + 16 * p + 2 * q4;
-        const size_t at = vlane + (size_t)c * C * a.dv;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[x][e] = 0;
-                if (t + 8 * x + (e & 1) < len) {
-                    const size_t i = at + (8 * x + (e & 1)) * a.dv + (e >> 1) * 8;
-                    v[x][e] = BF16 ? (uint32_t)static_cast<const uint16_t *>(a.V)[i]
-                                   : static_cast<const uint32_t *>(a.V)[i];
-                }
-            }
-    };
-    auto v_at = [&](int x, int e) { return __uint_as_float(BF16 ? v[x][e] << 16 : v[x][e]); };
     // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns k0 + 8 nt + 2 q4 + {0, 1}
     const int k0 = p * (DK / 4);
     float S[NT][4];
@@ -787,23 +784,32 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
-    if (nchunk > 0) fetch_v(0);
+
+    // W at the start of chunk c
+    auto save = [&](int c) {
+        float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+    };
+    if (SAVE && nchunk > 0) save(0);
 
     Ring ring(a.stages);
     for (int c = 0; c < nchunk; ++c, ring.next()) {
         const int turn = c & 1;
         const uint32_t uK = smem_u32(ssm + ring.s * STAGE), uH = uK + KALL;
         const float *vec = reinterpret_cast<const float *>(ssm + (ring.s + 1) * STAGE - kHalfVecBytes);
-        char *at = area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>();
-        uint4 *xfr = reinterpret_cast<uint4 *>(at) + lane;
-        float *iXs = reinterpret_cast<float *>(at + 4096), *iSs = iXs + 64;
-        uint4 *sfr = reinterpret_cast<uint4 *>(at + 4096 + 512) + lane;
-        bool ok = wait(&full[ring.s], ring.ph);
-        if (!SAVE && c >= 2) ok = ok && wait(&zfree[cg][turn], ((c >> 1) & 1) ^ 1);
+        char *at = turn_at(turn);
+        uint4 *xfr = reinterpret_cast<uint4 *>(at + 4096) + lane;
+        float *iXs = reinterpret_cast<float *>(at + 8192), *iSs = iXs + 64;
+        uint4 *sfr = reinterpret_cast<uint4 *>(at + 8192 + 512) + lane;
+        if (named_bar_or(2, 160, false)) return;  // with the gate; it says when a wait has run out
         // W^T K^T over this warp's quarter of DK, W^T's terms left for Z
-        if (ok) {
+        {
             float X[8][4] = {}, sS[2], iS[2];
-            uint32_t bb[KK][4][4];
+            uint32_t bb[KK][4][4], ah[KK][4], al[KK][4];
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -811,48 +817,53 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             row_scales<NT>(S, sS, iS);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                uint32_t hi[4], lo[4];
+                uint32_t(&hi)[4] = ah[kk], (&lo)[4] = al[kk], (&b)[4][4] = bb[kk];
                 a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
+                    mma_f16(X[nt], hi, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], lo, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
+                    mma_f16(X[nt], lo, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
                 if (!BF16) {
 #pragma unroll
                     for (int np = 0; np < 4; ++np)
-                        load_b(bb[kk][np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
+                        load_b(b[np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt)
-                        mma_f16(X[nt], hi, bb[kk][nt >> 1][2 * (nt & 1)], bb[kk][nt >> 1][2 * (nt & 1) + 1]);
-                }
-                if (!SAVE) {
-                    uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (p * KK + kk);
-                    d[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (ZF) d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        mma_f16(X[nt], hi, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
                 }
             }
-            if (!SAVE && q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
+            if (!SAVE) {
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (p * KK + kk);
+                    d[0] = make_uint4(ah[kk][0], ah[kk][1], ah[kk][2], ah[kk][3]);
+                    if (ZF) d[32] = make_uint4(al[kk][0], al[kk][1], al[kk][2], al[kk][3]);
+                }
+                if (q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
+            }
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
                 part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
                     iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
         }
-        // the first meeting; all leave together when a wait has run out
-        if (named_bar_or(1 + cg, 128, !ok)) return;
+        named_bar(1, 128);  // the first meeting
         // X of block p, in operand form
         {
             float X[2][4];
+            float4 v4[2];
+            load_v<BF16>(v4, at, 16 * p, lane);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
                 const float4 o0 = part[32 * (8 * p + x)], o1 = part[32 * (8 * p + 2 + x)],
                              o2 = part[32 * (8 * p + 4 + x)], o3 = part[32 * (8 * p + 6 + x)];
-                X[x][0] = v_at(x, 0) - ck.x * ((o0.x + o1.x) + (o2.x + o3.x));
-                X[x][1] = v_at(x, 1) - ck.y * ((o0.y + o1.y) + (o2.y + o3.y));
-                X[x][2] = v_at(x, 2) - ck.x * ((o0.z + o1.z) + (o2.z + o3.z));
-                X[x][3] = v_at(x, 3) - ck.y * ((o0.w + o1.w) + (o2.w + o3.w));
+                const float4 v = v4[x];
+                X[x][0] = v.x - ck.x * ((o0.x + o1.x) + (o2.x + o3.x));
+                X[x][1] = v.y - ck.y * ((o0.y + o1.y) + (o2.y + o3.y));
+                X[x][2] = v.z - ck.x * ((o0.z + o1.z) + (o2.z + o3.z));
+                X[x][3] = v.w - ck.y * ((o0.w + o1.w) + (o2.w + o3.w));
             }
             float sX[2], iX[2];
             uint32_t hi[4], lo[4];
@@ -861,26 +872,20 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
-            if (!SAVE) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&zready[cg][turn]);
-            } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&zready[turn]);
+            if (SAVE) {
                 float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + gq;
-                float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         wx[(size_t)(8 * x + (e & 1)) * a.dv + (e >> 1) * 8] = X[x][e];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
             }
         }
-        // H of the first half of the tokens and the next V, in the shadow of the meeting
-        uint32_t bh[2][KK][4], bl[2][KK][4];
+        // H's first fragments, in the shadow of the meeting
+        constexpr int HA = 2;  // blocks of tokens whose fragments are at hand
+        uint32_t bh[HA][KK][4], bl[HA][KK][4];
         auto load_h = [&](int y, int jj) {
 #pragma unroll
             for (int np = 0; np < KK; ++np) {
@@ -888,15 +893,14 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                 load_bt(bl[y][np], uH + KIMG, 16 * jj, k0 + 16 * np, lane);
             }
         };
-        load_h(0, 0);
-        load_h(1, 1);
+#pragma unroll
+        for (int jj = 0; jj < HA; ++jj) load_h(jj, jj);
         const float gam = vec[kVs * C];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
-        if (c + 1 < nchunk) fetch_v(c + 1);
-        named_bar(1 + cg, 128);  // the second meeting
+        named_bar(1, 128);  // the second meeting
 
         // W'^T = exp(G_C) W^T + X^T H
 #pragma unroll
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
             const float iH = vec[kVs * C + 1 + jj];
             const float u0 = iXs[16 * jj + gq] * iH, u1 = iXs[16 * jj + gq + 8] * iH;
-            uint32_t(&h2)[KK][4] = bh[jj & 1], (&l2)[KK][4] = bl[jj & 1];
+            uint32_t(&h2)[KK][4] = bh[jj % HA], (&l2)[KK][4] = bl[jj % HA];
             float U[NT][4] = {};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -916,7 +920,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 mma_f16(U[nt], hi, l2[nt >> 1][2 * (nt & 1)], l2[nt >> 1][2 * (nt & 1) + 1]);
-            if (jj < 2) load_h(jj, jj + 2);
+            if (jj + HA < 4) load_h(jj % HA, jj + HA);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 S[nt][0] = fmaf(u0, U[nt][0], S[nt][0]);
@@ -925,8 +929,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                 S[nt][3] = fmaf(u1, U[nt][3], S[nt][3]);
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[ring.s]);
+        if (SAVE && c + 1 < nchunk) save(c + 1);
     }
 
     if (a.W_out) {
@@ -954,20 +957,19 @@ cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
 template <int DK, bool BF16, int MODE>
 cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
     constexpr int stage = chain_stage_bytes<DK, BF16>(), zstage = z_stage_bytes<DK, BF16, MODE>();
-    constexpr int group = scan_group_bytes<DK, MODE>(), most = 225 * 1024;
-    r.cgs = scan_groups((long long)N * r.H, r.dv);
-    // two stages of each ring if that can be, so that the next chunk is loaded during
-    // this one; then a third of the chain's
-    if (2 * (stage + zstage) + r.cgs * group > most) r.cgs = 1;
-    r.stages = r.zstages = 2 * (stage + zstage) + r.cgs * group > most ? 1 : 2;
-    if (r.stages == 2 && 3 * stage + 2 * zstage + r.cgs * group <= most) r.stages = 3;
-    const int smem = r.stages * stage + r.zstages * zstage + r.cgs * group;
+    constexpr int area = scan_area_bytes<DK, MODE>();
+    // two stages of the chain's ring at least (the gate frees one when the chain has
+    // met it for the next), two of Z's or a third of the chain's where there is room
+    static_assert(2 * stage + zstage + area <= kScanSmem, "shared memory");
+    r.stages = 2;
+    r.zstages = 2 * (stage + zstage) + area <= kScanSmem ? 2 : 1;
+    if (3 * stage + 2 * zstage + area <= kScanSmem) r.stages = 3;
+    const int smem = r.stages * stage + r.zstages * zstage + area;
     static SmemOnce once;
-    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, most);
+    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, kScanSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * r.cgs)));
-    const int warps = MODE == kSave ? 4 * r.cgs + 1 : r.cgs == 1 ? 8 : 12;
-    delta_scan_kernel<DK, BF16, MODE><<<grid, 32 * warps, smem, s>>>(r);
+    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / 16));
+    delta_scan_kernel<DK, BF16, MODE><<<grid, 384, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
@@ -995,20 +997,10 @@ cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cud
     return a.bf16 ? prep_inst<128, true>(r, blocks, s) : prep_inst<128, false>(r, blocks, s);
 }
 
-// Column groups of a block (one block per SM): the fewest rounds of blocks over
-// the 148 SMs win, a round of two-group blocks counted 1.4 times.
-int scan_groups(long long heads, int dv) {
-    const char *f = getenv("DSHAPE");
-    if (f) return f[0] - '0';
-    const double one = (double)((heads * (dv / 16) + 147) / 148);
-    const double two = (double)((heads * (dv / 32) + 147) / 148) * 1.4;
-    return two < one ? 2 : 1;
-}
-
 cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
                         cudaStream_t s) {
     const ScanArgs r{a.V, a.W0, a.Z, a.W_out, a.seq_start, a.B, a.Hk, a.H, a.T, a.dv,
-                     a.w0_per_seq ? a.H : 0, 0, 0, 0, im, saveS, saveX, device_status_word()};
+                     a.w0_per_seq ? a.H : 0, 0, 0, im, saveS, saveX, device_status_word()};
     if (a.dk == 64)
         return a.bf16 ? scan_mode<64, true>(r, a.N, mode, s) : scan_mode<64, false>(r, a.N, mode, s);
     return a.bf16 ? scan_mode<128, true>(r, a.N, mode, s) : scan_mode<128, false>(r, a.N, mode, s);

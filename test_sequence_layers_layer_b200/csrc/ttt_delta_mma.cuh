@@ -126,6 +126,7 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+constexpr int kScanSmem = 231936;  // dynamic shared memory a scan may take (227 KB less its barriers)
 constexpr int kScanStatus = 61;  // a wait of the scans has run out
 
 // Place in a ring of stages: the stage and the parity of its use, without divisions.
@@ -154,10 +155,6 @@ struct Filler {
         copy(filled, to.s, &full[to.s]);
         ++filled;
         to.next();
-    }
-    // All steps that have a free stage, without waiting.
-    __device__ __forceinline__ void poll() {
-        while (filled < steps && (filled < to.stages || mbar_test(&empty[to.s], to.ph ^ 1))) put();
     }
     // The next step, waiting for its stage; false when a wait has run out.
     __device__ __forceinline__ bool next() {
@@ -278,7 +275,6 @@ struct SmemOnce {
 // The shared part of the chunk preparation's launch (ttt_delta_chunk.cu).
 cudaError_t launch_prep(const DeltaArgs &a, const Plan &p, const Images &im, cudaStream_t s);
 Images images_at(const Plan &p, void *workspace, bool bwd);
-int scan_groups(long long heads, int dv);
 cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *saveS, float *saveX,
                         cudaStream_t s);
 

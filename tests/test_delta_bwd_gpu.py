@@ -14,6 +14,14 @@ from oracle import delta as od
 from test_delta_gpu import err, make, offsets
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    assert ttt.ttt_device_status() == 0
+
+
 TOL = 5e-5
 
 

@@ -16,6 +16,14 @@ import test_sequence_layers_layer_b200 as ttt
 from oracle import delta as od
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    assert ttt.ttt_device_status() == 0
+
+
 F32_TOL = 2e-5
 BF16_TOL = 2.0 ** -8 + 2.0 ** -9
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}

@@ -16,6 +16,14 @@ import test_sequence_layers_layer_b200 as ttt
 from oracle import delta as od
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    assert ttt.ttt_device_status() == 0
+
+
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 TOL, SUM_TOL = 1e-5, 3e-5
 PARAMS = ("scale", "gamma1", "beta1", "gamma2", "beta2")
