@@ -91,22 +91,26 @@ __device__ __forceinline__ void convert_rows(const void *src, size_t row0, int l
 
 constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices (floats)
 
+// Vectors of the preparation: 1 / scales of K and Q, sums of decays as two floats,
+// eta / sK, and of the decays what the triangle needs (below), u, 1 / scales of T.
+enum PrepVec { kPiK, kPiQ, kPGh, kPGl, kPek, kProw, kPcol, kPu = kPcol + 3, kPiT, kPrepVecs };
+
 // Shared memory: K and Q images, A and T in fp32; the images that go out take
 // the places of what is no longer needed (T's terms and then M over A, H's high
 // terms over Q, its low terms over T).
 template <int DK, bool BF16>
 constexpr int prep_smem() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * 5 * C + 4 * 3 * 16 * 18;
+    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * kPrepVecs * C + 4 * 3 * 16 * 18;
 }
 
-// T = (I + L)^-1 for L strictly lower triangular, by 16 x 16 blocks in fp32: the four
-// diagonal blocks by forward substitution (a lane per column), then the blocks
-// below the diagonal, those nearest to it first:
+// T = (I + L)^-1 for L strictly lower triangular, by 16 x 16 blocks in fp32, by 128
+// threads (named barrier `bar`): the four diagonal blocks by forward substitution
+// (a lane per column), then the blocks below the diagonal, those nearest to it first:
 //   T_ab = -T_aa sum_{b <= c < a} L_ac T_cb.
-// Leaves the upper blocks of T as they are. Barriers inside; Y: 3 x 16 x 18 floats.
-__device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp < 4 && lane < 16) {
+// Leaves the upper blocks of T as they are. Y: 3 x 16 x 18 floats.
+__device__ __forceinline__ void invert(const float *L, float *T, float *Y, int tid, int bar) {
+    const int warp = tid >> 5, lane = tid & 31;
+    if (lane < 16) {
         const float *l = L + 16 * warp * kLd + 16 * warp;
         float x[16];
 #pragma unroll
@@ -124,12 +128,12 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kLd + 16 * warp + lane] = x[i];
     }
-    __syncthreads();
-    // half of the threads a block, two outputs each
-    const int side = tid >> 7, r = (tid & 127) >> 3, c = (tid & 7) * 2;
+    named_bar(bar, 128);
+    const int r = tid >> 3, c = (tid & 7) * 2;  // every thread two outputs of each block
 #pragma unroll
     for (int dist = 1; dist < 4; ++dist) {
-        for (int b = side; b < 4 - dist; b += 2) {
+#pragma unroll
+        for (int b = 0; b < 4 - dist; ++b) {
             float y0 = 0.f, y1 = 0.f;
             const float *l = L + (16 * (b + dist) + r) * kLd + 16 * b;
             const float *t = T + 16 * b * kLd + 16 * b + c;
@@ -146,8 +150,9 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
             }
             *reinterpret_cast<float2 *>(Y + (b * 16 + r) * 18 + c) = make_float2(y0, y1);
         }
-        __syncthreads();
-        for (int b = side; b < 4 - dist; b += 2) {
+        named_bar(bar, 128);
+#pragma unroll
+        for (int b = 0; b < 4 - dist; ++b) {
             float y0 = 0.f, y1 = 0.f;
             const float *t = T + (16 * (b + dist) + r) * kLd + 16 * (b + dist);
 #pragma unroll
@@ -164,13 +169,16 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y) {
             *reinterpret_cast<float2 *>(T + (16 * (b + dist) + r) * kLd + 16 * b + c) =
                 make_float2(y0, y1);
         }
-        __syncthreads();
+        named_bar(bar, 128);
     }
 }
 
 // One block per chunk and key head, its value heads one after the other. Warps
-// 0..3 work for Z (q_i.k_j, P, M), warps 4..7 for the weight (k_i.k_j, A, H), 16 rows
-// each; the inverse between them takes all.
+// 0..3 work for Z (q_i.k_j, P, T's terms, M), warps 4..7 for the weight (k_i.k_j, A, T,
+// H), 16 rows each. The decays Gam_ij of a block below the diagonal come as
+// products of two factors that are at most 1, around the last token r before the rows'
+// block: exp(G_i - G_r) exp(G_r - G_j); only the diagonal blocks take an exponential
+// an element.
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a) {
     extern __shared__ __align__(128) char psm[];
@@ -178,7 +186,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
     char *sK = psm, *sQ = sK + IMG;
     float *L = reinterpret_cast<float *>(sQ + IMG);  // A of the chunk, row-major
     float *T = L + C * kLd;
-    float *iK = T + C * kLd, *iQ = iK + C, *Gh = iQ + C, *Gl = Gh + C, *eta = Gl + C, *Y = eta + C;
+    float *pv = T + C * kLd, *Y = pv + kPrepVecs * C;
+    const float *iK = pv + kPiK * C, *iQ = pv + kPiQ * C, *Gh = pv + kPGh * C, *Gl = pv + kPGl * C,
+                *ek = pv + kPek * C, *it = pv + kPiT * C, *u = pv + kPu * C;
     char *sT = reinterpret_cast<char *>(L);   // T's two terms, then M's
     char *sHl = reinterpret_cast<char *>(T);  // H's low terms; its high terms over Q
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -190,8 +200,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
     const bool forw = warp >= 4;  // works for the weight
     const size_t kslot = (size_t)slot * a.Hk + hk;
     const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;
-    if (forw) convert_rows<DK, BF16>(a.K, krow, len, sK, a.im.K + kslot * a.im.kimg, iK, tid & 127);
-    else convert_rows<DK, BF16>(a.Q, krow, len, sQ, a.im.Q + kslot * a.im.kimg, iQ, tid);
+    if (forw)
+        convert_rows<DK, BF16>(a.K, krow, len, sK, a.im.K + kslot * a.im.kimg, pv + kPiK * C, tid & 127);
+    else
+        convert_rows<DK, BF16>(a.Q, krow, len, sQ, a.im.Q + kslot * a.im.kimg, pv + kPiQ * C, tid);
     __syncthreads();
 
     // k_i.k_j or q_i.k_j of this warp's 16 rows i, columns j up to the diagonal
@@ -226,7 +238,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
         const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
         const size_t hslot = (size_t)slot * a.H + h;
         float *vec = reinterpret_cast<float *>(a.im.vec + hslot * kVecBytes);
-        if (r > 0 && tid == 0) bulk_wait_read<0>();  // the head before has gone out
+        if (r > 0 && (tid == 0 || tid == 128)) bulk_wait_read<0>();  // the head before has gone out
         if (warp == 0) {
             // sums of decays in double, handed on as two floats: differences of
             // sums stay exact to the last bit of the decays. A decay below -200
@@ -243,101 +255,200 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
             double base = s[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double u = __shfl_up_sync(0xffffffffu, base, o);
-                if (lane >= o) base += u;
+                const double v = __shfl_up_sync(0xffffffffu, base, o);
+                if (lane >= o) base += v;
             }
             base -= s[1];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const double G = base + s[x];
                 const float hi = (float)G;
-                Gh[2 * lane + x] = hi;
-                Gl[2 * lane + x] = (float)(G - (double)hi);
+                pv[kPGh * C + 2 * lane + x] = hi;
+                pv[kPGl * C + 2 * lane + x] = (float)(G - (double)hi);
             }
-        } else if (warp == 1) {
+        }
+        __syncthreads();
+        if (tid < 2 * C) {
+            const int j = tid & 63;
+            const float hj = Gh[j], lj = Gl[j];
+            auto from = [&](int i) { return expf((Gh[i] - hj) + (Gl[i] - lj)); };
+            const float eta = j < len ? a.eta[hrow + j] : 0.f, e = eta * iK[j];
+            if (tid < C) {
+                const float dec = expf(hj + lj);
+                pv[kPek * C + j] = e;
+                const int q = j < 16 ? j : (j & ~15) - 1;
+                pv[kProw * C + j] = expf((hj - Gh[q]) + (lj - Gl[q]));
+                pv[kPu * C + j] = from(C - 1) * e;
+                vec[kVk * C + j] = dec * iK[j];
+                vec[kVq * C + j] = a.q_scale * dec * iQ[j];
+                if (j == 0) vec[kVs * C] = expf(Gh[C - 1] + Gl[C - 1]);
+            } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = 2 * lane + x;
-                eta[t] = t < len ? a.eta[hrow + t] : 0.f;
+                for (int y = 0; y < 3; ++y)  // around the last token before block y + 1
+                    pv[(kPcol + y) * C + j] = j < 16 * (y + 1) ? from(16 * y + 15) * e : 0.f;
+                vec[kVik * C + j] = iK[j];
+                vec[kViq * C + j] = iQ[j];
+                vec[kVgh * C + j] = hj;
+                vec[kVgl * C + j] = lj;
             }
         }
         __syncthreads();
 
         // A (to shared memory) or P (kept) from the products
         float P[8][4];
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) P[nt][e] = 0.f;
-            if (nt >= 2 * mt + 2) continue;  // above the diagonal
-            const int j0 = 8 * nt + 2 * q4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * mt + gq + (e >> 1) * 8, j = j0 + (e & 1);
-                if (forw ? j < i : j <= i) {
-                    const float gam = expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j])) * eta[j] * iK[j];
-                    P[nt][e] = gam * (kk[nt][e] * (forw ? iK[i] : iQ[i]));
-                    if (!forw) P[nt][e] *= a.q_scale;
-                }
-            }
-            if (forw) {
-                float *l = L + (16 * mt + gq) * kLd + j0;
-                *reinterpret_cast<float2 *>(l) = make_float2(P[nt][0], P[nt][1]);
-                *reinterpret_cast<float2 *>(l + 8 * kLd) = make_float2(P[nt][2], P[nt][3]);
-            }
-        }
-        if (tid < C) {
-            const float dec = expf(Gh[tid] + Gl[tid]);
-            vec[kVk * C + tid] = dec * iK[tid];
-            vec[kVq * C + tid] = a.q_scale * dec * iQ[tid];
-            vec[kVik * C + tid] = iK[tid];
-            vec[kViq * C + tid] = iQ[tid];
-            vec[kVgh * C + tid] = Gh[tid];
-            vec[kVgl * C + tid] = Gl[tid];
-        }
-        __syncthreads();
-        invert(L, T, Y);
-
-        // T's terms, row by row (over A); what T's rows were divided by goes to `it`
-        float *it = Y;
         {
-            const int row = tid >> 2, side = tid & 3;
-            const float *t = T + row * kLd + 16 * side;
-            float v[16], m = 0.f;
+            const int i0 = 16 * mt + gq, i1 = i0 + 8;
+            const float si[2] = {forw ? iK[i0] : a.q_scale * iQ[i0], forw ? iK[i1] : a.q_scale * iQ[i1]};
+            const float ri[2] = {si[0] * pv[kProw * C + i0], si[1] * pv[kProw * C + i1]};
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-                const float4 u = *reinterpret_cast<const float4 *>(t + j);
-                v[j] = u.x, v[j + 1] = u.y, v[j + 2] = u.z, v[j + 3] = u.w;
-            }
+            for (int nt = 0; nt < 8; ++nt) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (16 * side + j > row) v[j] = 0.f;
-                m = fmaxf(m, fabsf(v[j]));
-            }
-            float s, is;
-            pow2_scale(quad_max(m), s, is);
+                for (int e = 0; e < 4; ++e) P[nt][e] = 0.f;
+                const int j0 = 8 * nt + 2 * q4;
+                if (nt < 2 * mt) {  // below the diagonal blocks
+                    const float2 cj = *reinterpret_cast<const float2 *>(pv + (kPcol + mt - 1) * C + j0);
+                    P[nt][0] = kk[nt][0] * ri[0] * cj.x, P[nt][1] = kk[nt][1] * ri[0] * cj.y;
+                    P[nt][2] = kk[nt][2] * ri[1] * cj.x, P[nt][3] = kk[nt][3] * ri[1] * cj.y;
+                } else if (nt < 2 * mt + 2) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    split_f16(v[j + 2 * e] * s, v[j + 2 * e + 1] * s, hi[e], lo[e]);
-                const uint32_t o = img_off(row, 16 * side + j);
-                const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                *reinterpret_cast<uint4 *>(sT + o) = h4;
-                *reinterpret_cast<uint4 *>(sT + kImg + o) = l4;
-                if (a.im.T) {
-                    char *gT = a.im.T + hslot * 2 * kImg;
-                    *reinterpret_cast<uint4 *>(gT + o) = h4;
-                    *reinterpret_cast<uint4 *>(gT + kImg + o) = l4;
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = e < 2 ? i0 : i1, j = j0 + (e & 1);
+                        if (forw ? j < i : j <= i)
+                            P[nt][e] = kk[nt][e] * si[e >> 1] * ek[j] * expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j]));
+                    }
+                }
+                if (forw && nt < 2 * mt + 2) {
+                    float *l = L + i0 * kLd + j0;
+                    *reinterpret_cast<float2 *>(l) = make_float2(P[nt][0], P[nt][1]);
+                    *reinterpret_cast<float2 *>(l + 8 * kLd) = make_float2(P[nt][2], P[nt][3]);
                 }
             }
-            if (side == 0) it[row] = is, vec[kVit * C + row] = is;
         }
-        __syncthreads();
 
-        if (!forw) {
+        if (forw) {
+            named_bar(2, 128);  // A is there
+            invert(L, T, Y, tid & 127, 2);
+            named_arrive(3, 256);  // T is there
+            // H = T^T diag(u) K: rows j of this warp, summed over tokens i >= j
+            // (T^T's elements are read twice, once for the rows' scales: registers are short)
+            float Hc[DK / 8][4] = {}, sA[2], iA[2];
+            auto tile = [&](int nt, float(&A)[4]) {
+                const int i = 8 * nt + 2 * q4;
+                const float2 ui = *reinterpret_cast<const float2 *>(u + i);
+                const float *t = T + i * kLd + 16 * mt + gq;
+                // inside the diagonal block T holds zeros above the diagonal
+                A[0] = ui.x * t[0], A[1] = ui.y * t[kLd];
+                A[2] = ui.x * t[8], A[3] = ui.y * t[kLd + 8];
+            };
+            {
+                float m[2] = {0.f, 0.f};
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    if (nt < 2 * mt) continue;
+                    float A[4];
+                    tile(nt, A);
+                    m[0] = fmaxf(m[0], fmaxf(fabsf(A[0]), fabsf(A[1])));
+                    m[1] = fmaxf(m[1], fmaxf(fabsf(A[2]), fabsf(A[3])));
+                }
+                pow2_scale(quad_max(m[0]), sA[0], iA[0]);
+                pow2_scale(quad_max(m[1]), sA[1], iA[1]);
+            }
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb < mt) continue;
+                uint32_t hi[4], lo[4];
+                float A0[4], A1[4];
+                tile(2 * kb, A0);
+                tile(2 * kb + 1, A1);
+                a_terms(A0, A1, sA, hi, lo);
+#pragma unroll
+                for (int np = 0; np < DK / 16; ++np) {
+                    uint32_t bb[4];
+                    load_bt(bb, uK, 16 * kb, 16 * np, lane);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(Hc[2 * np + x], lo, bb[2 * x], bb[2 * x + 1]);
+                    }
+                    if (!BF16) {
+                        load_bt(bb, uK + KIMG, 16 * kb, 16 * np, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
+                    }
+                }
+            }
+            // one scale for the 16 rows: they are one step of the sums over tokens
+            float m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < DK / 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e >> 1] = fmaxf(m[e >> 1], fabsf(Hc[nt][e]));
+            float mm = fmaxf(m[0] * iA[0], m[1] * iA[1]), sH, iH;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+            pow2_scale(mm, sH, iH);
+            if (lane == 0) vec[kVs * C + 1 + mt] = iH;
+            const float sHr[2] = {iA[0] * sH, iA[1] * sH};
+            named_bar(4, 256);  // T is read, by both sides
+#pragma unroll
+            for (int nt = 0; nt < DK / 8; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t hi, lo;
+                    split_f16(Hc[nt][2 * x] * sHr[x], Hc[nt][2 * x + 1] * sHr[x], hi, lo);
+                    const uint32_t o = img_off(16 * mt + gq + 8 * x, 8 * nt) + 4 * q4;
+                    *reinterpret_cast<uint32_t *>(sQ + o) = hi;
+                    *reinterpret_cast<uint32_t *>(sHl + o) = lo;
+                }
+            fence_async_smem();
+            named_bar(2, 128);
+            if (tid == 128) {
+                bulk_store(a.im.H + hslot * a.im.himg, sQ, KIMG);
+                bulk_store(a.im.H + hslot * a.im.himg + KIMG, sHl, KIMG);
+                bulk_commit();
+            }
+        } else {
+            named_bar(3, 256);  // T is there
+            // T's terms, row by row, over A
+            {
+                const int row = tid >> 1, side = tid & 1;
+                const float *t = T + row * kLd + 32 * side;
+                float v[32], m = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(t + j);
+                    v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (32 * side + j > row) v[j] = 0.f;
+                    m = fmaxf(m, fabsf(v[j]));
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                float s, is;
+                pow2_scale(m, s, is);
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        split_f16(v[j + 2 * e] * s, v[j + 2 * e + 1] * s, hi[e], lo[e]);
+                    const uint32_t o = img_off(row, 32 * side + j);
+                    const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    const uint4 l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(sT + o) = h4;
+                    *reinterpret_cast<uint4 *>(sT + kImg + o) = l4;
+                    if (a.im.T) {
+                        char *gT = a.im.T + hslot * 2 * kImg;
+                        *reinterpret_cast<uint4 *>(gT + o) = h4;
+                        *reinterpret_cast<uint4 *>(gT + kImg + o) = l4;
+                    }
+                }
+                if (side == 0) pv[kPiT * C + row] = is, vec[kVit * C + row] = is;
+            }
+            named_bar(1, 128);
+            named_arrive(4, 256);  // T is read on this side
             // M = P T: rows i of this warp; T's row scales go into P's columns
             float M[8][4] = {}, sM[2], iM[2], sP[2], iP[2];
             const uint32_t uT = smem_u32(sT);
@@ -381,81 +492,15 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
                     *reinterpret_cast<uint32_t *>(sT + o) = hi;
                     *reinterpret_cast<uint32_t *>(sT + kImg + o) = lo;
                 }
-        } else {
-            // H = T^T diag(u) K: rows j of this warp, summed over tokens i >= j
-            float Hc[DK / 8][4] = {}, A[8][4] = {}, sA[2], iA[2];
-            const float GC = Gh[C - 1], GCl = Gl[C - 1];
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                if (nt < 2 * mt) continue;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = 8 * nt + 2 * q4 + x;
-                    const float u = expf((GC - Gh[i]) + (GCl - Gl[i])) * eta[i] * iK[i];
-                    const float *t = T + i * kLd + 16 * mt + gq;
-                    // inside the diagonal block T holds zeros above the diagonal
-                    A[nt][x] = u * t[0];
-                    A[nt][2 + x] = u * t[8];
-                }
+            fence_async_smem();
+            named_bar(1, 128);
+            if (tid == 0) {
+                bulk_store(a.im.M + hslot * 2 * kImg, sT, 2 * kImg);
+                bulk_commit();
             }
-            row_scales<8>(A, sA, iA);
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb < mt) continue;
-                uint32_t hi[4], lo[4];
-                a_terms(A[2 * kb], A[2 * kb + 1], sA, hi, lo);
-#pragma unroll
-                for (int np = 0; np < DK / 16; ++np) {
-                    uint32_t bb[4];
-                    load_bt(bb, uK, 16 * kb, 16 * np, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
-                        mma_f16(Hc[2 * np + x], lo, bb[2 * x], bb[2 * x + 1]);
-                    }
-                    if (!BF16) {
-                        load_bt(bb, uK + KIMG, 16 * kb, 16 * np, lane);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            mma_f16(Hc[2 * np + x], hi, bb[2 * x], bb[2 * x + 1]);
-                    }
-                }
-            }
-            // one scale for the 16 rows: they are one step of the sums over tokens
-            float m[2] = {0.f, 0.f};
-#pragma unroll
-            for (int nt = 0; nt < DK / 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m[e >> 1] = fmaxf(m[e >> 1], fabsf(Hc[nt][e]));
-            float mm = fmaxf(m[0] * iA[0], m[1] * iA[1]), sH, iH;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-            pow2_scale(mm, sH, iH);
-            if (lane == 0) vec[kVs * C + 1 + mt] = iH;
-            if (tid == 128) vec[kVs * C] = expf(GC + GCl);
-            const float sHr[2] = {iA[0] * sH, iA[1] * sH};
-            named_bar(2, 128);  // T is read
-#pragma unroll
-            for (int nt = 0; nt < DK / 8; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t hi, lo;
-                    split_f16(Hc[nt][2 * x] * sHr[x], Hc[nt][2 * x + 1] * sHr[x], hi, lo);
-                    const uint32_t o = img_off(16 * mt + gq + 8 * x, 8 * nt) + 4 * q4;
-                    *reinterpret_cast<uint32_t *>(sQ + o) = hi;
-                    *reinterpret_cast<uint32_t *>(sHl + o) = lo;
-                }
-        }
-        fence_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            bulk_store(a.im.M + hslot * 2 * kImg, sT, 2 * kImg);
-            bulk_store(a.im.H + hslot * a.im.himg, sQ, KIMG);
-            bulk_store(a.im.H + hslot * a.im.himg + KIMG, sHl, KIMG);
-            bulk_commit();
         }
     }
-    if (tid == 0) bulk_wait<0>();
+    if (tid == 0 || tid == 128) bulk_wait<0>();
 }
 
 // ---------------------------------------------------------------- scan

@@ -171,6 +171,11 @@ struct Filler {
     }
 };
 
+// Counts this warp in at a barrier that others wait at.
+__device__ __forceinline__ void named_arrive(int id, int nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // What a scan writes: Z as bf16, Z as fp32, or (for the backward) the weight
 // each chunk starts from and X.
 enum ScanMode { kZ16, kZ32, kSave };
