@@ -100,14 +100,14 @@ enum PrepVec { kPiK, kPiQ, kPGh, kPGl, kPek, kProw, kPcol, kPu = kPcol + 3, kPiT
 // terms over Q, its low terms over T).
 template <int DK, bool BF16>
 constexpr int prep_smem() {
-    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * kPrepVecs * C + 4 * 3 * 16 * 18;
+    return 2 * C * DK * 2 * (BF16 ? 1 : 2) + 2 * 4 * C * kLd + 4 * kPrepVecs * C + 4 * 32 * 36;
 }
 
-// T = (I + L)^-1 for L strictly lower triangular, by 16 x 16 blocks in fp32, by 128
-// threads (named barrier `bar`): the four diagonal blocks by forward substitution
-// (a lane per column), then the blocks below the diagonal, those nearest to it first:
-//   T_ab = -T_aa sum_{b <= c < a} L_ac T_cb.
-// Leaves the upper blocks of T as they are. Y: 3 x 16 x 18 floats.
+// T = (I + L)^-1 for L strictly lower triangular, in fp32, by 128 threads (named
+// barrier `bar`): the four 16 x 16 diagonal blocks by forward substitution (a lane per
+// column), then twice T_21 = -T_22 (L_21 T_11): for the two pairs of 16-blocks, and for
+// the pair of 32-blocks that they make. Writes the lower blocks and what lies above
+// the diagonal inside the 32 x 32 ones; Y: 32 x 36 floats.
 __device__ __forceinline__ void invert(const float *L, float *T, float *Y, int tid, int bar) {
     const int warp = tid >> 5, lane = tid & 31;
     if (lane < 16) {
@@ -116,59 +116,68 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y, int t
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i)  // row i of L as vectors: the same for all lanes
+        for (int i = 1; i < 16; ++i) {  // row i of L as vectors: the same for all lanes
+            float y = 0.f;              // two chains
 #pragma unroll
             for (int k4 = 0; k4 < i; k4 += 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(l + i * kLd + k4);
                 x[i] = fmaf(-v.x, x[k4], x[i]);
-                if (k4 + 1 < i) x[i] = fmaf(-v.y, x[k4 + 1], x[i]);
+                if (k4 + 1 < i) y = fmaf(v.y, x[k4 + 1], y);
                 if (k4 + 2 < i) x[i] = fmaf(-v.z, x[k4 + 2], x[i]);
-                if (k4 + 3 < i) x[i] = fmaf(-v.w, x[k4 + 3], x[i]);
+                if (k4 + 3 < i) y = fmaf(v.w, x[k4 + 3], y);
             }
+            x[i] -= y;
+        }
+        float *t = T + 16 * warp * kLd + 16 * warp + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) T[(16 * warp + i) * kLd + 16 * warp + lane] = x[i];
+        for (int i = 0; i < 16; ++i) t[i * kLd] = x[i];
+        if (!(warp & 1))  // above the pair's lower block: zeros, so that 32-blocks are whole
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t[i * kLd + 16] = 0.f;
     }
     named_bar(bar, 128);
-    const int r = tid >> 3, c = (tid & 7) * 2;  // every thread two outputs of each block
+    constexpr int kY = 36;
+    // R rows, four columns a thread: out = sign * X[rows][0 .. K) W[0 .. K)[cols]
+    auto product = [&](const float *X, int ldx, const float *W, int ldw, float *out, int ldo, int K,
+                       int r0, int rows, float sign) {
+        float acc[2][4] = {};
+#pragma unroll 4
+        for (int k = 0; k < K; k += 4) {
+            float4 x[2];
 #pragma unroll
-    for (int dist = 1; dist < 4; ++dist) {
+            for (int y = 0; y < 2; ++y)
+                if (y < rows) x[y] = *reinterpret_cast<const float4 *>(X + (r0 + y) * ldx + k);
 #pragma unroll
-        for (int b = 0; b < 4 - dist; ++b) {
-            float y0 = 0.f, y1 = 0.f;
-            const float *l = L + (16 * (b + dist) + r) * kLd + 16 * b;
-            const float *t = T + 16 * b * kLd + 16 * b + c;
+            for (int e = 0; e < 4; ++e) {
+                const float4 w = *reinterpret_cast<const float4 *>(W + (k + e) * ldw);
 #pragma unroll
-            for (int k = 0; k < 16 * dist; k += 4) {
-                const float4 l4 = *reinterpret_cast<const float4 *>(l + k);
-                const float lk[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 t2 = *reinterpret_cast<const float2 *>(t + (k + e) * kLd);
-                    y0 = fmaf(lk[e], t2.x, y0);
-                    y1 = fmaf(lk[e], t2.y, y1);
+                for (int y = 0; y < 2; ++y) {
+                    if (y >= rows) continue;
+                    const float f = e == 0 ? x[y].x : e == 1 ? x[y].y : e == 2 ? x[y].z : x[y].w;
+                    acc[y][0] = fmaf(f, w.x, acc[y][0]), acc[y][1] = fmaf(f, w.y, acc[y][1]);
+                    acc[y][2] = fmaf(f, w.z, acc[y][2]), acc[y][3] = fmaf(f, w.w, acc[y][3]);
                 }
             }
-            *reinterpret_cast<float2 *>(Y + (b * 16 + r) * 18 + c) = make_float2(y0, y1);
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            if (y < rows)
+                *reinterpret_cast<float4 *>(out + (r0 + y) * ldo) = make_float4(
+                    sign * acc[y][0], sign * acc[y][1], sign * acc[y][2], sign * acc[y][3]);
+    };
+    {  // two pairs of 16-blocks: 64 threads each, a row and four columns
+        const int pair = tid >> 6, r = (tid & 63) >> 2, c = (tid & 3) * 4, o = 32 * pair;
+        float *y = Y + 16 * pair * kY + c;
+        product(L + (o + 16) * kLd + o, kLd, T + o * kLd + o + c, kLd, y, kY, 16, r, 1, 1.f);
         named_bar(bar, 128);
-#pragma unroll
-        for (int b = 0; b < 4 - dist; ++b) {
-            float y0 = 0.f, y1 = 0.f;
-            const float *t = T + (16 * (b + dist) + r) * kLd + 16 * (b + dist);
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const float4 t4 = *reinterpret_cast<const float4 *>(t + k);
-                const float tk[4] = {t4.x, t4.y, t4.z, t4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 y2 = *reinterpret_cast<const float2 *>(Y + (b * 16 + k + e) * 18 + c);
-                    y0 = fmaf(-tk[e], y2.x, y0);
-                    y1 = fmaf(-tk[e], y2.y, y1);
-                }
-            }
-            *reinterpret_cast<float2 *>(T + (16 * (b + dist) + r) * kLd + 16 * b + c) =
-                make_float2(y0, y1);
-        }
+        product(T + (o + 16) * kLd + o + 16, kLd, y, kY, T + (o + 16) * kLd + o + c, kLd, 16, r, 1, -1.f);
+        named_bar(bar, 128);
+    }
+    {  // the pair of 32-blocks: two rows and four columns a thread
+        const int r = (tid >> 3) * 2, c = (tid & 7) * 4;
+        product(L + 32 * kLd, kLd, T + c, kLd, Y + c, kY, 32, r, 2, 1.f);
+        named_bar(bar, 128);
+        product(T + 32 * kLd + 32, kLd, Y + c, kY, T + 32 * kLd + c, kLd, 32, r, 2, -1.f);
         named_bar(bar, 128);
     }
 }
@@ -200,10 +209,45 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
     const bool forw = warp >= 4;  // works for the weight
     const size_t kslot = (size_t)slot * a.Hk + hk;
     const size_t krow = ((size_t)b * a.Hk + hk) * a.T + t0;
+    const int rep = a.H / a.Hk;
+    // the gates of a head: loaded a head ahead (the first with the rows)
+    float g2[2] = {0.f, 0.f}, eta1 = 0.f;
+    auto load_gates = [&](int h) {
+        const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
+        if (warp == 0)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) g2[x] = a.g && 2 * lane + x < len ? a.g[hrow + 2 * lane + x] : 0.f;
+        if (tid < 2 * C) eta1 = (tid & 63) < len ? a.eta[hrow + (tid & 63)] : 0.f;
+    };
+    load_gates(hk * rep);
+    // Sums of decays in double, handed on as two floats: differences of sums stay
+    // exact to the last bit of the decays. A decay below -200 is a factor of zero in
+    // fp32 and is held there, so that no sum is infinite and no difference NaN.
+    auto sum_gates = [&]() {
+        double s[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            s[x] = (double)(g2[x] < -200.f ? -200.f : g2[x]) + (x ? s[0] : 0.0);
+        double base = s[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double v = __shfl_up_sync(0xffffffffu, base, o);
+            if (lane >= o) base += v;
+        }
+        base -= s[1];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const double G = base + s[x];
+            const float hi = (float)G;
+            pv[kPGh * C + 2 * lane + x] = hi;
+            pv[kPGl * C + 2 * lane + x] = (float)(G - (double)hi);
+        }
+    };
     if (forw)
         convert_rows<DK, BF16>(a.K, krow, len, sK, a.im.K + kslot * a.im.kimg, pv + kPiK * C, tid & 127);
     else
         convert_rows<DK, BF16>(a.Q, krow, len, sQ, a.im.Q + kslot * a.im.kimg, pv + kPiQ * C, tid);
+    if (warp == 0) sum_gates();
     __syncthreads();
 
     // k_i.k_j or q_i.k_j of this warp's 16 rows i, columns j up to the diagonal
@@ -232,47 +276,20 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
         }
     }
 
-    const int rep = a.H / a.Hk;
     for (int r = 0; r < rep; ++r) {
         const int h = hk * rep + r;
-        const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
         const size_t hslot = (size_t)slot * a.H + h;
         float *vec = reinterpret_cast<float *>(a.im.vec + hslot * kVecBytes);
-        if (r > 0 && (tid == 0 || tid == 128)) bulk_wait_read<0>();  // the head before has gone out
-        if (warp == 0) {
-            // sums of decays in double, handed on as two floats: differences of
-            // sums stay exact to the last bit of the decays. A decay below -200
-            // is a factor of zero in fp32 and is held there, so that no sum is
-            // infinite and no difference NaN.
-            double s[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = 2 * lane + x;
-                float gt = a.g && t < len ? a.g[hrow + t] : 0.f;
-                gt = gt < -200.f ? -200.f : gt;
-                s[x] = (double)gt + (x ? s[0] : 0.0);
-            }
-            double base = s[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, base, o);
-                if (lane >= o) base += v;
-            }
-            base -= s[1];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const double G = base + s[x];
-                const float hi = (float)G;
-                pv[kPGh * C + 2 * lane + x] = hi;
-                pv[kPGl * C + 2 * lane + x] = (float)(G - (double)hi);
-            }
+        if (r > 0) {
+            if (tid == 0 || tid == 128) bulk_wait_read<0>();  // the head before has gone out
+            if (warp == 0) sum_gates();
+            __syncthreads();
         }
-        __syncthreads();
         if (tid < 2 * C) {
             const int j = tid & 63;
             const float hj = Gh[j], lj = Gl[j];
             auto from = [&](int i) { return expf((Gh[i] - hj) + (Gl[i] - lj)); };
-            const float eta = j < len ? a.eta[hrow + j] : 0.f, e = eta * iK[j];
+            const float e = eta1 * iK[j];
             if (tid < C) {
                 const float dec = expf(hj + lj);
                 pv[kPek * C + j] = e;
@@ -292,6 +309,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
                 vec[kVgl * C + j] = lj;
             }
         }
+        if (r + 1 < rep) load_gates(h + 1);
         __syncthreads();
 
         // A (to shared memory) or P (kept) from the products
@@ -300,6 +318,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
             const int i0 = 16 * mt + gq, i1 = i0 + 8;
             const float si[2] = {forw ? iK[i0] : a.q_scale * iQ[i0], forw ? iK[i1] : a.q_scale * iQ[i1]};
             const float ri[2] = {si[0] * pv[kProw * C + i0], si[1] * pv[kProw * C + i1]};
+            const float hi2[2] = {Gh[i0], Gh[i1]}, li2[2] = {Gl[i0], Gl[i1]};
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) {
 #pragma unroll
@@ -310,11 +329,16 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
                     P[nt][0] = kk[nt][0] * ri[0] * cj.x, P[nt][1] = kk[nt][1] * ri[0] * cj.y;
                     P[nt][2] = kk[nt][2] * ri[1] * cj.x, P[nt][3] = kk[nt][3] * ri[1] * cj.y;
                 } else if (nt < 2 * mt + 2) {
+                    const float2 hj = *reinterpret_cast<const float2 *>(Gh + j0);
+                    const float2 lj = *reinterpret_cast<const float2 *>(Gl + j0);
+                    const float2 ej = *reinterpret_cast<const float2 *>(ek + j0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e < 2 ? i0 : i1, j = j0 + (e & 1);
-                        if (forw ? j < i : j <= i)
-                            P[nt][e] = kk[nt][e] * si[e >> 1] * ek[j] * expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j]));
+                        const float d = (hi2[e >> 1] - (e & 1 ? hj.y : hj.x)) + (li2[e >> 1] - (e & 1 ? lj.y : lj.x));
+                        const float f = kk[nt][e] * si[e >> 1] * (e & 1 ? ej.y : ej.x) * expf(d);
+                        // above the diagonal the exponential may be infinite: chosen, not multiplied
+                        P[nt][e] = (forw ? j < i : j <= i) ? f : 0.f;
                     }
                 }
                 if (forw && nt < 2 * mt + 2) {
@@ -500,7 +524,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
             }
         }
     }
-    if (tid == 0 || tid == 128) bulk_wait<0>();
+    if (tid == 0 || tid == 128) bulk_wait_read<0>();  // shared memory is read; the writes end with the kernel
 }
 
 // ---------------------------------------------------------------- scan
