@@ -442,20 +442,21 @@ struct GradArgs {
     Images im;
 };
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 
-// Shared memory: K and Q images; a region that first holds X and T, then W
-// and Om, then the three 64 x 64 images; rho; vectors and partial sums.
+// Shared memory: K and Q images; a region that first holds X and T, then W, dZ
+// and dX, then W and Om, then the three 64 x 64 images; rho; vectors and partial
+// sums.
 template <int DK, int DV, bool BF16>
 struct GradSmem {
     static constexpr int IMG = C * DK * 2 * (BF16 ? 1 : 2);
     static constexpr int W = DK * DV * 2 * 2;          // W (or Om), two terms
-    static constexpr int R = C * DV * 2 * 2;           // rho (or X), two terms
-    static constexpr int big1 = 2 * W, big2 = R + 2 * kImg, big3 = 6 * kImg;
+    static constexpr int R = C * DV * 2 * 2;           // rho (or X, dZ, dX), two terms
+    static constexpr int big1 = W + (W > 2 * R ? W : 2 * R), big2 = R + 2 * kImg, big3 = 6 * kImg;
     static constexpr int big = big1 > big2 ? (big1 > big3 ? big1 : big3) : (big2 > big3 ? big2 : big3);
     static constexpr int oBig = 2 * IMG, oR = oBig + big, oF = oR + R;
-    // floats: Gh, Gl, eta, iR, iT (5 x 64), iS, iO (2 x 128), row maxima (2 x 64), 64
-    static constexpr int bytes = oF + 4 * (5 * C + 2 * 128 + 2 * C + 64);
+    // floats: Gh, Gl, eta, iR, iT (5 x 64), iS (128), iZ or iO (128), sums over warps (128)
+    static constexpr int bytes = oF + 4 * (5 * C + 128 + 128 + 128);
 };
 
 // Row (c0 .. c0 + 7) units of an fp32 matrix row, scaled to two fp16 terms.
@@ -481,45 +482,22 @@ __device__ __forceinline__ float2 h2f(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
-// A fragments of 16 rows (first row: p) of an fp32 matrix in global memory, rows
-// past `rows` zero, and the rows' scales.
-template <int KT>
-struct RowFrags {
-    float v[2 * KT][4];
-    float s[2], inv[2];
-    __device__ __forceinline__ void load(const float *p, int ld, int row0, int rows, int gq, int q4) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int row = row0 + gq + 8 * x;
-            const float *r = p + (size_t)row * ld + 2 * q4;
-#pragma unroll
-            for (int nt = 0; nt < 2 * KT; ++nt) {
-                float2 u = make_float2(0.f, 0.f);
-                if (row < rows) u = *reinterpret_cast<const float2 *>(r + 8 * nt);
-                v[nt][2 * x] = u.x;
-                v[nt][2 * x + 1] = u.y;
-            }
-        }
-        row_scales<2 * KT>(v, s, inv);
-    }
-};
-
 // One block per chunk and key head, its value heads one after the other; dQ and
 // dK of the chunk stay in registers and are added up over them. Warp (mt, hf)
-// holds the rows of tokens 16 mt .. 16 mt + 15 and half of the columns.
+// holds the rows of tokens 16 mt .. 16 mt + 15 and a quarter of the columns.
 template <int DK, int DV, bool BF16>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a) {
     extern __shared__ __align__(128) char gsm[];
     using SM = GradSmem<DK, DV, BF16>;
     constexpr int IMG = SM::IMG, KIMG = C * DK * 2;
-    constexpr int NK = DK / 16;  // 8-column tiles of half of DK
-    constexpr int NV = DV / 16;
+    constexpr int NK = DK / 32;  // 8-column tiles of a quarter of DK
+    constexpr int NV = DV / 32;
     constexpr int KV = DV / 16;  // 16-deep steps over DV
     char *sK = gsm, *sQ = sK + IMG, *big = gsm + SM::oBig, *sR = gsm + SM::oR;
     float *Gh = reinterpret_cast<float *>(gsm + SM::oF), *Gl = Gh + C, *eta = Gl + C, *iR = eta + C,
-          *iTs = iR + C, *iS = iTs + C, *iO = iS + 128, *rmax = iO + 128, *red = rmax + 2 * C;
+          *iTs = iR + C, *iS = iTs + C, *iZ = iS + 128, *iO = iZ, *rmax = iS, *red = iZ + 128;
     // partial sums over the warps, in the place of rho once it is read
-    float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 2 * C, *colp = dotp + 2 * C,
+    float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 4 * C, *colp = dotp + 4 * C,
           *dG = colp + 4 * C, *kt = dG + C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const int mt = warp & 3, hf = warp >> 2;
@@ -536,13 +514,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     float dQ[NK][4] = {}, dK[NK][4] = {};
     const int rep = a.H / a.Hk;
     const int row[2] = {16 * mt + gq, 16 * mt + gq + 8};
-    const int n0 = hf * (DK / 2);  // this warp's columns of DK
+    const int n0 = hf * (DK / 4);  // this warp's columns of DK
 
     for (int r = 0; r < rep; ++r) {
         const int h = hk * rep + r;
         const size_t hrow = ((size_t)b * a.H + h) * a.T + t0;
         const size_t hslot = (size_t)slot * a.H + h;
         const float *vec = reinterpret_cast<const float *>(a.im.vec + hslot * kVecBytes);
+        // what the head needs later is fetched into L2 meanwhile
+        if (lane == 0 && warp < 4) {
+            const float *src = warp == 0   ? a.saveS + hslot * DK * DV
+                               : warp == 1 ? a.saveO + hslot * DK * DV
+                               : warp == 2 ? a.dZ + hrow * DV
+                                           : a.dV + hrow * DV;
+            bulk_prefetch_l2(src, (warp < 2 ? DK : len) * DV * 4);
+        }
         __syncthreads();  // the head before is done with shared memory
         if (tid < C) {
             Gh[tid] = vec[kVgh * C + tid];
@@ -568,7 +554,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     reinterpret_cast<const uint4 *>(a.im.T + hslot * 2 * kImg)[u];
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+            for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w]);
             float s, is;
             pow2_scale(m, s, is);
 #pragma unroll
@@ -577,10 +563,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 char *d = big + img_off(rw, col);
                 put8(x[i], s, d, d + C * DV * 2);
             }
-            if (tid == 0) red[8] = is;
+            if (tid == 0) red[16] = is;
         }
         __syncthreads();
-        // rho = T X: 16 tokens, half of DV
+        // rho = T X: 16 tokens, a quarter of DV
         {
             float rho[NV][4] = {};
             const uint32_t uT = uB + SM::R;
@@ -593,8 +579,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
                 for (int np = 0; np < NV / 2; ++np) {
                     uint32_t xh[4], xl[4];
-                    load_bt(xh, uB, 16 * jj, hf * (DV / 2) + 16 * np, lane);
-                    load_bt(xl, uB + C * DV * 2, 16 * jj, hf * (DV / 2) + 16 * np, lane);
+                    load_bt(xh, uB, 16 * jj, hf * (DV / 4) + 16 * np, lane);
+                    load_bt(xl, uB + C * DV * 2, 16 * jj, hf * (DV / 4) + 16 * np, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(rho[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
@@ -608,7 +594,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             for (int nt = 0; nt < NV; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    rho[nt][e] *= iTs[row[e >> 1]] * red[8];
+                    rho[nt][e] *= iTs[row[e >> 1]] * red[16];
                     m[e >> 1] = fmaxf(m[e >> 1], fabsf(rho[nt][e]));
                 }
 #pragma unroll
@@ -620,49 +606,55 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float s, is;
-                pow2_scale(fmaxf(rmax[row[x]], rmax[C + row[x]]), s, is);
+                pow2_scale(fmaxf(fmaxf(rmax[row[x]], rmax[C + row[x]]),
+                                 fmaxf(rmax[2 * C + row[x]], rmax[3 * C + row[x]])),
+                           s, is);
                 if (q4 == 0 && hf == 0) iR[row[x]] = is;
 #pragma unroll
                 for (int nt = 0; nt < NV; ++nt) {
                     uint32_t hi, lo;
                     split_f16(rho[nt][2 * x] * s, rho[nt][2 * x + 1] * s, hi, lo);
-                    const uint32_t o = img_off(row[x], hf * (DV / 2) + 8 * nt) + 4 * q4;
+                    const uint32_t o = img_off(row[x], hf * (DV / 4) + 8 * nt) + 4 * q4;
                     *reinterpret_cast<uint32_t *>(sR + o) = hi;
                     *reinterpret_cast<uint32_t *>(sR + C * DV * 2 + o) = lo;
                 }
             }
         }
-        // W and Om, row by row (rows of DK), and <W, Om>
-        float wo = 0.f;
+        // 1 / scales of K and Q: of this thread's rows, and K's of all over T's (read above)
+        const float iKr[2] = {vec[kVik * C + row[0]], vec[kVik * C + row[1]]};
+        const float iQr[2] = {vec[kViq * C + row[0]], vec[kViq * C + row[1]]};
+        float *iKs = iTs;
+        if (tid < C) iKs[tid] = vec[kVik * C + tid];
+        __syncthreads();  // the row maxima are read
+        // W row by row (rows of DK), dZ and dX token by token
+        constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
+        const int srow = tid / LPR, scol = (tid % LPR) * 8;
+        auto stage = [&](const float(&w)[8], int rw, char *img, float *inv) {
+            float m = max8(w);
+#pragma unroll
+            for (int x = 1; x < LPR; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            float s, is;
+            // 64 rows an image, its two terms behind one another
+            char *d = img + (rw >> 6) * SM::R + img_off(rw & 63, scol);
+            pow2_scale(m, s, is);
+            put8(w, s, d, d + C * DV * 2);
+            if (tid % LPR == 0) inv[rw] = is;
+        };
+        char *sO = big + SM::W;  // dZ and dX, later Om
         {
-            constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
-            const float *gw = a.saveS + hslot * DK * DV, *go = a.saveO + hslot * DK * DV;
-#pragma unroll 2
-            for (int p = 0; p < DK / RPP; ++p) {
-                const int rw = p * RPP + tid / LPR, col = (tid % LPR) * 8;
-                float w[8], o[8];
-                get8(w, gw + (size_t)rw * DV + col);
-                get8(o, go + (size_t)rw * DV + col);
-                float mw = max8(w), mo = max8(o);
+            float w[DK / RPP][8], z[2 * C / RPP][8] = {};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) wo = fmaf(w[j], o[j], wo);
+            for (int p = 0; p < DK / RPP; ++p)
+                get8(w[p], a.saveS + hslot * DK * DV + (size_t)(p * RPP + srow) * DV + scol);
 #pragma unroll
-                for (int x = 1; x < LPR; x <<= 1) {
-                    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, x));
-                    mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, x));
-                }
-                float s, is;
-                // 64 rows of DK an image, its two terms behind one another
-                char *d = big + (rw >> 6) * (C * DV * 4) + img_off(rw & 63, col);
-                pow2_scale(mw, s, is);
-                put8(w, s, d, d + C * DV * 2);
-                if (tid % LPR == 0) iS[rw] = is;
-                pow2_scale(mo, s, is);
-                put8(o, s, d + SM::W, d + SM::W + C * DV * 2);
-                if (tid % LPR == 0) iO[rw] = is;
+            for (int p = 0; p < 2 * C / RPP; ++p) {
+                const int t = (p * RPP + srow) & (C - 1);
+                if (t < len) get8(z[p], (p * RPP < C ? a.dZ : a.dV) + (hrow + t) * DV + scol);
             }
-            wo = warp_sum(wo);
-            if (lane == 0) red[16 + warp] = wo;
+#pragma unroll
+            for (int p = 0; p < DK / RPP; ++p) stage(w[p], p * RPP + srow, big, iS);
+#pragma unroll
+            for (int p = 0; p < 2 * C / RPP; ++p) stage(z[p], p * RPP + srow, sO, iZ);
         }
         __syncthreads();
 
@@ -673,21 +665,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             dec[x] = expf(Gh[row[x]] + Gl[row[x]]);
             rest[x] = expf((GC - Gh[row[x]]) + (GCl - Gl[row[x]]));
         }
-        const uint32_t uW = uB + (n0 >> 6) * (C * DV * 4), uO = uW + SM::W;
+        const uint32_t uW = uB + (n0 >> 6) * SM::R, uO = uW + SM::W;
         const int nrow = n0 & 63;
-        float phi[4][4] = {}, eps[4][4] = {};  // tokens 32 hf + ..
+        float phi[2][4] = {}, eps[2][4] = {};  // tokens 16 hf + ..
         float dot[2] = {0.f, 0.f}, ktp[2] = {0.f, 0.f};
         // dZ, then dX, against W and rho
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-            RowFrags<KV> f;
-            f.load((pass ? a.dV : a.dZ) + hrow * DV, DV, 16 * mt, len, gq, q4);
+            const uint32_t uZ = uB + SM::W + pass * SM::R;
+            const float iz[2] = {iZ[pass * C + row[0]], iZ[pass * C + row[1]]};
             float N[NK][4] = {};
-            float(&cc)[4][4] = pass ? eps : phi;
+            float(&cc)[2][4] = pass ? eps : phi;
 #pragma unroll
             for (int kk = 0; kk < KV; ++kk) {
                 uint32_t hi[4], lo[4];
-                a_terms(f.v[2 * kk], f.v[2 * kk + 1], f.s, hi, lo);
+                ldsm_x4(hi, ldsm_addr(uZ, 16 * mt, 16 * kk, lane));
+                ldsm_x4(lo, ldsm_addr(uZ + C * DV * 2, 16 * mt, 16 * kk, lane));
 #pragma unroll
                 for (int np = 0; np < NK / 2; ++np) {
                     uint32_t wh[4], wl[4];
@@ -700,17 +693,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                         mma_f16(N[2 * np + x], hi, wl[2 * x], wl[2 * x + 1]);
                     }
                 }
-#pragma unroll
-                for (int np = 0; np < 2; ++np) {
-                    if (2 * hf + np > mt) continue;  // above the diagonal
+                if (hf <= mt) {  // not above the diagonal
                     uint32_t rh[4], rl[4];
-                    load_b(rh, uR, 32 * hf + 16 * np, 16 * kk, lane);
-                    load_b(rl, uR + C * DV * 2, 32 * hf + 16 * np, 16 * kk, lane);
+                    load_b(rh, uR, 16 * hf, 16 * kk, lane);
+                    load_b(rl, uR + C * DV * 2, 16 * hf, 16 * kk, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(cc[2 * np + x], hi, rh[2 * x], rh[2 * x + 1]);
-                        mma_f16(cc[2 * np + x], lo, rh[2 * x], rh[2 * x + 1]);
-                        mma_f16(cc[2 * np + x], hi, rl[2 * x], rl[2 * x + 1]);
+                        mma_f16(cc[x], hi, rh[2 * x], rh[2 * x + 1]);
+                        mma_f16(cc[x], lo, rh[2 * x], rh[2 * x + 1]);
+                        mma_f16(cc[x], hi, rl[2 * x], rl[2 * x + 1]);
                     }
                 }
             }
@@ -719,7 +710,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int col = n0 + 8 * nt + 2 * q4;
-                    const float w = (pass ? -dec[x] : a.q_scale * dec[x]) * f.inv[x];
+                    const float w = (pass ? -dec[x] : a.q_scale * dec[x]) * iz[x];
                     const float y0 = w * N[nt][2 * x] * iS[col], y1 = w * N[nt][2 * x + 1] * iS[col + 1];
                     const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
                     const char *im = pass ? sK : sQ;
@@ -728,17 +719,45 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                         const float2 l = h2f(*reinterpret_cast<const uint32_t *>(im + KIMG + o));
                         kq.x += l.x, kq.y += l.y;
                     }
-                    const float inv = vec[(pass ? kVik : kViq) * C + row[x]];
+                    const float inv = pass ? iKr[x] : iQr[x];
                     dot[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), dot[x]);
                     float *d = pass ? &dK[nt][2 * x] : &dQ[nt][2 * x];
                     d[0] += y0, d[1] += y1;
                 }
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    cc[nt][e] *= f.inv[e >> 1] * iR[32 * hf + 8 * nt + 2 * q4 + (e & 1)];
+                    cc[nt][e] *= iz[e >> 1] * iR[16 * hf + 8 * nt + 2 * q4 + (e & 1)];
         }
+        __syncthreads();  // dZ and dX are read: Om takes their place
+        // Om, and <W, Om> with W as it was staged
+        {
+            float o[DK / RPP][8], wo = 0.f;
+#pragma unroll
+            for (int p = 0; p < DK / RPP; ++p)
+                get8(o[p], a.saveO + hslot * DK * DV + (size_t)(p * RPP + srow) * DV + scol);
+#pragma unroll
+            for (int p = 0; p < DK / RPP; ++p) {
+                const int rw = p * RPP + srow;
+                const char *d = big + (rw >> 6) * SM::R + img_off(rw & 63, scol);
+                const uint4 h = *reinterpret_cast<const uint4 *>(d);
+                const uint4 l = *reinterpret_cast<const uint4 *>(d + C * DV * 2);
+                const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = h2f(hh[j]), v = h2f(ll[j]);
+                    s = fmaf(u.x + v.x, o[p][2 * j], s);
+                    s = fmaf(u.y + v.y, o[p][2 * j + 1], s);
+                }
+                wo = fmaf(s, iS[rw], wo);
+                stage(o[p], rw, sO, iO);
+            }
+            wo = warp_sum(wo);
+            if (lane == 0) red[32 + warp] = wo;
+        }
+        __syncthreads();
         // rho against Om
         {
             float N[NK][4] = {};
@@ -773,43 +792,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                         const float2 l = h2f(*reinterpret_cast<const uint32_t *>(sK + KIMG + o));
                         kq.x += l.x, kq.y += l.y;
                     }
-                    const float inv = vec[kVik * C + row[x]];
+                    const float inv = iKr[x];
                     ktp[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), ktp[x]);
                     dK[nt][2 * x] = fmaf(eta[row[x]], y0, dK[nt][2 * x]);
                     dK[nt][2 * x + 1] = fmaf(eta[row[x]], y1, dK[nt][2 * x + 1]);
                 }
         }
-        // the triangle: q_i.k_j and k_i.k_j of this warp's 16 x 32 block
-        float kk2[4][4] = {}, qk2[4][4] = {};
+        // the triangle: q_i.k_j and k_i.k_j of this warp's 16 x 16 block
+        float kk2[2][4] = {}, qk2[2][4] = {};
+        if (hf <= mt) {
 #pragma unroll
-        for (int k = 0; k < DK; k += 16) {
-            uint32_t ak[4], aq[4], akl[4], aql[4];
-            ldsm_x4(ak, ldsm_addr(uK, 16 * mt, k, lane));
-            ldsm_x4(aq, ldsm_addr(uQ, 16 * mt, k, lane));
-            if (!BF16) {
-                ldsm_x4(akl, ldsm_addr(uK + KIMG, 16 * mt, k, lane));
-                ldsm_x4(aql, ldsm_addr(uQ + KIMG, 16 * mt, k, lane));
-            }
-#pragma unroll
-            for (int np = 0; np < 2; ++np) {
-                if (2 * hf + np > mt) continue;
-                uint32_t bb[4];
-                load_b(bb, uK, 32 * hf + 16 * np, k, lane);
+            for (int k = 0; k < DK; k += 16) {
+                uint32_t ak[4], aq[4], bb[4];
+                ldsm_x4(ak, ldsm_addr(uK, 16 * mt, k, lane));
+                ldsm_x4(aq, ldsm_addr(uQ, 16 * mt, k, lane));
+                load_b(bb, uK, 16 * hf, k, lane);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    mma_f16(kk2[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
-                    mma_f16(qk2[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
-                    if (!BF16) {
-                        mma_f16(kk2[2 * np + x], akl, bb[2 * x], bb[2 * x + 1]);
-                        mma_f16(qk2[2 * np + x], aql, bb[2 * x], bb[2 * x + 1]);
-                    }
+                    mma_f16(kk2[x], ak, bb[2 * x], bb[2 * x + 1]);
+                    mma_f16(qk2[x], aq, bb[2 * x], bb[2 * x + 1]);
                 }
                 if (!BF16) {
-                    load_b(bb, uK + KIMG, 32 * hf + 16 * np, k, lane);
+                    uint32_t akl[4], aql[4], bl[4];
+                    ldsm_x4(akl, ldsm_addr(uK + KIMG, 16 * mt, k, lane));
+                    ldsm_x4(aql, ldsm_addr(uQ + KIMG, 16 * mt, k, lane));
+                    load_b(bl, uK + KIMG, 16 * hf, k, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(kk2[2 * np + x], ak, bb[2 * x], bb[2 * x + 1]);
-                        mma_f16(qk2[2 * np + x], aq, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(kk2[x], akl, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(qk2[x], aql, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(kk2[x], ak, bl[2 * x], bl[2 * x + 1]);
+                        mma_f16(qk2[x], aq, bl[2 * x], bl[2 * x + 1]);
                     }
                 }
             }
@@ -817,27 +830,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         __syncthreads();  // rho, W and Om are read
         float rs[2] = {0.f, 0.f}, mx[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < 2; ++nt) {
             float cs[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = row[e >> 1], j = 32 * hf + 8 * nt + 2 * q4 + (e & 1);
+                const int i = row[e >> 1], j = 16 * hf + 8 * nt + 2 * q4 + (e & 1);
                 float p = 0.f, q = 0.f;
                 if (j <= i) {
                     const float gam = expf((Gh[i] - Gh[j]) + (Gl[i] - Gl[j]));
-                    const float ikj = vec[kVik * C + j];
+                    const float ikj = iKs[j], iqi = iQr[e >> 1], iki = iKr[e >> 1];
                     p = a.q_scale * gam * phi[nt][e];
                     if (j < i) q = -gam * eps[nt][e];
-                    const float w = ikj * (p * qk2[nt][e] * vec[kViq * C + i] +
-                                           q * kk2[nt][e] * vec[kVik * C + i]);
+                    const float w = ikj * (p * qk2[nt][e] * iqi + q * kk2[nt][e] * iki);
                     cs[e & 1] += w;
                     rs[e >> 1] = fmaf(eta[j], w, rs[e >> 1]);
                     p *= eta[j];
                     q *= eta[j];
                     // as operands: the rows of K and Q they meet carry their scales
                     mx[0] = fmaxf(mx[0], fabsf(p * ikj));
-                    mx[1] = fmaxf(mx[1], fabsf(p * vec[kViq * C + i]));
-                    mx[2] = fmaxf(mx[2], fabsf(q) * fmaxf(ikj, vec[kVik * C + i]));
+                    mx[1] = fmaxf(mx[1], fabsf(p * iqi));
+                    mx[2] = fmaxf(mx[2], fabsf(q) * fmaxf(ikj, iki));
                 }
                 phi[nt][e] = p;
                 eps[nt][e] = q;
@@ -846,7 +858,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             for (int x = 0; x < 2; ++x) {
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
-                if (gq == 0) colp[mt * C + 32 * hf + 8 * nt + 2 * q4 + x] = cs[x];
+                if (gq == 0) colp[mt * C + 16 * hf + 8 * nt + 2 * q4 + x] = cs[x];
             }
         }
 #pragma unroll
@@ -863,7 +875,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         for (int y = 0; y < 3; ++y) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
-            if (lane == 0) red[32 + 8 * y + warp] = mx[y];
+            if (lane == 0) red[48 + 16 * y + warp] = mx[y];
         }
         __syncthreads();  // sums and maxima are there
         float sx[3], ix[3];
@@ -871,21 +883,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         for (int y = 0; y < 3; ++y) {
             float m = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, red[32 + 8 * y + w]);
+            for (int w = 0; w < 16; ++w) m = fmaxf(m, red[48 + 16 * y + w]);
             pow2_scale(m, sx[y], ix[y]);
         }
         char *i1 = big, *i2 = big + 2 * kImg, *i3 = big + 4 * kImg;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const int j0 = 32 * hf + 8 * nt + 2 * q4;
-            const float k0 = vec[kVik * C + j0], k1 = vec[kVik * C + j0 + 1];
+        for (int nt = 0; nt < 2; ++nt) {
+            const int j0 = 16 * hf + 8 * nt + 2 * q4;
+            const float k0 = iKs[j0], k1 = iKs[j0 + 1];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int i = row[x];
-                const float qi = vec[kViq * C + i], ki = vec[kVik * C + i];
+                const float qi = iQr[x], ki = iKr[x];
                 const float p0 = phi[nt][2 * x], p1 = phi[nt][2 * x + 1];
                 const float e0 = eps[nt][2 * x], e1 = eps[nt][2 * x + 1];
-                const uint32_t o = img_off(i, 32 * hf + 8 * nt) + 4 * q4;
+                const uint32_t o = img_off(i, 16 * hf + 8 * nt) + 4 * q4;
                 uint32_t hi, lo;
                 split_f16(p0 * k0 * sx[0], p1 * k1 * sx[0], hi, lo);
                 *reinterpret_cast<uint32_t *>(i1 + o) = hi;
@@ -913,20 +925,31 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
         if (tid < C) {
             const float cs = (colp[tid] + colp[C + tid]) + (colp[2 * C + tid] + colp[3 * C + tid]);
-            const float k2 = dotp[tid] + dotp[C + tid];
+            const float k2 = (dotp[tid] + dotp[C + tid]) + (dotp[2 * C + tid] + dotp[3 * C + tid]);
+            const float rp = (rowp[tid] + rowp[C + tid]) + (rowp[2 * C + tid] + rowp[3 * C + tid]);
             if (tid < len) a.deta[hrow + tid] = cs + k2;
-            dG[tid] = (rowp[tid] + rowp[C + tid]) - eta[tid] * (cs + k2);
+            dG[tid] = rp - eta[tid] * (cs + k2);
             kt[tid] = eta[tid] * k2;
         }
         __syncthreads();
-        if (a.dg && tid < C && tid < len) {
-            // sums in double: the terms of later tokens cancel
-            double s = 0.0, w = 0.0;
-            for (int i = C - 1; i >= tid; --i) s += (double)dG[i];
-            for (int i = 0; i < C; ++i) w += (double)kt[i];
-            double d = 0.0;
-            for (int i = 0; i < 8; ++i) d += (double)red[16 + i];
-            a.dg[hrow + tid] = (float)(s + w + (double)expf(GC + GCl) * d);
+        if (a.dg && warp == 15) {
+            // sums in double: the terms of later tokens cancel. Lane l holds tokens 2 l, 2 l + 1.
+            const double d0 = dG[2 * lane], d1 = dG[2 * lane + 1];
+            double s = d0 + d1, w = (double)kt[2 * lane] + (double)kt[2 * lane + 1];
+            double d = lane < 16 ? (double)red[32 + lane] : 0.0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double v = __shfl_down_sync(0xffffffffu, s, o);
+                if (lane + o < 32) s += v;
+                w += __shfl_xor_sync(0xffffffffu, w, o);
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+            }
+            w += (double)expf(GC + GCl) * d;
+            // s holds the tokens from 2 l on
+            const double later = __shfl_down_sync(0xffffffffu, s, 1);
+            if (2 * lane < len) a.dg[hrow + 2 * lane] = (float)(s + w);
+            if (2 * lane + 1 < len)
+                a.dg[hrow + 2 * lane + 1] = (float)(d1 + (lane < 31 ? later : 0.0) + w);
         }
         // dQ += (phi eta) K, dK += (phi eta)^T Q + (E + E^T) K
         const uint32_t u1 = smem_u32(i1), u2 = smem_u32(i2), u3 = smem_u32(i3);
