@@ -506,11 +506,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     if (!ChunkSearch{a.seq_start, a.T, a.N}.find(slot, n, t0, len)) return;
     const int b = a.seq_start ? 0 : n;
     const size_t kslot = (size_t)slot * a.Hk + hk;
+    const uint32_t uK = smem_u32(sK), uQ = smem_u32(sQ);
     for (int u = tid; u < IMG / 16; u += kGradThreads) {
-        reinterpret_cast<uint4 *>(sK)[u] = reinterpret_cast<const uint4 *>(a.im.K + kslot * IMG)[u];
-        reinterpret_cast<uint4 *>(sQ)[u] = reinterpret_cast<const uint4 *>(a.im.Q + kslot * IMG)[u];
+        cp_async16(uK + 16 * u, a.im.K + kslot * IMG + 16 * (size_t)u, true);
+        cp_async16(uQ + 16 * u, a.im.Q + kslot * IMG + 16 * (size_t)u, true);
     }
-    const uint32_t uK = smem_u32(sK), uQ = smem_u32(sQ), uB = smem_u32(big), uR = smem_u32(sR);
+    const uint32_t uB = smem_u32(big), uR = smem_u32(sR);
     float dQ[NK][4] = {}, dK[NK][4] = {};
     const int rep = a.H / a.Hk;
     const int row[2] = {16 * mt + gq, 16 * mt + gq + 8};
@@ -566,6 +567,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             if (tid == 0) red[16] = is;
         }
         __syncthreads();
+        constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
+        const int srow = tid / LPR, scol = (tid % LPR) * 8;
         // rho = T X: 16 tokens, a quarter of DV
         {
             float rho[NV][4] = {};
@@ -627,8 +630,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         if (tid < C) iKs[tid] = vec[kVik * C + tid];
         __syncthreads();  // the row maxima are read
         // W row by row (rows of DK), dZ and dX token by token
-        constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
-        const int srow = tid / LPR, scol = (tid % LPR) * 8;
         auto stage = [&](const float(&w)[8], int rw, char *img, float *inv) {
             float m = max8(w);
 #pragma unroll
@@ -656,6 +657,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
             for (int p = 0; p < 2 * C / RPP; ++p) stage(z[p], p * RPP + srow, sO, iZ);
         }
+        cp_async_wait_all();  // K and Q, asked for at the start
         __syncthreads();
 
         const float GC = Gh[C - 1], GCl = Gl[C - 1];
