@@ -709,7 +709,7 @@ def _tensors(fn, index, **want):
 class _On:
     """The device and the stream of a call: empty() allocates for it, run() makes it."""
 
-    __slots__ = ("fn", "index", "device", "handle", "side", "torch")
+    __slots__ = ("fn", "index", "device", "handle", "side", "torch", "held")
 
     def __init__(self, fn, first, stream):
         import torch
@@ -730,6 +730,14 @@ class _On:
         if stream != current:
             self.handle, self.side = stream.cuda_stream, stream
 
+    def uses(self, *tensors):
+        """The call reads or writes these (None: nothing): on another stream than the current one
+        their memory is not handed out again before the call is done."""
+        if self.side is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.side)
+
     def empty(self, shape, dtype):
         t = self.torch.empty(shape, dtype=dtype, device=self.device)
         if self.side is not None:
@@ -748,7 +756,11 @@ class _On:
     def workspace(self, given, need):
         """A workspace of `need` bytes (a given one is checked): its address and size."""
         if given is None:
-            return self.empty(max(need, 256), self.torch.uint8).data_ptr(), max(need, 256)
+            # held to the end of the call: freed before the launch, another
+            # thread's allocation on this stream could be put in its place
+            self.held = self.empty(max(need, 256), self.torch.uint8)
+            return self.held.data_ptr(), max(need, 256)
+        self.uses(given)
         if given.get_device() != self.index or not given.is_contiguous():
             raise ValueError(f"{self.fn}: workspace must be contiguous and on cuda:{self.index}")
         return given.data_ptr(), given.numel() * given.element_size()
@@ -811,6 +823,7 @@ def delta_fwd(Q, K, V, eta, g=None, W0=None, *, w0_per_seq=False, seq_start=None
     L = lib()
     ws, nbytes = on.workspace(workspace,
                               L.ttt_delta_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, code))
+    on.uses(Q, K, V, eta, g, W0, Z, seq_start)
     on.run("ttt_delta_fwd", L.ttt_delta_fwd, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
            eta.data_ptr(), _p(g), _p(W0), Z.data_ptr(), _p(W_out), _p(seq_start), n_seq, q_scale,
            B, Hk, H, T, dk, dv, code,
@@ -835,6 +848,7 @@ def delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out=None, *, w0_per_seq=False, seq_sta
     L = lib()
     ws, nbytes = on.workspace(workspace,
                               L.ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, code))
+    on.uses(Q, K, V, eta, g, W0, dZ, dW_out, seq_start)
     on.run("ttt_delta_bwd", L.ttt_delta_bwd, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
            eta.data_ptr(), _p(g), _p(W0), dZ.data_ptr(), _p(dW_out), grads["Q"].data_ptr(),
            grads["K"].data_ptr(), grads["V"].data_ptr(), grads["eta"].data_ptr(),
@@ -864,6 +878,7 @@ def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_
         _tensors("delta_decode", on.index, Z=(Z, (zt,), (B, H, n, dv)))
     _tensors("delta_decode", on.index, W=(W, (torch.float32,), (slots, H, dk, dv)),
              state_index=(state_index, (torch.int32,), (B,)))
+    on.uses(Q, K, V, eta, g, W, Z, state_index)
     on.run("ttt_delta_decode", lib().ttt_delta_decode, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
            eta.data_ptr(), _p(g), W.data_ptr(), Z.data_ptr(), _p(state_index), slots, q_scale, B,
            Hk, H, n, dk, dv, code, TTT_F_Z_BF16 if z_bf16 else 0)
@@ -920,6 +935,7 @@ def join_fwd(X, Z, gate=None, scale=None, post_gamma=None, post_beta=None, pre_g
                                            post_beta, pre_gamma, pre_beta, rms, act)
     R = None if Z is None else on.like(X, X.dtype)
     Hn = on.like(X, X.dtype) if want_h else None
+    on.uses(X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta)
     on.run("ttt_join_fwd", lib().ttt_join_fwd, X.data_ptr(), _p(Z), _p(gate), _p(scale),
            _p(post_gamma), _p(post_beta), _p(pre_gamma), _p(pre_beta), _p(R), _p(Hn), eps, B, H, T,
            d, code, flags)
@@ -945,6 +961,7 @@ def join_bwd(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, dR, 
     L = lib()
     ws, nbytes = on.workspace(workspace, L.ttt_join_bwd_workspace_bytes(B, H, T, d))
     at = lambda n: _p(g.get(n))  # noqa: E731
+    on.uses(R, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, dR, dH)
     on.run("ttt_join_bwd", L.ttt_join_bwd, R.data_ptr(), _p(Z), _p(gate), _p(scale),
            _p(post_gamma), _p(post_beta), _p(pre_gamma), _p(dR), _p(dH), at("X"), at("Z"),
            at("gate"), at("scale"), at("gamma1"), at("beta1"), at("gamma2"), at("beta2"), eps, B,
