@@ -587,15 +587,17 @@ __device__ __forceinline__ void load_v(float4 (&v)[2], const char *vt, int row0,
 // Behind the stages: the four warps' shares of X [to][from][2 tiles], and, twice for
 // the chunks in turn, V [64][16], the terms of X [4 blocks][hi, lo], 1 / their
 // scales and those of W^T, the terms of W^T [DK / 16][hi, (lo)].
-template <int DK, int MODE>
+template <bool BF16>
+constexpr int scan_v_bytes() { return C * 16 * (BF16 ? 2 : 4); }
+template <int DK, bool BF16, int MODE>
 constexpr int scan_turn_bytes() {
-    return 4096 + 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
+    return scan_v_bytes<BF16>() + 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
 }
-template <int DK, int MODE>
-constexpr int scan_area_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MODE>(); }
+template <int DK, bool BF16, int MODE, int MT>
+constexpr int scan_area_bytes() { return MT * (16 * 1024 + 2 * scan_turn_bytes<DK, BF16, MODE>()); }
 
-// Scan over the chunks. Four warps own 16 columns of W for the whole sequence, as
-// the rows of W^T [16][DK] in accumulator registers, a quarter of DK each:
+// Scan over the chunks. Four warps own 16 MT columns of W for the whole sequence,
+// as the rows of W^T [16 MT][DK] in accumulator registers, a quarter of DK each:
 // accumulator fragments packed pairwise are A fragments, so W^T K^T and X^T H
 // follow one another in registers. Twice a chunk the four meet:
 //   1. each has its quarter's share of W^T K^T for all 64 tokens and hands the
@@ -611,7 +613,7 @@ constexpr int scan_area_bytes() { return 16 * 1024 + 2 * scan_turn_bytes<DK, MOD
 // chain's next images need not wait for Z; one thread of a warp of its own fills
 // each ring. The last warp, the gate, does the chain's waiting: a wait on an
 // mbarrier costs a warp about 150 cycles even when nothing is waited for.
-template <int DK, bool BF16, int MODE>
+template <int DK, bool BF16, int MODE, int MT>
 __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(128) char ssm[];
     __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4];
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     constexpr int STAGE = chain_stage_bytes<DK, BF16>(), ZSTAGE = z_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
     constexpr int NT = DK / 32, KK = DK / 64;  // 8-column tiles and 16-deep steps of a quarter
-    const int groups = a.dv / 16;
+    const int groups = a.dv / (16 * MT);
     const int grp = blockIdx.x % groups, sh = blockIdx.x / groups;
     const int n = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = warp & 3;
@@ -649,15 +651,18 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     __syncthreads();
 
     const int gq = lane >> 2, q4 = lane & 3;
-    const int v0 = grp * 16;
+    const int v0 = grp * 16 * MT;
     const size_t vrow = ((size_t)b * a.H + h) * a.T + t0;
     char *zst = ssm + a.stages * STAGE, *area = zst + a.zstages * ZSTAGE;
     auto wait = [&](uint64_t *bar, int parity) {
         return mbar_wait_warp(bar, parity, abort, a.status, kScanStatus);
     };
 
-    // what the chunks in turn keep: V, X's terms, 1 / scales, W^T's terms
-    auto turn_at = [&](int turn) { return area + 16 * 1024 + turn * scan_turn_bytes<DK, MODE>(); };
+    // what the chunks in turn keep for 16 columns: V, X's terms, 1 / scales, W^T's terms
+    constexpr int VB = scan_v_bytes<BF16>();
+    auto turn_at = [&](int turn, int m) {
+        return area + MT * 16 * 1024 + (turn * MT + m) * scan_turn_bytes<DK, BF16, MODE>();
+    };
 
     if (warp == 11) {  // ------------------------------------------------ the gate
         // Waits for all that a chunk needs and then meets the chain, which so waits on
@@ -682,12 +687,16 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
         for (int c = 0; c < nchunk; ++c) {
             // X of the chunk two before is formed: its V has been read
             if (c >= 2 && !wait(&zready[c & 1], ((c >> 1) & 1) ^ 1)) break;
-            const uint32_t d = smem_u32(turn_at(c & 1));
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int u = lane + 32 * i, row = u / PER, part = u % PER, t = c * C + row;
-                const bool in = t < len;
-                cp_async16(d + v_off<BF16>(row, part), src + (in ? t * ld : 0) + part * 16, in);
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t d = smem_u32(turn_at(c & 1, m));
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int u = lane + 32 * i, row = u / PER, part = u % PER, t = c * C + row;
+                    const bool in = t < len;
+                    cp_async16(d + v_off<BF16>(row, part),
+                               src + (in ? t * ld : 0) + (m * PER + part) * 16, in);
+                }
             }
             cp_async_arrive(&tready[c & 1]);
         }
@@ -736,104 +745,107 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             const uint32_t uQ = smem_u32(zst + ring.s * ZSTAGE), uM = uQ + KALL;
             // the enum's order, counted from kVq on
             const float *vec = reinterpret_cast<const float *>(zst + (ring.s + 1) * ZSTAGE - kHalfVecBytes) - kVq * C;
-            const char *at = turn_at(turn);
-            const uint4 *xfr = reinterpret_cast<const uint4 *>(at + 4096) + lane;        // [block][hi, lo][32]
-            const float *iXs = reinterpret_cast<const float *>(at + 8192), *iSs = iXs + 64;
-            const uint4 *sfr = reinterpret_cast<const uint4 *>(at + 8192 + 512) + lane;  // [step][hi, (lo)][32]
             if (!wait(&zfull[ring.s], ring.ph) || !wait(&zready[turn], (c >> 1) & 1)) return;
-            float Z[2][4] = {}, ZM[2][4] = {};
-            // (Q W)^T of block p, quarter by quarter
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float z[2][4] = {};
+            for (int m = 0; m < MT; ++m) {  // 16 columns
+                const char *at = turn_at(turn, m);
+                const uint4 *xfr = reinterpret_cast<const uint4 *>(at + VB) + lane;        // [block][hi, lo][32]
+                const float *iXs = reinterpret_cast<const float *>(at + VB + 4096), *iSs = iXs + 64;
+                const uint4 *sfr = reinterpret_cast<const uint4 *>(at + VB + 4096 + 512) + lane;  // [step][hi, (lo)][32]
+                float Z[2][4] = {}, ZM[2][4] = {};
+                // (Q W)^T of block p, quarter by quarter
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
-                    const uint4 fh = d[0];
-                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
-                    uint32_t bb[4];
-                    load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
+                for (int w = 0; w < 4; ++w) {
+                    float z[2][4] = {};
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
-                    if (ZF) {
-                        const uint4 fl = d[32];
-                        const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
+                        const uint4 fh = d[0];
+                        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
+                        uint32_t bb[4];
+                        load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
-                        if (!BF16) {
-                            load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
+                        if (ZF) {
+                            const uint4 fl = d[32];
+                            const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
+                            for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
+                            if (!BF16) {
+                                load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
+                            }
                         }
                     }
+                    const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) Z[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], Z[x][e]);
                 }
-                const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
+                // (M X)^T
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int jj = 0; jj < 4; ++jj) {
+                    if (jj > p) continue;  // M_ij is zero for i < j; the same for the whole warp
+                    const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+                    const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                    const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
+                    float z[2][4] = {};
+                    uint32_t bm[4];
+                    load_b(bm, uM, 16 * p, 16 * jj, lane);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) Z[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], Z[x][e]);
-            }
-            // (M X)^T
+                    for (int x = 0; x < 2; ++x) {
+                        mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
+                    }
+                    if (ZF) {
+                        load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                if (jj > p) continue;  // M_ij is zero for i < j; the same for the whole warp
-                const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
-                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
-                const float i0 = iXs[16 * jj + gq], i1 = iXs[16 * jj + gq + 8];
-                float z[2][4] = {};
-                uint32_t bm[4];
-                load_b(bm, uM, 16 * p, 16 * jj, lane);
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ZM[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], ZM[x][e]);
+                }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                    if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
+                    const int i = 16 * p + 8 * x + 2 * q4;
+                    const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i);
+                    const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i);
+                    float(&z)[4] = Z[x], (&u)[4] = ZM[x];
+                    z[0] = cq.x * z[0] + im.x * u[0], z[1] = cq.y * z[1] + im.y * u[1];
+                    z[2] = cq.x * z[2] + im.x * u[2], z[3] = cq.y * z[3] + im.y * u[3];
                 }
-                if (ZF) {
-                    load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
+                // everything is read: the arrivals do not wait for the stores behind them
+                __syncwarp();
+                if (m == MT - 1 && lane == 0) {
+                    mbar_arrive(&tready[turn]);
+                    mbar_arrive(&zempty[ring.s]);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) ZM[x][e] = fmaf(e < 2 ? i0 : i1, z[x][e], ZM[x][e]);
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = 16 * p + 8 * x + 2 * q4;
-                const float2 cq = *reinterpret_cast<const float2 *>(vec + kVq * C + i);
-                const float2 im = *reinterpret_cast<const float2 *>(vec + kVm * C + i);
-                float(&z)[4] = Z[x], (&u)[4] = ZM[x];
-                z[0] = cq.x * z[0] + im.x * u[0], z[1] = cq.y * z[1] + im.y * u[1];
-                z[2] = cq.x * z[2] + im.x * u[2], z[3] = cq.y * z[3] + im.y * u[3];
-            }
-            // everything is read: the arrivals do not wait for the stores behind them
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&tready[turn]);
-                mbar_arrive(&zempty[ring.s]);
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = c * C + 16 * p + 8 * x;
-                const float(&z)[4] = Z[x];
-                if (ZF) {
-                    const int t = i + 2 * q4;
-                    float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + gq;
-                    if (t < len) o[0] = z[0], o[8] = z[2];
-                    if (t + 1 < len) o[a.dv] = z[1], o[a.dv + 8] = z[3];
-                } else {
-                    // 8 x 8 blocks transposed between the lanes: a token per row
-                    const __nv_bfloat162 p0 = __floats2bfloat162_rn(z[0], z[1]);
-                    const __nv_bfloat162 p1 = __floats2bfloat162_rn(z[2], z[3]);
-                    const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
-                    const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
-                    const int t = i + gq;
-                    if (t < len) {
-                        uint32_t *o = reinterpret_cast<uint32_t *>(
-                            static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 2 * q4);
-                        o[0] = r0;
-                        o[4] = r1;
+                for (int x = 0; x < 2; ++x) {
+                    const int i = c * C + 16 * p + 8 * x;
+                    const float(&z)[4] = Z[x];
+                    if (ZF) {
+                        const int t = i + 2 * q4;
+                        float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + 16 * m + gq;
+                        if (t < len) o[0] = z[0], o[8] = z[2];
+                        if (t + 1 < len) o[a.dv] = z[1], o[a.dv + 8] = z[3];
+                    } else {
+                        // 8 x 8 blocks transposed between the lanes: a token per row
+                        const __nv_bfloat162 p0 = __floats2bfloat162_rn(z[0], z[1]);
+                        const __nv_bfloat162 p1 = __floats2bfloat162_rn(z[2], z[3]);
+                        const uint32_t r0 = movt(*reinterpret_cast<const uint32_t *>(&p0));
+                        const uint32_t r1 = movt(*reinterpret_cast<const uint32_t *>(&p1));
+                        const int t = i + gq;
+                        if (t < len) {
+                            uint32_t *o = reinterpret_cast<uint32_t *>(
+                                static_cast<__nv_bfloat16 *>(a.Z) + (vrow + t) * a.dv + v0 + 16 * m + 2 * q4);
+                            o[0] = r0;
+                            o[4] = r1;
+                        }
                     }
                 }
             }
@@ -842,26 +854,30 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     }
 
     // -------------------------------------------------------------- the chain
-    float4 *part = reinterpret_cast<float4 *>(area) + lane;  // [to][from][tile][32]
+    float4 *part = reinterpret_cast<float4 *>(area) + lane;  // [16 columns][to][from][tile][32]
     // W^T: row gq (elements 0, 1) and gq + 8 (2, 3), columns k0 + 8 nt + 2 q4 + {0, 1}
     const int k0 = p * (DK / 4);
-    float S[NT][4];
+    float S[MT][NT][4];
     const size_t state = (size_t)DK * a.dv, mine = (size_t)(k0 + 2 * q4) * a.dv + v0 + gq;
     const float *w0 = a.W0 ? a.W0 + ((size_t)n * a.w_heads + h) * state + mine : nullptr;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[m][nt][e] = w0 ? w0[(size_t)(8 * nt + (e & 1)) * a.dv + 16 * m + (e >> 1) * 8] : 0.f;
 
     // W at the start of chunk c
     auto save = [&](int c) {
         float *ws = a.saveS + ((size_t)(slot0 + c) * a.H + h) * state + mine;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                ws[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    ws[(size_t)(8 * nt + (e & 1)) * a.dv + 16 * m + (e >> 1) * 8] = S[m][nt][e];
     };
     if (SAVE && nchunk > 0) save(0);
 
@@ -870,64 +886,79 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
         const int turn = c & 1;
         const uint32_t uK = smem_u32(ssm + ring.s * STAGE), uH = uK + KALL;
         const float *vec = reinterpret_cast<const float *>(ssm + (ring.s + 1) * STAGE - kHalfVecBytes);
-        char *at = turn_at(turn);
-        uint4 *xfr = reinterpret_cast<uint4 *>(at + 4096) + lane;
-        float *iXs = reinterpret_cast<float *>(at + 8192), *iSs = iXs + 64;
-        uint4 *sfr = reinterpret_cast<uint4 *>(at + 8192 + 512) + lane;
         if (named_bar_or(2, 160, false)) return;  // with the gate; it says when a wait has run out
         // W^T K^T over this warp's quarter of DK, W^T's terms left for Z
         {
-            float X[8][4] = {}, sS[2], iS[2];
-            uint32_t bb[KK][4][4], ah[KK][4], al[KK][4];
+            float X[MT][8][4] = {}, sS[MT][2], iS[MT][2];
+            uint32_t bb[KK][4][4];
+            auto load_k = [&](uint32_t(&b)[4][4], uint32_t u, int kk) {
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
+                for (int np = 0; np < 4; ++np) load_b(b[np], u, 16 * np, k0 + 16 * kk, lane);
+            };
+            if (MT == 1) {  // all on their way; with 32 columns the registers are short
 #pragma unroll
-                for (int np = 0; np < 4; ++np) load_b(bb[kk][np], uK, 16 * np, k0 + 16 * kk, lane);
-            row_scales<NT>(S, sS, iS);
+                for (int kk = 0; kk < KK; ++kk) load_k(bb[kk], uK, kk);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) row_scales<NT>(S[m], sS[m], iS[m]);
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                uint32_t(&hi)[4] = ah[kk], (&lo)[4] = al[kk], (&b)[4][4] = bb[kk];
-                a_terms(S[2 * kk], S[2 * kk + 1], sS, hi, lo);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], hi, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-                    mma_f16(X[nt], lo, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
-                if (!BF16) {
-#pragma unroll
-                    for (int np = 0; np < 4; ++np)
-                        load_b(b[np], uK + KIMG, 16 * np, k0 + 16 * kk, lane);
+                uint32_t(&b)[4][4] = bb[MT == 1 ? kk : 0];
+                uint32_t hi[MT][4];
+                if (MT > 1) load_k(b, uK, kk);
+                auto add = [&](float(&x)[8][4], const uint32_t(&t)[4]) {
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt)
-                        mma_f16(X[nt], hi, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
+                        mma_f16(x[nt], t, b[nt >> 1][2 * (nt & 1)], b[nt >> 1][2 * (nt & 1) + 1]);
+                };
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t lo[4];
+                    a_terms(S[m][2 * kk], S[m][2 * kk + 1], sS[m], hi[m], lo);
+                    add(X[m], hi[m]);
+                    add(X[m], lo);
+                    if (!SAVE) {
+                        uint4 *d = reinterpret_cast<uint4 *>(turn_at(turn, m) + VB + 4096 + 512) + lane +
+                                   32 * (ZF ? 2 : 1) * (p * KK + kk);
+                        d[0] = make_uint4(hi[m][0], hi[m][1], hi[m][2], hi[m][3]);
+                        if (ZF) d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                if (!BF16) {
+                    load_k(b, uK + KIMG, kk);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) add(X[m], hi[m]);
                 }
             }
-            if (!SAVE) {
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (p * KK + kk);
-                    d[0] = make_uint4(ah[kk][0], ah[kk][1], ah[kk][2], ah[kk][3]);
-                    if (ZF) d[32] = make_uint4(al[kk][0], al[kk][1], al[kk][2], al[kk][3]);
+            for (int m = 0; m < MT; ++m) {
+                if (!SAVE && q4 == 0) {
+                    float *iSs = reinterpret_cast<float *>(turn_at(turn, m) + VB + 4096) + 64;
+                    iSs[16 * p + gq] = iS[m][0], iSs[16 * p + gq + 8] = iS[m][1];
                 }
-                if (q4 == 0) iSs[16 * p + gq] = iS[0], iSs[16 * p + gq + 8] = iS[1];
-            }
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-                part[32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] = make_float4(
-                    iS[0] * X[nt][0], iS[0] * X[nt][1], iS[1] * X[nt][2], iS[1] * X[nt][3]);
+                for (int nt = 0; nt < 8; ++nt)
+                    part[1024 * m + 32 * (8 * (nt >> 1) + 2 * p + (nt & 1))] =
+                        make_float4(iS[m][0] * X[m][nt][0], iS[m][0] * X[m][nt][1],
+                                    iS[m][1] * X[m][nt][2], iS[m][1] * X[m][nt][3]);
+            }
         }
         named_bar(1, 128);  // the first meeting
         // X of block p, in operand form
-        {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            char *at = turn_at(turn, m);
+            uint4 *xfr = reinterpret_cast<uint4 *>(at + VB) + lane;
+            float *iXs = reinterpret_cast<float *>(at + VB + 4096);
+            const float4 *in = part + 1024 * m;
             float X[2][4];
             float4 v4[2];
             load_v<BF16>(v4, at, 16 * p, lane);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float2 ck = *reinterpret_cast<const float2 *>(vec + kVk * C + 16 * p + 8 * x + 2 * q4);
-                const float4 o0 = part[32 * (8 * p + x)], o1 = part[32 * (8 * p + 2 + x)],
-                             o2 = part[32 * (8 * p + 4 + x)], o3 = part[32 * (8 * p + 6 + x)];
+                const float4 o0 = in[32 * (8 * p + x)], o1 = in[32 * (8 * p + 2 + x)],
+                             o2 = in[32 * (8 * p + 4 + x)], o3 = in[32 * (8 * p + 6 + x)];
                 const float4 v = v4[x];
                 X[x][0] = v.x - ck.x * ((o0.x + o1.x) + (o2.x + o3.x));
                 X[x][1] = v.y - ck.y * ((o0.y + o1.y) + (o2.y + o3.y));
@@ -941,10 +972,12 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             xfr[32 * (2 * p)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             xfr[32 * (2 * p + 1)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (q4 == 0) iXs[16 * p + gq] = iX[0], iXs[16 * p + gq + 8] = iX[1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&zready[turn]);
+            if (m == MT - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&zready[turn]);
+            }
             if (SAVE) {
-                float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + gq;
+                float *wx = a.saveX + (((size_t)(slot0 + c) * a.H + h) * C + 16 * p + 2 * q4) * a.dv + v0 + 16 * m + gq;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -966,36 +999,44 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
         for (int jj = 0; jj < HA; ++jj) load_h(jj, jj);
         const float gam = vec[kVs * C];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] *= gam;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][nt][e] *= gam;
         named_bar(1, 128);  // the second meeting
 
         // W'^T = exp(G_C) W^T + X^T H
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
-            const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
-            const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
             const float iH = vec[kVs * C + 1 + jj];
-            const float u0 = iXs[16 * jj + gq] * iH, u1 = iXs[16 * jj + gq + 8] * iH;
             uint32_t(&h2)[KK][4] = bh[jj % HA], (&l2)[KK][4] = bl[jj % HA];
-            float U[NT][4] = {};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16(U[nt], hi, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
+            for (int m = 0; m < MT; ++m) {
+                const char *at = turn_at(turn, m);
+                const uint4 *xfr = reinterpret_cast<const uint4 *>(at + VB) + lane;
+                const float *iXs = reinterpret_cast<const float *>(at + VB + 4096);
+                const uint4 fh = xfr[32 * (2 * jj)], fl = xfr[32 * (2 * jj + 1)];
+                const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
+                const float u0 = iXs[16 * jj + gq] * iH, u1 = iXs[16 * jj + gq + 8] * iH;
+                float U[NT][4] = {};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16(U[nt], lo, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16(U[nt], hi, l2[nt >> 1][2 * (nt & 1)], l2[nt >> 1][2 * (nt & 1) + 1]);
-            if (jj + HA < 4) load_h(jj % HA, jj + HA);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], lo, h2[nt >> 1][2 * (nt & 1)], h2[nt >> 1][2 * (nt & 1) + 1]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                S[nt][0] = fmaf(u0, U[nt][0], S[nt][0]);
-                S[nt][1] = fmaf(u0, U[nt][1], S[nt][1]);
-                S[nt][2] = fmaf(u1, U[nt][2], S[nt][2]);
-                S[nt][3] = fmaf(u1, U[nt][3], S[nt][3]);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(U[nt], hi, l2[nt >> 1][2 * (nt & 1)], l2[nt >> 1][2 * (nt & 1) + 1]);
+                if (m == MT - 1 && jj + HA < 4) load_h(jj % HA, jj + HA);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    S[m][nt][0] = fmaf(u0, U[nt][0], S[m][nt][0]);
+                    S[m][nt][1] = fmaf(u0, U[nt][1], S[m][nt][1]);
+                    S[m][nt][2] = fmaf(u1, U[nt][2], S[m][nt][2]);
+                    S[m][nt][3] = fmaf(u1, U[nt][3], S[m][nt][3]);
+                }
             }
         }
         if (SAVE && c + 1 < nchunk) save(c + 1);
@@ -1004,10 +1045,12 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     if (a.W_out) {
         float *w = a.W_out + ((size_t)n * a.H + h) * state + mine;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[(size_t)(8 * nt + (e & 1)) * a.dv + (e >> 1) * 8] = S[nt][e];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[(size_t)(8 * nt + (e & 1)) * a.dv + 16 * m + (e >> 1) * 8] = S[m][nt][e];
     }
 }
 
@@ -1023,25 +1066,48 @@ cudaError_t prep_inst(const PrepArgs &r, int blocks, cudaStream_t s) {
     return e;
 }
 
-template <int DK, bool BF16, int MODE>
-cudaError_t scan_inst(ScanArgs r, int N, cudaStream_t s) {
+template <int DK, bool BF16, int MODE, int MT>
+constexpr bool scan_fits() {
+    return 2 * chain_stage_bytes<DK, BF16>() + z_stage_bytes<DK, BF16, MODE>() +
+               scan_area_bytes<DK, BF16, MODE, MT>() <= kScanSmem;
+}
+
+template <int DK, bool BF16, int MODE, int MT>
+cudaError_t scan_run(ScanArgs r, int N, cudaStream_t s) {
     constexpr int stage = chain_stage_bytes<DK, BF16>(), zstage = z_stage_bytes<DK, BF16, MODE>();
-    constexpr int area = scan_area_bytes<DK, MODE>();
+    constexpr int area = scan_area_bytes<DK, BF16, MODE, MT>();
     // two stages of the chain's ring at least (the gate frees one when the chain has
     // met it for the next), two of Z's or a third of the chain's where there is room
-    static_assert(2 * stage + zstage + area <= kScanSmem, "shared memory");
+    static_assert(scan_fits<DK, BF16, MODE, MT>(), "shared memory");
     r.stages = 2;
     r.zstages = 2 * (stage + zstage) + area <= kScanSmem ? 2 : 1;
     if (3 * stage + 2 * zstage + area <= kScanSmem) r.stages = 3;
     const int smem = r.stages * stage + r.zstages * zstage + area;
     static SmemOnce once;
-    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE>, kScanSmem);
+    cudaError_t e = once.allow(delta_scan_kernel<DK, BF16, MODE, MT>, kScanSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / 16));
-    delta_scan_kernel<DK, BF16, MODE><<<grid, 384, smem, s>>>(r);
+    const unsigned grid = (unsigned)((long long)N * r.H * (r.dv / (16 * MT)));
+    delta_scan_kernel<DK, BF16, MODE, MT><<<grid, 384, smem, s>>>(r);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(s);
     return e;
+}
+
+template <int DK, bool BF16, int MODE>
+cudaError_t scan_inst(const ScanArgs &r, int N, cudaStream_t s) {
+    // 16 columns a block, or 32 where that saves rounds over the SMs. A chunk of 32
+    // takes 1.6 - 1.8 times one of 16 (the fragments of K and H are loaded once for
+    // both, but the chain's warps are latency-bound and have twice the work), so 32
+    // pay from a ratio of rounds of 9 : 5 on. T 2048, bf16, us with 16 / 32 columns:
+    //   d 64:   64 heads (2 rounds / 1) 74 / 63    96 (3 / 2) 108 / 117   148 (4 / 2) 143 / 119
+    //   d 128:  24 heads (2 rounds / 1) 92 / 86    48 (3 / 2) 139 / 165   148 (8 / 4) 362 / 328
+    // The saving scan, whose stores of W bound it, takes 16 (16 heads of 128, T 8192: 159 / 389).
+    if constexpr (MODE != kSave && scan_fits<DK, BF16, MODE, 2>()) {
+        const long long blocks = (long long)N * r.H * (r.dv / 16);
+        const long long rounds16 = (blocks + 147) / 148, rounds32 = (blocks / 2 + 147) / 148;
+        if (9 * rounds32 < 5 * rounds16) return scan_run<DK, BF16, MODE, 2>(r, N, s);
+    }
+    return scan_run<DK, BF16, MODE, 1>(r, N, s);
 }
 
 template <int DK, bool BF16>

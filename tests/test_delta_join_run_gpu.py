@@ -255,3 +255,21 @@ def test_a_value_that_is_not_a_number_stays_in_its_sequence_and_head(T):
         assert torch.isnan(Z[1, 0, 11:]).any() and torch.isnan(W[1, 0]).any(), name
         assert torch.equal(Z[0], Z0[0]) and torch.equal(W[0], W0[0])
         assert torch.equal(Z[1, 1], Z0[1, 1]) and torch.equal(W[1, 1], W0[1, 1])
+
+
+@pytest.mark.parametrize("dk,dv,dt,H", [(64, 64, "bf16", 38), (64, 128, "fp32", 19),
+                                        (128, 128, "bf16", 19), (128, 64, "fp32", 38)])
+@pytest.mark.parametrize("z_bf16", [False, True])
+def test_more_heads_than_one_round_of_blocks(dk, dv, dt, H, z_bf16):
+    """Just more blocks of 16 columns than SMs, where the scan may take 32 columns a block."""
+    x = make(1, 1, H, 130, dk, dv, dt, seed=H + dk)
+    Z, W = ttt.delta_fwd(**x, w0_per_seq=True, z_bf16=z_bf16)
+    Zr, Wr = od.delta_f64(**x, w0_per_seq=True)
+    assert err(Z, Zr) <= (BF16_TOL if z_bf16 else FWD) and err(W, Wr) <= FWD
+    kw = dict(w0_per_seq=True, z_bf16=z_bf16, seq_start=offsets([0, 0, 65, 120]))
+    x["W0"] = torch.cat([x["W0"], 2 * x["W0"], -x["W0"]])
+    Z = torch.full(x["V"].shape, 7.0, device="cuda", dtype=Z.dtype)
+    _, W = ttt.delta_fwd(**x, Z=Z, **kw)
+    Zr, Wr = od.delta_f64(**x, w0_per_seq=True, seq_start=[0, 0, 65, 120])
+    assert bool((Z[:, :, 120:] == 7).all()) and err(W, Wr) <= FWD
+    assert err(Z[:, :, :120], Zr[:, :, :120]) <= (BF16_TOL if z_bf16 else FWD)
