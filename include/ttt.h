@@ -1,8 +1,10 @@
 /*
  * ttt.h -- C ABI of libttt.so: the forward pass of a Test-Time-Training (TTT)
  * layer on one NVIDIA B200 (sm_100a), the backward passes of TTT-Linear and
- * large-chunk TTT, and the affine-map calls of a sequence-parallel
- * large-chunk forward.
+ * large-chunk TTT, the affine-map calls of a sequence-parallel large-chunk
+ * forward, the gated delta rule (the online linear layer with a forget gate:
+ * forward, backward, decode from a pool of states), and the join between two
+ * blocks (norm, gate, residual, norm) with its backward.
  *
  * What the layer computes. The hidden state of a TTT layer is a fast weight W
  * per (batch, head) sequence: a linear map, or a small MLP. Tokens arrive as
@@ -478,7 +480,11 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  *             (none: its W_out is its start weight), N = n_seq. Offsets must
  *             not decrease and lie in [0, T]; the host cannot see them, so the
  *             kernels clamp them. Rows of Z outside every sequence are left as
- *             they were.
+ *             they were, and no input is read there.
+ * Nothing is checked for being finite: an infinity or a NaN in a token's inputs
+ *   stays in its sequence and the value heads that read it, where it may also
+ *   reach the tokens before it in the same chunk of 64. g is taken as -200 below that (exp(g) is
+ *   0 in fp32); above 0 the weight grows and may overflow.
  * workspace: device memory of at least ttt_delta_workspace_bytes(...) bytes,
  *   256-byte aligned, owned by the caller, clobbered. Calls that share one must
  *   not overlap on the GPU (two captured graphs that may run at the same time

@@ -1,5 +1,5 @@
 // ttt_delta.cu -- the gated delta rule token by token: decode with the states
-// in a pool, and the forward of short sequences.
+// in a pool, and the forward of at most 24 tokens.
 //
 // Per token, with Wd = a W, a = exp(g): rho = v - k Wd, u = eta rho,
 // W = Wd + k^T u, and z = c q W = c (a q W_old + (q.k) u): both products with
@@ -15,8 +15,8 @@
 // cost one reduction over the block and a barrier each, 0.4 - 0.8 us, whatever
 // the number of rows up to about one block an SM partition; that chain, not
 // memory, bounds longer calls, which is why they go chunk by chunk instead.
-// Shorter sums than the rows' 128 terms do not arise: everything is held and
-// added up in fp32, bf16 inputs are exact in it, and only a bf16 Z is rounded.
+// Everything is held and added up in fp32; bf16 inputs are exact in it, and only
+// a bf16 Z is rounded.
 #include "../../include/ttt.h"
 #include "ttt_delta.cuh"
 

