@@ -10,10 +10,13 @@
 //   dK = -D dX W^T + diag(exp(G_C - G) eta) rho Om^T + (phi eta)^T Q + (E + E^T) K,
 //        E_ij = eps_ij eta_j
 //   deta_j = sum_i phi_ij (q_i.k_j) + sum_i eps_ij (k_i.k_j) + exp(G_C - G_j) k_j.(Om rho_j)
-//   dG_i = sum_j eta_j (phi_ij q_i.k_j + eps_ij k_i.k_j) - eta_i (the sums of deta_i)
-//          + q_i.(c D_i W dZ_i) - k_i.(D_i W dX_i),
-//   dG_C += sum_j eta_j exp(G_C - G_j) k_j.(Om rho_j) + exp(G_C) <W, Om>,
-//   dg_t = sum_{i >= t} dG_i.
+//   dg_t = sum_{i >= t} (q_i.(c D_i W dZ_i) - k_i.(D_i W dX_i))
+//          + sum_{j < t <= i} eta_j (phi_ij q_i.k_j + eps_ij k_i.k_j)
+//          + sum_{j < t} eta_j exp(G_C - G_j) k_j.(Om rho_j) + exp(G_C) <W, Om>:
+// what g_t scales, and nothing that would have to cancel (the sums of dL/dG_i from t on
+// hold every pair j, i >= t twice with opposite signs). The pairs across t come one
+// token after the other: t + 1 gains those of column t below the diagonal and loses
+// those of row t left of it.
 // The forward scan runs again first and keeps W at the start of each chunk and
 // X; the reverse scan keeps Om at its end. Everything is fp32, its products two
 // fp16 terms an operand (ttt_delta_mma.cuh). No atomics: every sum has one order.
@@ -489,10 +492,13 @@ __device__ __forceinline__ float2 h2f(uint32_t u) {
 // holds the rows of tokens 16 mt .. 16 mt + 15 and a quarter of the columns.
 // Reads 272 KB and writes 64 KB a chunk at 128 x 128 (bf16), more than a block's
 // shared memory, so one block an SM, whose loads and products take turns. 2048 chunks of
-// 128 x 128 take 436 us (31 us a block; 107 us at the copy rate): issue slots used to 30 %, shared memory 54 %, tensor pipe 27 %, DRAM 19 %; the
-// stalls are waits for loads. Eight warps of 255 registers instead of sixteen of 128,
-// with dZ and dX as fragments from global memory, took 510; W asked for before rho is
-// formed 450 (its registers spill).
+// 128 x 128 take 471 us (34 us a block; 107 us at the copy rate): issue slots used to
+// 30 %, shared memory 54 %, tensor pipe 27 %, DRAM 19 %; the stalls are waits for loads.
+// Eight warps of 255 registers instead of sixteen of 128, with dZ and dX as fragments
+// from global memory, took 17 % longer; W asked for before rho is formed 3 % (its registers
+// spill). The low terms' products in the same sums as the high ones' take 436 us, and
+// double the gradients' errors (8e-7 of a gradient's norm instead of 4.5e-7): the tensor
+// cores cut off what is below a sum's last bit, once a product.
 template <int DK, int DV, bool BF16>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a) {
     extern __shared__ __align__(128) char gsm[];
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
           *iTs = iR + C, *iS = iTs + C, *iZ = iS + 128, *iO = iZ, *rmax = iS, *red = iZ + 128;
     // partial sums over the warps, in the place of rho once it is read
     float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 4 * C, *colp = dotp + 4 * C,
-          *dG = colp + 4 * C, *kt = dG + C;
+          *decp = colp + 4 * C, *diag = decp + 4 * C, *from = diag + C, *upto = from + C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const int mt = warp & 3, hf = warp >> 2;
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         const int srow = tid / LPR, scol = (tid % LPR) * 8;
         // rho = T X: 16 tokens, a quarter of DV
         {
-            float rho[NV][4] = {};
+            float rho[NV][4] = {}, small[NV][4] = {};
             const uint32_t uT = uB + SM::R;
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
@@ -595,8 +601,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(rho[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
-                        mma_f16(rho[2 * np + x], tl, xh[2 * x], xh[2 * x + 1]);
-                        mma_f16(rho[2 * np + x], th, xl[2 * x], xl[2 * x + 1]);
+                        mma_f16(small[2 * np + x], tl, xh[2 * x], xh[2 * x + 1]);
+                        mma_f16(small[2 * np + x], th, xl[2 * x], xl[2 * x + 1]);
                     }
                 }
             }
@@ -605,7 +611,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             for (int nt = 0; nt < NV; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    rho[nt][e] *= iTs[row[e >> 1]] * red[16];
+                    rho[nt][e] = (rho[nt][e] + small[nt][e]) * (iTs[row[e >> 1]] * red[16]);
                     m[e >> 1] = fmaxf(m[e >> 1], fabsf(rho[nt][e]));
                 }
 #pragma unroll
@@ -682,63 +688,65 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         // dZ, then dX, against W and rho
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-            const uint32_t uZ = uB + SM::W + pass * SM::R;
+            uint32_t uZ = uB + SM::W + pass * SM::R;
             const float iz[2] = {iZ[pass * C + row[0]], iZ[pass * C + row[1]]};
-            float N[NK][4] = {};
             float(&cc)[2][4] = pass ? eps : phi;
+            float cs[2][4] = {};
 #pragma unroll
-            for (int kk = 0; kk < KV; ++kk) {
-                uint32_t hi[4], lo[4];
-                ldsm_x4(hi, ldsm_addr(uZ, 16 * mt, 16 * kk, lane));
-                ldsm_x4(lo, ldsm_addr(uZ + C * DV * 2, 16 * mt, 16 * kk, lane));
+            for (int np = 0; np < NK / 2; ++np) {
+                // A's fragments are loaded anew; their addresses are not worth registers
+                asm volatile("" : "+r"(uZ));
+                float N[2][4] = {}, Ns[2][4] = {};
 #pragma unroll
-                for (int np = 0; np < NK / 2; ++np) {
-                    uint32_t wh[4], wl[4];
+                for (int kk = 0; kk < KV; ++kk) {
+                    uint32_t hi[4], lo[4], wh[4], wl[4];
+                    ldsm_x4(hi, ldsm_addr(uZ, 16 * mt, 16 * kk, lane));
+                    ldsm_x4(lo, ldsm_addr(uZ + C * DV * 2, 16 * mt, 16 * kk, lane));
                     load_b(wh, uW, nrow + 16 * np, 16 * kk, lane);
                     load_b(wl, uW + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(N[2 * np + x], hi, wh[2 * x], wh[2 * x + 1]);
-                        mma_f16(N[2 * np + x], lo, wh[2 * x], wh[2 * x + 1]);
-                        mma_f16(N[2 * np + x], hi, wl[2 * x], wl[2 * x + 1]);
+                        mma_f16(N[x], hi, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(Ns[x], lo, wh[2 * x], wh[2 * x + 1]);
+                        mma_f16(Ns[x], hi, wl[2 * x], wl[2 * x + 1]);
+                    }
+                    if (np == 0 && hf <= mt) {  // not above the diagonal
+                        load_b(wh, uR, 16 * hf, 16 * kk, lane);
+                        load_b(wl, uR + C * DV * 2, 16 * hf, 16 * kk, lane);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mma_f16(cc[x], hi, wh[2 * x], wh[2 * x + 1]);
+                            mma_f16(cs[x], lo, wh[2 * x], wh[2 * x + 1]);
+                            mma_f16(cs[x], hi, wl[2 * x], wl[2 * x + 1]);
+                        }
                     }
                 }
-                if (hf <= mt) {  // not above the diagonal
-                    uint32_t rh[4], rl[4];
-                    load_b(rh, uR, 16 * hf, 16 * kk, lane);
-                    load_b(rl, uR + C * DV * 2, 16 * hf, 16 * kk, lane);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(cc[x], hi, rh[2 * x], rh[2 * x + 1]);
-                        mma_f16(cc[x], lo, rh[2 * x], rh[2 * x + 1]);
-                        mma_f16(cc[x], hi, rl[2 * x], rl[2 * x + 1]);
+                        const int nt = 2 * np + y, col = n0 + 8 * nt + 2 * q4;
+                        const float w = (pass ? -dec[x] : a.q_scale * dec[x]) * iz[x];
+                        const float y0 = w * (N[y][2 * x] + Ns[y][2 * x]) * iS[col], y1 = w * (N[y][2 * x + 1] + Ns[y][2 * x + 1]) * iS[col + 1];
+                        const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
+                        const char *im = pass ? sK : sQ;
+                        float2 kq = h2f(*reinterpret_cast<const uint32_t *>(im + o));
+                        if (!BF16) {
+                            const float2 l = h2f(*reinterpret_cast<const uint32_t *>(im + KIMG + o));
+                            kq.x += l.x, kq.y += l.y;
+                        }
+                        const float inv = pass ? iKr[x] : iQr[x];
+                        dot[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), dot[x]);
+                        float *d = pass ? &dK[nt][2 * x] : &dQ[nt][2 * x];
+                        d[0] += y0, d[1] += y1;
                     }
-                }
             }
-#pragma unroll
-            for (int nt = 0; nt < NK; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int col = n0 + 8 * nt + 2 * q4;
-                    const float w = (pass ? -dec[x] : a.q_scale * dec[x]) * iz[x];
-                    const float y0 = w * N[nt][2 * x] * iS[col], y1 = w * N[nt][2 * x + 1] * iS[col + 1];
-                    const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
-                    const char *im = pass ? sK : sQ;
-                    float2 kq = h2f(*reinterpret_cast<const uint32_t *>(im + o));
-                    if (!BF16) {
-                        const float2 l = h2f(*reinterpret_cast<const uint32_t *>(im + KIMG + o));
-                        kq.x += l.x, kq.y += l.y;
-                    }
-                    const float inv = pass ? iKr[x] : iQr[x];
-                    dot[x] = fmaf(inv, fmaf(kq.x, y0, kq.y * y1), dot[x]);
-                    float *d = pass ? &dK[nt][2 * x] : &dQ[nt][2 * x];
-                    d[0] += y0, d[1] += y1;
-                }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    cc[nt][e] *= iz[e >> 1] * iR[16 * hf + 8 * nt + 2 * q4 + (e & 1)];
+                    cc[nt][e] = (cc[nt][e] + cs[nt][e]) *
+                                (iz[e >> 1] * iR[16 * hf + 8 * nt + 2 * q4 + (e & 1)]);
         }
         __syncthreads();  // dZ and dX are read: Om takes their place
         // Om, and <W, Om> with W as it was staged
@@ -769,33 +777,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
         __syncthreads();
         // rho against Om
-        {
-            float N[NK][4] = {};
+        uint32_t uA = uR;
+#pragma unroll
+        for (int np = 0; np < NK / 2; ++np) {
+            asm volatile("" : "+r"(uA));
+            float N[2][4] = {}, Ns[2][4] = {};
 #pragma unroll
             for (int kk = 0; kk < KV; ++kk) {
-                uint32_t hi[4], lo[4];
-                ldsm_x4(hi, ldsm_addr(uR, 16 * mt, 16 * kk, lane));
-                ldsm_x4(lo, ldsm_addr(uR + C * DV * 2, 16 * mt, 16 * kk, lane));
+                uint32_t hi[4], lo[4], wh[4], wl[4];
+                ldsm_x4(hi, ldsm_addr(uA, 16 * mt, 16 * kk, lane));
+                ldsm_x4(lo, ldsm_addr(uA + C * DV * 2, 16 * mt, 16 * kk, lane));
+                load_b(wh, uO, nrow + 16 * np, 16 * kk, lane);
+                load_b(wl, uO + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
 #pragma unroll
-                for (int np = 0; np < NK / 2; ++np) {
-                    uint32_t wh[4], wl[4];
-                    load_b(wh, uO, nrow + 16 * np, 16 * kk, lane);
-                    load_b(wl, uO + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        mma_f16(N[2 * np + x], hi, wh[2 * x], wh[2 * x + 1]);
-                        mma_f16(N[2 * np + x], lo, wh[2 * x], wh[2 * x + 1]);
-                        mma_f16(N[2 * np + x], hi, wl[2 * x], wl[2 * x + 1]);
-                    }
+                for (int x = 0; x < 2; ++x) {
+                    mma_f16(N[x], hi, wh[2 * x], wh[2 * x + 1]);
+                    mma_f16(Ns[x], lo, wh[2 * x], wh[2 * x + 1]);
+                    mma_f16(Ns[x], hi, wl[2 * x], wl[2 * x + 1]);
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < NK; ++nt)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int col = n0 + 8 * nt + 2 * q4;
+                    const int nt = 2 * np + y, col = n0 + 8 * nt + 2 * q4;
                     const float w = rest[x] * iR[row[x]];
-                    const float y0 = w * N[nt][2 * x] * iO[col], y1 = w * N[nt][2 * x + 1] * iO[col + 1];
+                    const float y0 = w * (N[y][2 * x] + Ns[y][2 * x]) * iO[col], y1 = w * (N[y][2 * x + 1] + Ns[y][2 * x + 1]) * iO[col + 1];
                     const uint32_t o = img_off(row[x], n0 + 8 * nt) + 4 * q4;
                     float2 kq = h2f(*reinterpret_cast<const uint32_t *>(sK + o));
                     if (!BF16) {
@@ -811,6 +818,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         // the triangle: q_i.k_j and k_i.k_j of this warp's 16 x 16 block
         float kk2[2][4] = {}, qk2[2][4] = {};
         if (hf <= mt) {
+            float ks[2][4] = {}, qs[2][4] = {};
 #pragma unroll
             for (int k = 0; k < DK; k += 16) {
                 uint32_t ak[4], aq[4], bb[4];
@@ -829,13 +837,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     load_b(bl, uK + KIMG, 16 * hf, k, lane);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(kk2[x], akl, bb[2 * x], bb[2 * x + 1]);
-                        mma_f16(qk2[x], aql, bb[2 * x], bb[2 * x + 1]);
-                        mma_f16(kk2[x], ak, bl[2 * x], bl[2 * x + 1]);
-                        mma_f16(qk2[x], aq, bl[2 * x], bl[2 * x + 1]);
+                        mma_f16(ks[x], akl, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(qs[x], aql, bb[2 * x], bb[2 * x + 1]);
+                        mma_f16(ks[x], ak, bl[2 * x], bl[2 * x + 1]);
+                        mma_f16(qs[x], aq, bl[2 * x], bl[2 * x + 1]);
                     }
                 }
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk2[x][e] += ks[x][e], qk2[x][e] += qs[x][e];
         }
         __syncthreads();  // rho, W and Om are read
         float rs[2] = {0.f, 0.f}, mx[3] = {0.f, 0.f, 0.f};
@@ -852,8 +864,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     p = a.q_scale * gam * phi[nt][e];
                     if (j < i) q = -gam * eps[nt][e];
                     const float w = ikj * (p * qk2[nt][e] * iqi + q * kk2[nt][e] * iki);
-                    cs[e & 1] += w;
-                    rs[e >> 1] = fmaf(eta[j], w, rs[e >> 1]);
+                    if (j < i) {
+                        cs[e & 1] += w;
+                        rs[e >> 1] = fmaf(eta[j], w, rs[e >> 1]);
+                    } else
+                        diag[i] = w;
                     p *= eta[j];
                     q *= eta[j];
                     // as operands: the rows of K and Q they meet carry their scales
@@ -873,13 +888,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float d = dot[x] + rs[x], k2 = ktp[x];
+            float d = dot[x], w = rs[x], k2 = ktp[x];
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
                 d += __shfl_xor_sync(0xffffffffu, d, o);
+                w += __shfl_xor_sync(0xffffffffu, w, o);
                 k2 += __shfl_xor_sync(0xffffffffu, k2, o);
             }
-            if (q4 == 0) rowp[hf * C + row[x]] = d, dotp[hf * C + row[x]] = k2;
+            if (q4 == 0)
+                decp[hf * C + row[x]] = d, rowp[hf * C + row[x]] = w, dotp[hf * C + row[x]] = k2;
         }
 #pragma unroll
         for (int y = 0; y < 3; ++y) {
@@ -934,32 +951,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             }
         }
         if (tid < C) {
-            const float cs = (colp[tid] + colp[C + tid]) + (colp[2 * C + tid] + colp[3 * C + tid]);
-            const float k2 = (dotp[tid] + dotp[C + tid]) + (dotp[2 * C + tid] + dotp[3 * C + tid]);
-            const float rp = (rowp[tid] + rowp[C + tid]) + (rowp[2 * C + tid] + rowp[3 * C + tid]);
-            if (tid < len) a.deta[hrow + tid] = cs + k2;
-            dG[tid] = rp - eta[tid] * (cs + k2);
-            kt[tid] = eta[tid] * k2;
+            auto sum4 = [&](const float *v) {
+                return (v[tid] + v[C + tid]) + (v[2 * C + tid] + v[3 * C + tid]);
+            };
+            const float cs = sum4(colp), k2 = sum4(dotp);
+            if (tid < len) a.deta[hrow + tid] = (cs + diag[tid]) + k2;
+            from[tid] = sum4(decp);
+            upto[tid] = eta[tid] * (cs + k2) - sum4(rowp);
         }
         __syncthreads();
         if (a.dg && warp == 15) {
-            // sums in double: the terms of later tokens cancel. Lane l holds tokens 2 l, 2 l + 1.
-            const double d0 = dG[2 * lane], d1 = dG[2 * lane + 1];
-            double s = d0 + d1, w = (double)kt[2 * lane] + (double)kt[2 * lane + 1];
-            double d = lane < 16 ? (double)red[32 + lane] : 0.0;
+            // sums over tokens in double. Lane l holds tokens 2 l, 2 l + 1.
+            const double a0 = from[2 * lane], a1 = from[2 * lane + 1];
+            const double b0 = upto[2 * lane], b1 = upto[2 * lane + 1];
+            double s = a0 + a1, u = b0 + b1, d = lane < 16 ? (double)red[32 + lane] : 0.0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const double v = __shfl_down_sync(0xffffffffu, s, o);
                 if (lane + o < 32) s += v;
-                w += __shfl_xor_sync(0xffffffffu, w, o);
+                const double w = __shfl_up_sync(0xffffffffu, u, o);
+                if (lane >= o) u += w;
                 d += __shfl_xor_sync(0xffffffffu, d, o);
             }
-            w += (double)expf(GC + GCl) * d;
-            // s holds the tokens from 2 l on
+            // s: from token 2 l on, u: up to token 2 l + 1
             const double later = __shfl_down_sync(0xffffffffu, s, 1);
-            if (2 * lane < len) a.dg[hrow + 2 * lane] = (float)(s + w);
+            const double before = __shfl_up_sync(0xffffffffu, u, 1);
+            const double c0 = lane > 0 ? before : 0.0, wo = (double)expf(GC + GCl) * d;
+            if (2 * lane < len) a.dg[hrow + 2 * lane] = (float)(s + c0 + wo);
             if (2 * lane + 1 < len)
-                a.dg[hrow + 2 * lane + 1] = (float)(d1 + (lane < 31 ? later : 0.0) + w);
+                a.dg[hrow + 2 * lane + 1] = (float)(a1 + (lane < 31 ? later : 0.0) + (c0 + b0) + wo);
         }
         // dQ += (phi eta) K, dK += (phi eta)^T Q + (E + E^T) K
         const uint32_t u1 = smem_u32(i1), u2 = smem_u32(i2), u3 = smem_u32(i3);

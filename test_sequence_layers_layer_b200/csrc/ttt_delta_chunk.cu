@@ -268,8 +268,10 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
     if (warp == 0) sum_gates();
     __syncthreads();
 
-    // k_i.k_j or q_i.k_j of this warp's 16 rows i, columns j up to the diagonal
-    float kk[8][4] = {};
+    // k_i.k_j or q_i.k_j of this warp's 16 rows i, columns j up to the diagonal; products
+    // of low terms in sums of their own (the tensor cores cut off what is below a
+    // sum's last bit, once a product)
+    float kk[8][4] = {}, small[BF16 ? 1 : 8][4] = {};
     const uint32_t uK = smem_u32(sK), uA = forw ? uK : smem_u32(sQ);
 #pragma unroll
     for (int k = 0; k < DK; k += 16) {
@@ -284,15 +286,21 @@ __global__ void __launch_bounds__(kPrepThreads, 2) delta_prep_kernel(PrepArgs a)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 mma_f16(kk[2 * np + x], ah, bb[2 * x], bb[2 * x + 1]);
-                if (!BF16) mma_f16(kk[2 * np + x], al, bb[2 * x], bb[2 * x + 1]);
+                if (!BF16) mma_f16(small[BF16 ? 0 : 2 * np + x], al, bb[2 * x], bb[2 * x + 1]);
             }
             if (!BF16) {
                 load_b(bb, uK + KIMG, 16 * np, k, lane);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) mma_f16(kk[2 * np + x], ah, bb[2 * x], bb[2 * x + 1]);
+                for (int x = 0; x < 2; ++x)
+                    mma_f16(small[BF16 ? 0 : 2 * np + x], ah, bb[2 * x], bb[2 * x + 1]);
             }
         }
     }
+    if (!BF16)
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kk[nt][e] += small[BF16 ? 0 : nt][e];
 
     for (int r = 0; r < rep; ++r) {
         const int h = hk * rep + r;

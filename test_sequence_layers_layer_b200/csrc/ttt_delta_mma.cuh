@@ -5,7 +5,9 @@
 // [2^13, 2^14), x s = hi + lo + e, hi = fp16(x s), lo = fp16(x s - hi) and |e| <= 2^-22
 // of |x s| (2^-25 absolute for the elements more than 2^17 below the largest): the
 // precision of fp32 products, in two or three fp16 products (lo lo is left
-// out) instead of the three or six that bf16 terms would take for the same bits. A
+// out) instead of the three or six that bf16 terms would take for the same bits. Where a
+// sum runs over many steps, hi hi and the others go to accumulators of their own: the
+// tensor cores cut a sum off below its last bit at every step, and so a third as often. A
 // bf16 operand is one term, exact in fp16 (8 bits of 11) down to 2^-27 of its
 // row's largest size. The scales are taken out again in fp32, where the rows of
 // the result are scaled anyway.

@@ -288,3 +288,19 @@ def test_gates_above_zero(T):
     ref = od.delta_grads(*(x[n] for n in RULE), dZ, None, w0_per_seq=True)
     for n, r in ref.items():
         assert err(g[n], r) <= BWD, n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,starts", [(1, None), (10, list(range(11))), (150, [0, 1, 70, 150])])
+def test_a_decay_of_nothing_has_no_gradient(T, starts, dt):
+    """Without a start weight the first token's decay scales zero: its gradient is exactly 0."""
+    N = 1 if starts is None else len(starts) - 1
+    x = make(1, 2, 4, T, 128, 64, dt, seed=T, N=N)
+    gen = torch.Generator().manual_seed(3)
+    dZ, dW = torch.randn(x["V"].shape, generator=gen), torch.randn((N, 4, 128, 64), generator=gen)
+    kw = {} if starts is None else dict(seq_start=offsets(starts))
+    g = ttt.delta_bwd(*(x[n] for n in RULE[:5]), None, dZ.cuda(), dW.cuda(), **kw)["g"]
+    first = [0] if starts is None else starts[:-1]
+    assert not g[:, :, first].any()
+    ref = od.delta_grads(*(x[n] for n in RULE[:5]), None, dZ, dW, seq_start=starts)["g"]
+    assert float((g.double().cpu() - ref).abs().max()) <= BWD * float(ref.abs().max())
