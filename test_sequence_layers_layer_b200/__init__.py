@@ -712,18 +712,19 @@ def _tensors(fn, index, **want):
 class _On:
     """The device and the stream of a call: empty() allocates for it, run() makes it."""
 
-    __slots__ = ("fn", "index", "device", "handle", "side", "torch", "held")
+    __slots__ = ("fn", "index", "handle", "side", "torch", "held")
 
     def __init__(self, fn, first, stream):
         import torch
-        if not first.is_cuda:
+        index = first.get_device()
+        if index < 0:
             raise ValueError(f"{fn}: tensors must be on a CUDA device, got {first.device}")
-        self.torch, self.fn, self.device, self.side = torch, fn, first.device, None
-        self.index = index = first.get_device()
+        self.torch, self.fn, self.index, self.side = torch, fn, index, None
+        if stream is None:  # the address alone: a Stream object costs a microsecond
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
+            return
         current = torch.cuda.current_stream(index)
         self.handle = current.cuda_stream
-        if stream is None:
-            return
         if isinstance(stream, int):
             # 0 is the legacy default stream, which torch knows as its default stream
             stream = torch.cuda.ExternalStream(stream, device=first.device) if stream else \
@@ -742,7 +743,7 @@ class _On:
                     t.record_stream(self.side)
 
     def empty(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        t = self.torch.empty(shape, dtype=dtype, device=self.index)
         if self.side is not None:
             # memory the current stream may still be using: the call waits for
             # that, and the block is not handed out again before the call is done
@@ -763,9 +764,9 @@ class _On:
             # thread's allocation on this stream could be put in its place
             self.held = self.empty(max(need, 256), self.torch.uint8)
             return self.held.data_ptr(), max(need, 256)
-        self.uses(given)
         if given.get_device() != self.index or not given.is_contiguous():
             raise ValueError(f"{self.fn}: workspace must be contiguous and on cuda:{self.index}")
+        self.uses(given)
         return given.data_ptr(), given.numel() * given.element_size()
 
     def run(self, name, f, *args):
@@ -860,17 +861,9 @@ def delta_bwd(Q, K, V, eta, g, W0, dZ, dW_out=None, *, w0_per_seq=False, seq_sta
     return grads
 
 
-def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, Z=None,
-                        stream=None):
-    """n tokens of the gated delta rule per row, the states updated in place (ttt_delta_decode).
-    Q, K [B, Hk, n, dk], V [B, H, n, dv], eta and g (or None) [B, H, n] fp32, W
-    [slots, H, dk, dv] fp32; row b continues state state_index[b] (int32 [B]; None: state b).
-    Rows whose index is outside the pool are padding: their Z is left as it is (undefined in a
-    new Z). The other rows' indices must be distinct. Returns Z [B, H, n, dv]."""
-    import torch
-    on = _On("delta_decode", Q, stream)
-    B, Hk, H, n, dk, dv, _, _, code = _delta_shapes("delta_decode", on.index, Q, K, V, eta, g, None,
-                                                    False, None)
+def _delta_decode(on, Q, K, V, eta, g, W, state_index, q_scale, z_bf16, Z, B, Hk, H, n, dk, dv):
+    """The decode call, Q, K, V, eta and g being checked already."""
+    torch = on.torch
     zt = torch.bfloat16 if z_bf16 else torch.float32
     if W.dim() != 4:
         raise ValueError("delta_decode: W must be [slots, H, dk, dv]")
@@ -878,24 +871,44 @@ def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_
     if Z is None:
         Z = on.like(V, zt)
     else:
-        _tensors("delta_decode", on.index, Z=(Z, (zt,), (B, H, n, dv)))
+        _tensors("delta_decode", on.index, Z=(Z, (zt,), V.shape))
     _tensors("delta_decode", on.index, W=(W, (torch.float32,), (slots, H, dk, dv)),
              state_index=(state_index, (torch.int32,), (B,)))
     on.uses(Q, K, V, eta, g, W, Z, state_index)
     on.run("ttt_delta_decode", lib().ttt_delta_decode, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
            eta.data_ptr(), _p(g), W.data_ptr(), Z.data_ptr(), _p(state_index), slots, q_scale, B,
-           Hk, H, n, dk, dv, code, TTT_F_Z_BF16 if z_bf16 else 0)
+           Hk, H, n, dk, dv, _dtype_code(Q), TTT_F_Z_BF16 if z_bf16 else 0)
     return Z
+
+
+def delta_decode_tokens(Q, K, V, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, Z=None,
+                        stream=None):
+    """n tokens of the gated delta rule per row, the states updated in place (ttt_delta_decode).
+    Q, K [B, Hk, n, dk], V [B, H, n, dv], eta and g (or None) [B, H, n] fp32, W
+    [slots, H, dk, dv] fp32; row b continues state state_index[b] (int32 [B]; None: state b).
+    Rows whose index is outside the pool are padding: their Z is left as it is (undefined in a
+    new Z). The other rows' indices must be distinct. Returns Z [B, H, n, dv]."""
+    on = _On("delta_decode", Q, stream)
+    B, Hk, H, n, dk, dv, _, _, _ = _delta_shapes("delta_decode", on.index, Q, K, V, eta, g, None,
+                                                 False, None)
+    return _delta_decode(on, Q, K, V, eta, g, W, state_index, q_scale, z_bf16, Z, B, Hk, H, n, dk,
+                         dv)
 
 
 def delta_decode(q, k, v, eta, g, W, *, state_index=None, q_scale=1.0, z_bf16=False, z=None,
                  stream=None):
     """delta_decode_tokens for one token per row: q, k [B, Hk, dk], v [B, H, dv], eta and g (or
     None) [B, H]. Returns z [B, H, dv]."""
-    one = lambda t: None if t is None else t.unsqueeze(2)  # noqa: E731
-    return delta_decode_tokens(one(q), one(k), one(v), one(eta), one(g), W,
-                               state_index=state_index, q_scale=q_scale, z_bf16=z_bf16, Z=one(z),
-                               stream=stream).squeeze(2)
+    on = _On("delta_decode", q, stream)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("delta_decode: q, k, v must be [B, heads, d]")
+    B, Hk, dk = q.shape
+    _, H, dv = v.shape
+    f32, same = (on.torch.float32,), (q.dtype,)
+    _tensors("delta_decode", on.index, q=(q, same, (B, Hk, dk)), k=(k, same, (B, Hk, dk)),
+             v=(v, same, (B, H, dv)), eta=(eta, f32, (B, H)), g=(g, f32, (B, H)))
+    return _delta_decode(on, q, k, v, eta, g, W, state_index, q_scale, z_bf16, z, B, Hk, H, 1, dk,
+                         dv)
 
 
 _ACTS = {"silu": 0, "sigmoid": TTT_F_GATE_SIGMOID}
