@@ -14,8 +14,8 @@
 // squares; the next row's loads are on their way meanwhile. The norm of a head is a
 // shuffle among its d / 8 threads; the norm of the row a block reduction with one
 // barrier. Sums and statistics are fp32.
-// 32,768 rows of 8 x 128, bf16 with fp32 z, RMS norms: forward 77 us (403 MB at
-// 5.2 TB/s, 0.81 of the copy rate; issue slots used to 59 %), backward 160 us and 8 us
+// 32,768 rows of 8 x 128, bf16 with fp32 z, RMS norms: forward 76 us (403 MB at
+// 5.3 TB/s, 0.82 of the copy rate; issue slots used to 62 %), backward 160 us and 8 us
 // for the parameters' sums (940 MB at 5.6 TB/s, 0.86). Without loads ahead, with exact
 // divisions and two-barrier sums they took 170 and 257 us.
 //
@@ -225,14 +225,16 @@ __global__ void __launch_bounds__(NT, 512 / NT) join_fwd_kernel(JoinArgs a) {
         if (a.Z) {
             norm_v(z, inv_d, a.eps, a.rms, live, hsum);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float y = s[j] * fmaf(z[j], g1[j], b1[j]);
-                if (a.gate) {
+            for (int j = 0; j < V; ++j) z[j] = s[j] * fmaf(z[j], g1[j], b1[j]);
+            if (a.gate) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
                     const float sg = sigmoid(g[j]);
-                    y *= a.silu ? g[j] * sg : sg;
+                    z[j] *= a.silu ? g[j] * sg : sg;
                 }
-                r[j] += y;
             }
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[j] += z[j];
             if (live) store_v<BF16>(a.R, at, r);
         }
         if (a.Hn) {
