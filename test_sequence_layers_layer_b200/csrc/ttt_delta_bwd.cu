@@ -492,13 +492,13 @@ __device__ __forceinline__ float2 h2f(uint32_t u) {
 // holds the rows of tokens 16 mt .. 16 mt + 15 and a quarter of the columns.
 // Reads 272 KB and writes 64 KB a chunk at 128 x 128 (bf16), more than a block's
 // shared memory, so one block an SM, whose loads and products take turns. 2048 chunks of
-// 128 x 128 take 471 us (34 us a block; 107 us at the copy rate): issue slots used to
-// 30 %, shared memory 54 %, tensor pipe 27 %, DRAM 19 %; the stalls are waits for loads.
-// Eight warps of 255 registers instead of sixteen of 128, with dZ and dX as fragments
-// from global memory, took 17 % longer; W asked for before rho is formed 3 % (its registers
-// spill). The low terms' products in the same sums as the high ones' take 436 us, and
-// double the gradients' errors (8e-7 of a gradient's norm instead of 4.5e-7): the tensor
-// cores cut off what is below a sum's last bit, once a product.
+// 128 x 128 take 434 us (31 us a block; 107 us at the copy rate): issue slots used to
+// 30 %, shared memory 57 %, tensor pipe 26 %, DRAM 19 %; the stalls are waits for loads,
+// shared memory and barriers. Eight warps of 255 registers instead of sixteen of 128, with
+// dZ and dX as fragments from global memory, took 17 % longer, W asked for before rho is
+// formed 3 %. The low terms' products in the same sums as the high ones' would take 8 %
+// less, and double the gradients' errors (8e-7 of a gradient's norm instead of 4.5e-7): the
+// tensor cores cut off what is below a sum's last bit, once a product.
 template <int DK, int DV, bool BF16>
 __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a) {
     extern __shared__ __align__(128) char gsm[];
@@ -530,6 +530,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     const int rep = a.H / a.Hk;
     const int row[2] = {16 * mt + gq, 16 * mt + gq + 8};
     const int n0 = hf * (DK / 4);  // this warp's columns of DK
+    // this lane's places in an image for fragments of A (rows of block mt), of B with rows as
+    // n (from row 0) and as k (columns from 0): steps of 16 rows are 2048 bytes, of 16
+    // columns step16()
+    const uint32_t oA = ldsm_addr(0, 16 * mt, 0, lane);
+    const int rB = ((lane >> 4) << 3) + (lane & 7), cB = ((lane >> 3) & 1) * 8;
+    const int rT = (lane & 7) + ((lane >> 3) & 1) * 8, cT = (lane >> 4) * 8;
+    const uint32_t oB = img_off(rB, cB), oX = img_off(rT, hf * (DV / 4) + cT), oK = img_off(rT, n0 + cT);
 
     for (int r = 0; r < rep; ++r) {
         const int h = hk * rep + r;
@@ -591,13 +598,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             for (int jj = 0; jj < 4; ++jj) {
                 if (jj > mt) break;
                 uint32_t th[4], tl[4];
-                ldsm_x4(th, ldsm_addr(uT, 16 * mt, 16 * jj, lane));
-                ldsm_x4(tl, ldsm_addr(uT + kImg, 16 * mt, 16 * jj, lane));
+                ldsm_x4(th, step16(uT + oA, jj));
+                ldsm_x4(tl, step16(uT + oA, jj) + kImg);
 #pragma unroll
                 for (int np = 0; np < NV / 2; ++np) {
                     uint32_t xh[4], xl[4];
-                    load_bt(xh, uB, 16 * jj, hf * (DV / 4) + 16 * np, lane);
-                    load_bt(xl, uB + C * DV * 2, 16 * jj, hf * (DV / 4) + 16 * np, lane);
+                    ldsm_x4_t(xh, step16(uB + oX, np) + 2048 * jj);
+                    ldsm_x4_t(xl, step16(uB + oX, np) + 2048 * jj + C * DV * 2);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(rho[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
@@ -681,29 +688,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             dec[x] = expf(Gh[row[x]] + Gl[row[x]]);
             rest[x] = expf((GC - Gh[row[x]]) + (GCl - Gl[row[x]]));
         }
-        const uint32_t uW = uB + (n0 >> 6) * SM::R, uO = uW + SM::W;
-        const int nrow = n0 & 63;
+        // rows n0 .. of W and of Om
+        const uint32_t uW = uB + (n0 >> 6) * SM::R + (n0 & 63) * 128, uO = uW + SM::W;
         float phi[2][4] = {}, eps[2][4] = {};  // tokens 16 hf + ..
         float dot[2] = {0.f, 0.f}, ktp[2] = {0.f, 0.f};
         // dZ, then dX, against W and rho
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-            uint32_t uZ = uB + SM::W + pass * SM::R;
+            const uint32_t uZ = uB + SM::W + pass * SM::R;
             const float iz[2] = {iZ[pass * C + row[0]], iZ[pass * C + row[1]]};
             float(&cc)[2][4] = pass ? eps : phi;
             float cs[2][4] = {};
 #pragma unroll
             for (int np = 0; np < NK / 2; ++np) {
-                // A's fragments are loaded anew; their addresses are not worth registers
-                asm volatile("" : "+r"(uZ));
                 float N[2][4] = {}, Ns[2][4] = {};
-#pragma unroll
+#pragma unroll 4  // all eight: more loads ahead than registers (297 bytes spilled, 36 us)
                 for (int kk = 0; kk < KV; ++kk) {
                     uint32_t hi[4], lo[4], wh[4], wl[4];
-                    ldsm_x4(hi, ldsm_addr(uZ, 16 * mt, 16 * kk, lane));
-                    ldsm_x4(lo, ldsm_addr(uZ + C * DV * 2, 16 * mt, 16 * kk, lane));
-                    load_b(wh, uW, nrow + 16 * np, 16 * kk, lane);
-                    load_b(wl, uW + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
+                    ldsm_x4(hi, step16(uZ + oA, kk));
+                    ldsm_x4(lo, step16(uZ + oA, kk) + C * DV * 2);
+                    ldsm_x4(wh, step16(uW + oB, kk) + 2048 * np);
+                    ldsm_x4(wl, step16(uW + oB, kk) + 2048 * np + C * DV * 2);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(N[x], hi, wh[2 * x], wh[2 * x + 1]);
@@ -711,8 +716,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                         mma_f16(Ns[x], hi, wl[2 * x], wl[2 * x + 1]);
                     }
                     if (np == 0 && hf <= mt) {  // not above the diagonal
-                        load_b(wh, uR, 16 * hf, 16 * kk, lane);
-                        load_b(wl, uR + C * DV * 2, 16 * hf, 16 * kk, lane);
+                        ldsm_x4(wh, step16(uR + oB + 2048 * hf, kk));
+                        ldsm_x4(wl, step16(uR + oB + 2048 * hf, kk) + C * DV * 2);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             mma_f16(cc[x], hi, wh[2 * x], wh[2 * x + 1]);
@@ -777,18 +782,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
         __syncthreads();
         // rho against Om
-        uint32_t uA = uR;
 #pragma unroll
         for (int np = 0; np < NK / 2; ++np) {
-            asm volatile("" : "+r"(uA));
             float N[2][4] = {}, Ns[2][4] = {};
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < KV; ++kk) {
                 uint32_t hi[4], lo[4], wh[4], wl[4];
-                ldsm_x4(hi, ldsm_addr(uA, 16 * mt, 16 * kk, lane));
-                ldsm_x4(lo, ldsm_addr(uA + C * DV * 2, 16 * mt, 16 * kk, lane));
-                load_b(wh, uO, nrow + 16 * np, 16 * kk, lane);
-                load_b(wl, uO + C * DV * 2, nrow + 16 * np, 16 * kk, lane);
+                ldsm_x4(hi, step16(uR + oA, kk));
+                ldsm_x4(lo, step16(uR + oA, kk) + C * DV * 2);
+                ldsm_x4(wh, step16(uO + oB, kk) + 2048 * np);
+                ldsm_x4(wl, step16(uO + oB, kk) + 2048 * np + C * DV * 2);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     mma_f16(N[x], hi, wh[2 * x], wh[2 * x + 1]);
@@ -820,11 +823,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         if (hf <= mt) {
             float ks[2][4] = {}, qs[2][4] = {};
 #pragma unroll
-            for (int k = 0; k < DK; k += 16) {
+            for (int k = 0; k < DK / 16; ++k) {
                 uint32_t ak[4], aq[4], bb[4];
-                ldsm_x4(ak, ldsm_addr(uK, 16 * mt, k, lane));
-                ldsm_x4(aq, ldsm_addr(uQ, 16 * mt, k, lane));
-                load_b(bb, uK, 16 * hf, k, lane);
+                ldsm_x4(ak, step16(uK + oA, k));
+                ldsm_x4(aq, step16(uQ + oA, k));
+                ldsm_x4(bb, step16(uK + oB + 2048 * hf, k));
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     mma_f16(kk2[x], ak, bb[2 * x], bb[2 * x + 1]);
@@ -832,9 +835,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 }
                 if (!BF16) {
                     uint32_t akl[4], aql[4], bl[4];
-                    ldsm_x4(akl, ldsm_addr(uK + KIMG, 16 * mt, k, lane));
-                    ldsm_x4(aql, ldsm_addr(uQ + KIMG, 16 * mt, k, lane));
-                    load_b(bl, uK + KIMG, 16 * hf, k, lane);
+                    ldsm_x4(akl, step16(uK + oA, k) + KIMG);
+                    ldsm_x4(aql, step16(uQ + oA, k) + KIMG);
+                    ldsm_x4(bl, step16(uK + oB + 2048 * hf, k) + KIMG);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(ks[x], akl, bb[2 * x], bb[2 * x + 1]);
@@ -983,17 +986,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
         // dQ += (phi eta) K, dK += (phi eta)^T Q + (E + E^T) K
         const uint32_t u1 = smem_u32(i1), u2 = smem_u32(i2), u3 = smem_u32(i3);
+        const uint32_t oAt = img_off(rB, 16 * mt + cB);  // A read across
 #pragma unroll
         for (int np = 0; np < NK / 2; ++np) {
             float q[2][4] = {}, k[2][4] = {}, e[2][4] = {};
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 uint32_t bk[4], bq[4], bkl[4], bql[4], ah[4], al[4];
-                load_bt(bk, uK, 16 * jj, n0 + 16 * np, lane);
-                load_bt(bq, uQ, 16 * jj, n0 + 16 * np, lane);
+                ldsm_x4_t(bk, step16(uK + oK, np) + 2048 * jj);
+                ldsm_x4_t(bq, step16(uQ + oK, np) + 2048 * jj);
                 if (!BF16) {
-                    load_bt(bkl, uK + KIMG, 16 * jj, n0 + 16 * np, lane);
-                    load_bt(bql, uQ + KIMG, 16 * jj, n0 + 16 * np, lane);
+                    ldsm_x4_t(bkl, step16(uK + oK, np) + 2048 * jj + KIMG);
+                    ldsm_x4_t(bql, step16(uQ + oK, np) + 2048 * jj + KIMG);
                 }
                 auto add = [&](float(&acc)[2][4], const uint32_t(&bh)[4], const uint32_t(&bl)[4]) {
 #pragma unroll
@@ -1004,19 +1008,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     }
                 };
                 if (jj <= mt) {
-                    ldsm_x4(ah, ldsm_addr(u1, 16 * mt, 16 * jj, lane));
-                    ldsm_x4(al, ldsm_addr(u1 + kImg, 16 * mt, 16 * jj, lane));
+                    ldsm_x4(ah, step16(u1 + oA, jj));
+                    ldsm_x4(al, step16(u1 + oA, jj) + kImg);
                     add(q, bk, bkl);
                 }
                 if (jj >= mt) {  // A = (phi eta)^T: read across
-                    const uint32_t o = img_off(16 * jj + (lane & 7) + ((lane >> 4) << 3),
-                                               16 * mt + ((lane >> 3) & 1) * 8);
-                    ldsm_x4_t(ah, u2 + o);
-                    ldsm_x4_t(al, u2 + kImg + o);
+                    ldsm_x4_t(ah, u2 + oAt + 2048 * jj);
+                    ldsm_x4_t(al, u2 + oAt + 2048 * jj + kImg);
                     add(k, bq, bql);
                 }
-                ldsm_x4(ah, ldsm_addr(u3, 16 * mt, 16 * jj, lane));
-                ldsm_x4(al, ldsm_addr(u3 + kImg, 16 * mt, 16 * jj, lane));
+                ldsm_x4(ah, step16(u3 + oA, jj));
+                ldsm_x4(al, step16(u3 + oA, jj) + kImg);
                 add(e, bk, bkl);
             }
 #pragma unroll

@@ -81,6 +81,12 @@ __device__ __forceinline__ uint32_t img_off(int row, int col) {
                       ((((col & 63) >> 3) ^ (row & 7)) << 4));
 }
 
+// An address inside an image, k steps of 16 columns on. The steps must not carry into a bit
+// that the first column has; images stand at multiples of 128 bytes.
+__device__ __forceinline__ uint32_t step16(uint32_t at, int k) {
+    return (at ^ ((k & 3) << 5)) + (k >> 2) * (C * 128);
+}
+
 // Shared address of this lane's row for an ldmatrix.x4 of a 16 x 16 block at
 // (row, col). Plain, as A: registers a0..a3. Plain, as B with the rows as n and
 // the columns as k: {b0, b1} of the first 8 rows, then of the next 8 (order 0, 2 / 1, 3).
