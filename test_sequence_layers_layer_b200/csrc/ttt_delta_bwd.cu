@@ -1042,17 +1042,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             }
 }
 
-// Sum over the sequences of a shared start weight's gradient, in order.
-__global__ void __launch_bounds__(256) delta_sum_kernel(const float *per_seq, float *out, int N,
-                                                        size_t n4) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+// Sum over the sequences of a shared start weight's gradient, in order, sixteen loads
+// on their way. Bound by their latency, the order being fixed: 512 sequences of 16 heads of
+// 128 x 128, 537 MB, in 111 us, of 2 heads in 97 (124 and 113 in blocks of 256, one by one).
+constexpr int kSumThreads = 64;
+__global__ void __launch_bounds__(kSumThreads) delta_sum_kernel(const float *per_seq, float *out,
+                                                                int N, size_t n4) {
+    const size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x;
     if (i >= n4) return;
     const float4 *p = reinterpret_cast<const float4 *>(per_seq) + i;
-    float4 s = p[0];
-    for (int k = 1; k < N; ++k) {
-        const float4 v = p[(size_t)k * n4];
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    int k = 0;
+    for (; k + 16 <= N; k += 16, p += 16 * n4) {
+        float4 v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = p[j * n4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) add(v[j]);
     }
+    for (; k < N; ++k, p += n4) add(*p);
     reinterpret_cast<float4 *>(out)[i] = s;
 }
 
@@ -1177,7 +1186,8 @@ cudaError_t launch_delta_bwd(const DeltaBwdArgs &g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (sum) {
         const size_t n4 = (size_t)a.H * a.dk * a.dv / 4;
-        delta_sum_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(sums, g.dW0, a.N, n4);
+        delta_sum_kernel<<<(unsigned)((n4 + kSumThreads - 1) / kSumThreads), kSumThreads, 0, s>>>(
+            sums, g.dW0, a.N, n4);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         count_launch(s);
