@@ -390,16 +390,14 @@ bool join_supported(int H, int d) {
 namespace {
 int join_threads(int H, int d) { return (H * d / V + 31) / 32 * 32; }
 // Blocks of the persistent kernels: as many as are resident at 128 registers a
-// thread, at most one per row; in the backward eight of one warp or of two (more partial
-// rows to add up then cost what they gain: 200,000 rows of 64, 289 + 17 us with sixteen,
-// 279 + 10 with eight; the forward takes 89 and 136) and three of up to four warps. The
-// count depends on the shape alone, so the order of the parameter sums is the same in
-// every call. Rows of more than 1024 channels leave one or two blocks an SM, whose phases
-// overlap less: 8192 rows of 4096, backward, 360 us at a floor of 146.
+// thread (168 in the backward's narrow blocks), at most one per row: 200,000 rows of 64
+// take 88 and 209 us (136 and 279 with eight blocks an SM, 6 heads of 64 and 65,536 rows
+// 149 instead of 205, of which a third had to wait for a second round). The count depends
+// on the shape alone, so the order of the parameter sums is the same in every call. Rows
+// of more than 1024 channels leave one or two blocks an SM, whose phases overlap less:
+// 8192 rows of 4096, backward, 359 us at a floor of 146.
 int join_blocks(long long rows, int nt, bool bwd) {
-    int per_sm = 512 / nt;
-    if (bwd && per_sm > 8) per_sm = 8;
-    if (bwd && nt > 64 && nt <= kJoinThreads) per_sm = 3;
+    const int per_sm = (bwd && nt <= kJoinThreads ? 384 : 512) / nt;
     const long long n = 148LL * (per_sm < 1 ? 1 : per_sm);
     return (int)(rows < n ? rows : n);
 }
