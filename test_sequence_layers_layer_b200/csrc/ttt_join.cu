@@ -28,9 +28,12 @@
 namespace ttt {
 namespace {
 
-// Blocks of up to 128 threads (rows of up to 1024 channels) may take 168 registers a
-// thread and keep the parameters in them; blocks of up to 512 (D <= 4096) have 128.
-constexpr int kJoinThreads = 128, kJoinMaxThreads = 512;
+// Threads of the largest blocks of an instance. The forward: up to 128 (rows of up to
+// 1024 channels), four blocks an SM, and up to 512 (D <= 4096). The backward keeps the
+// parameters in registers up to 384 threads (192: two blocks of 168 registers an SM, so
+// three of 128 threads; 256 and 384: one block); the 512-thread blocks have 128 registers
+// and read them again for each row.
+constexpr int kJoinThreads = 128, kJoinBwdThreads = 192, kJoinMaxThreads = 512;
 constexpr int kJoinParams = 5;        // scale, gamma1, beta1, gamma2, beta2
 
 constexpr int V = 8;  // channels of a thread
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) join_fwd_kernel(JoinArgs a) {
 }
 
 template <int NT, bool BF16, bool ZBF16>
-__global__ void __launch_bounds__(NT, NT == kJoinThreads ? 3 : 1) join_bwd_kernel(JoinBwdArgs a) {
+__global__ void __launch_bounds__(NT, NT == kJoinBwdThreads ? 2 : 1) join_bwd_kernel(JoinBwdArgs a) {
     __shared__ __align__(16) float slots[32];
     const int D = a.H * a.d, c = threadIdx.x * V;
     const bool live = c < D;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(NT, NT == kJoinThreads ? 3 : 1) join_bwd_kerne
     __syncthreads();
     Sums sums{slots, (int)(blockDim.x >> 5), a.H == 1 ? 0 : a.d / V, 0};
     const float inv_d = 1.f / (float)a.d, inv_D = 1.f / (float)D;
-    constexpr bool KEEP = NT == kJoinThreads;  // else the parameters are read again for each row
+    constexpr bool KEEP = NT < kJoinMaxThreads;  // else the parameters are read again for each row
     float ks[V], kg1[V], kb1[V], kg2[V];
     if (KEEP) {
         param_v(ks, a.scale, c, live, 1.f);
@@ -394,10 +397,10 @@ int join_threads(int H, int d) { return (H * d / V + 31) / 32 * 32; }
 // take 88 and 209 us (136 and 279 with eight blocks an SM, 6 heads of 64 and 65,536 rows
 // 149 instead of 205, of which a third had to wait for a second round). The count depends
 // on the shape alone, so the order of the parameter sums is the same in every call. Rows
-// of more than 1024 channels leave one or two blocks an SM, whose phases overlap less:
-// 8192 rows of 4096, backward, 359 us at a floor of 146.
+// of more than 1536 channels leave one block an SM, whose phases overlap with nothing:
+// 8192 rows of 4096, backward, 360 us at a floor of 146.
 int join_blocks(long long rows, int nt, bool bwd) {
-    const int per_sm = (bwd && nt <= kJoinThreads ? 384 : 512) / nt;
+    const int per_sm = (bwd && nt <= 384 ? 384 : 512) / nt;
     const long long n = 148LL * (per_sm < 1 ? 1 : per_sm);
     return (int)(rows < n ? rows : n);
 }
@@ -442,7 +445,11 @@ cudaError_t launch_join_fwd(const JoinArgs &a, cudaStream_t s) {
 cudaError_t launch_join_bwd(const JoinBwdArgs &a, cudaStream_t s) {
     const int nt = join_threads(a.H, a.d), D = a.H * a.d;
     const int grid = join_blocks((long long)a.B * a.T, nt, true);
-    if (nt <= kJoinThreads) run_bwd<kJoinThreads>(a, grid, nt, s);
+    // 16,384 rows, us with the instance named and with that of 512 threads: 24 heads of 64
+    // (192) 125 / 293, 16 of 128 (256) 207 / 332, 20 of 128 (384) 282 / 588
+    if (nt <= kJoinBwdThreads) run_bwd<kJoinBwdThreads>(a, grid, nt, s);
+    else if (nt <= 256) run_bwd<256>(a, grid, nt, s);
+    else if (nt <= 384) run_bwd<384>(a, grid, nt, s);
     else run_bwd<kJoinMaxThreads>(a, grid, nt, s);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -75,6 +75,15 @@ def test_join(B, H, T, d, dt, z_bf16, rms, act):
     check(make(B, H, T, d, dt, z_bf16, seed=H * d + T), dt, rms=rms, act=act)
 
 
+@pytest.mark.parametrize("dt,z_bf16", [("bf16", False), ("fp32", True)])
+@pytest.mark.parametrize("rms,act", [(False, "sigmoid"), (True, "silu")])
+@pytest.mark.parametrize("B,H,T,d", [(1, 24, 500, 64), (2, 16, 150, 128), (1, 20, 333, 128),
+                                     (1, 1, 190, 2056), (1, 30, 170, 128)])
+def test_join_wide_rows(B, H, T, d, dt, z_bf16, rms, act):
+    """Rows of more than 1024 channels, in every size of block; more rows than blocks."""
+    check(make(B, H, T, d, dt, z_bf16, seed=H + T), dt, rms=rms, act=act)
+
+
 @pytest.mark.parametrize("absent", [("gate",), ("scale",), ("gamma1", "beta1"), ("beta1", "beta2"),
                                     ("gamma2", "beta2"), ("gate",) + PARAMS])
 def test_join_optional_inputs(absent):
