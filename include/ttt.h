@@ -492,8 +492,8 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  * Supported: any T >= 1, dk and dv in {64, 128}, TTT_BF16 or TTT_FP32.
  *   Deterministic. The weight, the sums over tokens and the decays are held
  *   in fp32 (their products on the tensor cores take an fp32 operand as two
- *   fp16 terms under a power-of-two scale, 22 significant bits); with
- *   TTT_F_Z_BF16 the products that only Z depends on take one term.
+ *   fp16 terms under a power-of-two scale, 22 significant bits). A bf16 Z is
+ *   the fp32 Z rounded, bit for bit.
  * flags: TTT_F_W0_PER_SEQ, TTT_F_Z_BF16.
  */
 TTT_API size_t ttt_delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,

@@ -569,13 +569,12 @@ struct ScanArgs {
 };
 
 // Bytes of a stage of the chain's ring (K, H with two terms, vectors) and of Z's (Q, M
-// with one term or two, vectors).
+// with two terms, vectors).
 template <int DK, bool BF16>
 constexpr int chain_stage_bytes() { return ((BF16 ? 1 : 2) + 2) * C * DK * 2 + kHalfVecBytes; }
 template <int DK, bool BF16, int MODE>
 constexpr int z_stage_bytes() {
-    return MODE == kSave ? 0
-                         : (BF16 ? 1 : 2) * C * DK * 2 + (MODE == kZ32 ? 2 : 1) * kImg + kHalfVecBytes;
+    return MODE == kSave ? 0 : (BF16 ? 1 : 2) * C * DK * 2 + 2 * kImg + kHalfVecBytes;
 }
 // Where the 16-byte unit `part` of a token's 16 columns of V stands: rows of 32 bytes
 // (bf16) with the halves of every other four swapped, so that the eight rows of an
@@ -612,12 +611,12 @@ __device__ __forceinline__ void load_v(float4 (&v)[2], const char *vt, int row0,
 
 // Behind the stages: the four warps' shares of X [to][from][2 tiles], and, twice for
 // the chunks in turn, V [64][16], the terms of X [4 blocks][hi, lo], 1 / their
-// scales and those of W^T, the terms of W^T [DK / 16][hi, (lo)].
+// scales and those of W^T, the terms of W^T [DK / 16][hi, lo].
 template <bool BF16>
 constexpr int scan_v_bytes() { return C * 16 * (BF16 ? 2 : 4); }
 template <int DK, bool BF16, int MODE>
 constexpr int scan_turn_bytes() {
-    return scan_v_bytes<BF16>() + 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * (MODE == kZ32 ? 2 : 1));
+    return scan_v_bytes<BF16>() + 4096 + 512 + (MODE == kSave ? 0 : DK / 16 * 512 * 2);
 }
 template <int DK, bool BF16, int MODE, int MT>
 constexpr int scan_area_bytes() { return MT * (16 * 1024 + 2 * scan_turn_bytes<DK, BF16, MODE>()); }
@@ -652,7 +651,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     __shared__ uint64_t full[4], empty[4], zfull[4], zempty[4];
     __shared__ uint64_t tready[2], zready[2];  // for the chunks in turn
     __shared__ int abort_flag;
-    constexpr bool ZF = MODE == kZ32, SAVE = MODE == kSave;
+    constexpr bool SAVE = MODE == kSave;
     constexpr int STAGE = chain_stage_bytes<DK, BF16>(), ZSTAGE = z_stage_bytes<DK, BF16, MODE>();
     constexpr int KIMG = C * DK * 2, KALL = KIMG * (BF16 ? 1 : 2);
     constexpr int NT = DK / 32, KK = DK / 64;  // 8-column tiles and 16-deep steps of a quarter
@@ -750,7 +749,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
             const size_t ks = (size_t)(slot0 + c) * a.Hk + hk, hs = (size_t)(slot0 + c) * a.H + h;
             mbar_arrive_expect_tx(bar, ZSTAGE);
             bulk_load(d, a.im.Q + ks * KALL, KALL, bar);
-            bulk_load(d + KALL, a.im.M + hs * 2 * kImg, (ZF ? 2 : 1) * kImg, bar);
+            bulk_load(d + KALL, a.im.M + hs * 2 * kImg, 2 * kImg, bar);
             bulk_load(d + ZSTAGE - kHalfVecBytes, a.im.vec + hs * kVecBytes + kHalfVecBytes,
                       kHalfVecBytes, bar);
         };
@@ -784,7 +783,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                 const char *at = turn_at(turn, m);
                 const uint4 *xfr = reinterpret_cast<const uint4 *>(at + VB) + lane;        // [block][hi, lo][32]
                 const float *iXs = reinterpret_cast<const float *>(at + VB + 4096), *iSs = iXs + 64;
-                const uint4 *sfr = reinterpret_cast<const uint4 *>(at + VB + 4096 + 512) + lane;  // [step][hi, (lo)][32]
+                const uint4 *sfr = reinterpret_cast<const uint4 *>(at + VB + 4096 + 512) + lane;  // [step][hi, lo][32]
                 float Z[2][4] = {}, ZM[2][4] = {};
                 // (Q W)^T of block p, quarter by quarter
 #pragma unroll
@@ -792,23 +791,19 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                     float z[2][4] = {};
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        const uint4 *d = sfr + 32 * (ZF ? 2 : 1) * (w * KK + kk);
-                        const uint4 fh = d[0];
-                        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w};
+                        const uint4 *d = sfr + 64 * (w * KK + kk);
+                        const uint4 fh = d[0], fl = d[32];
+                        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lo[4] = {fl.x, fl.y, fl.z, fl.w};
                         uint32_t bb[4];
                         load_b(bb, uQ, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
-                        if (ZF) {
-                            const uint4 fl = d[32];
-                            const uint32_t lo[4] = {fl.x, fl.y, fl.z, fl.w};
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
-                            if (!BF16) {
-                                load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
+                        for (int x = 0; x < 2; ++x) mma_f16(z[x], lo, bb[2 * x], bb[2 * x + 1]);
+                        if (!BF16) {
+                            load_b(bb, uQ + KIMG, 16 * p, w * (DK / 4) + 16 * kk, lane);
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
-                            }
+                            for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bb[2 * x], bb[2 * x + 1]);
                         }
                     }
                     const float i0 = iSs[16 * w + gq], i1 = iSs[16 * w + gq + 8];
@@ -830,13 +825,11 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                        if (ZF) mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
+                        mma_f16(z[x], lo, bm[2 * x], bm[2 * x + 1]);
                     }
-                    if (ZF) {
-                        load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
+                    load_b(bm, uM + kImg, 16 * p, 16 * jj, lane);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
-                    }
+                    for (int x = 0; x < 2; ++x) mma_f16(z[x], hi, bm[2 * x], bm[2 * x + 1]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -861,7 +854,7 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                 for (int x = 0; x < 2; ++x) {
                     const int i = c * C + 16 * p + 8 * x;
                     const float(&z)[4] = Z[x];
-                    if (ZF) {
+                    if (MODE == kZ32) {
                         const int t = i + 2 * q4;
                         float *o = static_cast<float *>(a.Z) + (vrow + t) * a.dv + v0 + 16 * m + gq;
                         if (t < len) o[0] = z[0], o[8] = z[2];
@@ -952,9 +945,9 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
                     add(X[m], lo);
                     if (!SAVE) {
                         uint4 *d = reinterpret_cast<uint4 *>(turn_at(turn, m) + VB + 4096 + 512) + lane +
-                                   32 * (ZF ? 2 : 1) * (p * KK + kk);
+                                   64 * (p * KK + kk);
                         d[0] = make_uint4(hi[m][0], hi[m][1], hi[m][2], hi[m][3]);
-                        if (ZF) d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        d[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 if (!BF16) {
