@@ -150,14 +150,10 @@ __global__ void __launch_bounds__(352, 1) delta_rev_kernel(RevArgs a) {
         if (lane == 0) {
             if (warp == 8) {
                 Filler<decltype(chain_copy)> f(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
-                while (f.filled < nchunk && f.next()) {
-                }
-                if (*abort) f.drain();
+                f.run();
             } else {
                 Filler<decltype(z_copy)> f(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
-                while (f.filled < nchunk && f.next()) {
-                }
-                if (*abort) f.drain();
+                f.run();
             }
         }
         return;

@@ -755,15 +755,11 @@ __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
         };
         if (lane == 0 && warp == 8) {
             Filler<decltype(chain_copy)> f(full, empty, a.stages, nchunk, abort, a.status, chain_copy);
-            while (f.filled < nchunk && f.next()) {
-            }
-            if (*abort) f.drain();
+            f.run();
         }
         if (lane == 0 && warp == 9 && !SAVE) {
             Filler<decltype(z_copy)> f(zfull, zempty, a.zstages, nchunk, abort, a.status, z_copy);
-            while (f.filled < nchunk && f.next()) {
-            }
-            if (*abort) f.drain();
+            f.run();
         }
         return;
     }

@@ -22,8 +22,14 @@
 
 namespace ttt {
 namespace delta {
-
 using namespace sm100;
+}  // namespace delta
+}  // namespace ttt
+
+#include "ttt_delta_ring.cuh"
+
+namespace ttt {
+namespace delta {
 
 constexpr int C = kDeltaC;
 constexpr int kImg = C * C * 2;  // bytes of a 64 x 64 fp16 image
@@ -135,49 +141,6 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
 }
 
 constexpr int kScanSmem = 231936;  // dynamic shared memory a scan may take (227 KB less its barriers)
-constexpr int kScanStatus = 61;  // a wait of the scans has run out
-
-// Place in a ring of stages: the stage and the parity of its use, without divisions.
-struct Ring {
-    int stages, s = 0, ph = 0;
-    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
-    __device__ __forceinline__ void next() {
-        if (++s == stages) s = 0, ph ^= 1;
-    }
-};
-
-// What one thread needs to keep a ring of stages filled. copy(step, stage, bar)
-// issues the copies of a step after announcing their bytes on the barrier.
-template <class Copy>
-struct Filler {
-    uint64_t *full, *empty;
-    Copy copy;
-    int steps, filled;
-    Ring to;
-    volatile int *abort;
-    int *status;
-    __device__ __forceinline__ Filler(uint64_t *f, uint64_t *e, int stages, int n, volatile int *ab,
-                                      int *st, Copy c)
-        : full(f), empty(e), copy(c), steps(n), filled(0), to(stages), abort(ab), status(st) {}
-    __device__ __forceinline__ void put() {
-        copy(filled, to.s, &full[to.s]);
-        ++filled;
-        to.next();
-    }
-    // The next step, waiting for its stage; false when a wait has run out.
-    __device__ __forceinline__ bool next() {
-        if (filled >= to.stages && !mbar_wait(&empty[to.s], to.ph ^ 1, abort, status, kScanStatus))
-            return false;
-        put();
-        return true;
-    }
-    // After an abort: copies in flight land before the block's shared memory goes.
-    __device__ __forceinline__ void drain() {
-        Ring r(to.stages);
-        for (int i = 0; i < filled; ++i, r.next())
-            if (i >= filled - to.stages) mbar_drain(&full[r.s], r.ph);
-    }
-};
 
 // Counts this warp in at a barrier that others wait at.
 __device__ __forceinline__ void named_arrive(int id, int nthreads) {
