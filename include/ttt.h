@@ -563,6 +563,8 @@ TTT_API ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V,
  * R may be X. Norm is LayerNorm with the population variance, or with
  * TTT_F_RMS RMSNorm x / sqrt(mean(x^2) + eps); eps > 0. act is SiLU, or with
  * TTT_F_GATE_SIGMOID the sigmoid. h is the norm of r as stored. Sums in fp32.
+ * Squares whose sum leaves fp32 (finite channels of about 1e18 and more) count as
+ * an infinite norm: the normed row or head is its beta, no gradient goes through it.
  * Supported: H = 1 with d a multiple of 8, or d in {16, 32, 64, 128, 256}; D <= 4096.
  * flags: TTT_F_Z_BF16, TTT_F_RMS, TTT_F_GATE_SIGMOID.
  */

@@ -148,9 +148,10 @@ __device__ __forceinline__ float norm_v(float (&x)[V], float inv_n, float eps, b
 #pragma unroll
         for (int j = 0; j < V; ++j) x[j] = live ? x[j] - m : 0.f;
     }
-    // the fast root and one Newton step: within an ulp of the exact quotient
+    // the fast root and one Newton step: within an ulp of the exact quotient. A sum of
+    // squares above fp32's range gives a factor of 0 (the step would make it inf * 0); NaN stays.
     const float q = sum(dot_v(x, x)) * inv_n + eps, y = rsqrtf(q);
-    const float i = y * fmaf(-0.5f * q * y, y, 1.5f);
+    const float i = q < INFINITY ? y * fmaf(-0.5f * q * y, y, 1.5f) : y;
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] *= i;
     return i;
