@@ -494,6 +494,9 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  *   in fp32 (their products on the tensor cores take an fp32 operand as two
  *   fp16 terms under a power-of-two scale, 22 significant bits). A bf16 Z is
  *   the fp32 Z rounded, bit for bit.
+ * No output (the workspace is one) may overlap an input or another output, but
+ *   that Z may be V and W_out, with TTT_F_W0_PER_SEQ, W0 (the same address and
+ *   size); else TTT_ERR_ARG.
  * flags: TTT_F_W0_PER_SEQ, TTT_F_Z_BF16.
  */
 TTT_API size_t ttt_delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,
@@ -517,6 +520,9 @@ TTT_API ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, co
  * 256-byte aligned, clobbered (per chunk of 64 tokens and head 8 dk dv + 256 dv
  * bytes for the weights and gradients at its ends, and the forward's images);
  * calls that share one must not overlap on the GPU. Deterministic: no atomics.
+ * No output may overlap an input or another output, but that dQ, dK, dV, deta,
+ * dg and dW0 may each be the fp32 input whose gradient it is, and dW0 dW_out
+ * (the same address and size); else TTT_ERR_ARG. dV may not be dZ.
  * flags: TTT_F_W0_PER_SEQ.
  */
 TTT_API size_t ttt_delta_bwd_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv,
@@ -540,7 +546,8 @@ TTT_API ttt_status ttt_delta_bwd(const void *Q, const void *K, const void *V, co
  *               beyond the index, and its Z is left as it was. The indices
  *               of the other rows must be distinct: two rows of one call that
  *               name one state race on it.
- * Arguments otherwise as ttt_delta_fwd. No workspace. flags: TTT_F_Z_BF16.
+ * Arguments otherwise as ttt_delta_fwd. No workspace. Z may be V; Z and W overlap
+ * nothing else (TTT_ERR_ARG). flags: TTT_F_Z_BF16.
  */
 TTT_API ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V, const float *eta,
                                     const float *g, float *W, void *Z, const int *state_index,

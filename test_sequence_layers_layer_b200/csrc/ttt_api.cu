@@ -13,6 +13,7 @@
 #include "ttt_common.cuh"
 #include "ttt_delta.cuh"
 #include "ttt_join.cuh"
+#include "ttt_overlap.h"
 
 namespace ttt {
 
@@ -714,6 +715,15 @@ static ttt_status check_delta_shape(int B, int Hk, int H, int T, int dk, int dv,
     return TTT_OK;
 }
 
+// Bytes of the rule's arrays.
+struct DeltaBytes {
+    size_t qk, v, gate, state, starts;  // Q or K, V, eta or g, one weight of every head, offsets
+    DeltaBytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq, ttt_dtype dt)
+        : qk((size_t)B * Hk * T * dk * (dt == TTT_BF16 ? 2 : 4)),
+          v((size_t)B * H * T * dv * (dt == TTT_BF16 ? 2 : 4)), gate((size_t)B * H * T * 4),
+          state((size_t)H * dk * dv * 4), starts(((size_t)n_seq + 1) * 4) {}
+};
+
 size_t ttt_delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int n_seq,
                                  ttt_dtype dt) {
     const int N = n_seq > 0 ? n_seq : B;
@@ -747,9 +757,17 @@ ttt_status ttt_delta_fwd(const void *Q, const void *K, const void *V, const floa
     const void *ptrs[] = {Q, K, V, eta, g, W0, Z, W_out, seq_start, need ? workspace : nullptr};
     st = check_device_ptrs(ptrs, 10);
     if (st != TTT_OK) return st;
+    const bool per_seq = flags & TTT_F_W0_PER_SEQ, z_bf16 = flags & TTT_F_Z_BF16;
+    const DeltaBytes n(B, Hk, H, T, dk, dv, n_seq, dt);
+    const Range in[] = {{Q, n.qk}, {K, n.qk}, {V, n.v}, {eta, n.gate}, {g, n.gate},
+                        {W0, (per_seq ? N : 1) * n.state}, {seq_start, n.starts}};
+    // a block reads the columns of V and W0 that it writes, and no others
+    const OutRange out[] = {{{Z, (size_t)B * H * T * dv * (z_bf16 ? 2 : 4)}, 1u << 2},
+                            {{W_out, N * n.state}, 1u << 5},
+                            {{workspace, need}, 0}};
+    if (outputs_clash(out, in)) return TTT_ERR_ARG;
     const DeltaArgs a{Q, K, V, eta, g, W0, Z, W_out, seq_start, B, Hk, H, T, dk, dv, N, q_scale,
-                      dt == TTT_BF16, (flags & TTT_F_W0_PER_SEQ) != 0,
-                      (flags & TTT_F_Z_BF16) != 0, workspace};
+                      dt == TTT_BF16, per_seq, z_bf16, workspace};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     timing_begin(cs);
     return launched(launch_delta_fwd(a, cs));
@@ -789,9 +807,24 @@ ttt_status ttt_delta_bwd(const void *Q, const void *K, const void *V, const floa
     if (st != TTT_OK) return st;
     st = check_device_ptrs(ptrs, 16);
     if (st != TTT_OK) return st;
+    const bool per_seq = flags & TTT_F_W0_PER_SEQ;
+    const DeltaBytes n(B, Hk, H, T, dk, dv, n_seq, dt);
+    const size_t w0 = (per_seq ? N : 1) * n.state;
+    const Range in[] = {{Q, n.qk}, {K, n.qk}, {V, n.v}, {eta, n.gate}, {g, n.gate}, {W0, w0},
+                        {dZ, (size_t)B * H * T * dv * 4}, {dW_out, N * n.state},
+                        {seq_start, n.starts}};
+    // Q, K, V, g and W0 are read before the first gradient is written; eta and dW_out by the
+    // block that writes over them. dZ is read again once dV is there.
+    const OutRange out[] = {{{dQ, (size_t)B * Hk * T * dk * 4}, 1u << 0},
+                            {{dK, (size_t)B * Hk * T * dk * 4}, 1u << 1},
+                            {{dV, (size_t)B * H * T * dv * 4}, 1u << 2},
+                            {{deta, n.gate}, 1u << 3},
+                            {{dg, n.gate}, 1u << 4},
+                            {{dW0, w0}, 1u << 5 | 1u << 7},
+                            {{workspace, ttt_delta_bwd_workspace_bytes(B, Hk, H, T, dk, dv, n_seq, dt)}, 0}};
+    if (outputs_clash(out, in)) return TTT_ERR_ARG;
     const DeltaBwdArgs a{{Q, K, V, eta, g, W0, nullptr, nullptr, seq_start, B, Hk, H, T, dk, dv, N,
-                          q_scale, dt == TTT_BF16, (flags & TTT_F_W0_PER_SEQ) != 0, false,
-                          workspace},
+                          q_scale, dt == TTT_BF16, per_seq, false, workspace},
                          dZ, dW_out, dQ, dK, dV, deta, dg, dW0};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     timing_begin(cs);
@@ -815,6 +848,12 @@ ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V, const f
     const void *ptrs[] = {Q, K, V, eta, g, W, Z, state_index};
     st = check_device_ptrs(ptrs, 8);
     if (st != TTT_OK) return st;
+    const DeltaBytes by(B, Hk, H, n, dk, dv, B - 1, dt);  // B indices
+    const Range in[] = {{Q, by.qk}, {K, by.qk}, {V, by.v}, {eta, by.gate}, {g, by.gate},
+                        {state_index, by.starts}};
+    const OutRange out[] = {{{Z, (size_t)B * H * n * dv * (flags & TTT_F_Z_BF16 ? 2 : 4)}, 1u << 2},
+                            {{W, n_slots * by.state}, 0}};
+    if (outputs_clash(out, in)) return TTT_ERR_ARG;
     const DeltaArgs a{Q, K, V, eta, g, nullptr, Z, nullptr, nullptr, B, Hk, H, n, dk, dv, B,
                       q_scale, dt == TTT_BF16, true, (flags & TTT_F_Z_BF16) != 0, nullptr};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
