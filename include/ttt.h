@@ -572,6 +572,8 @@ TTT_API ttt_status ttt_delta_decode(const void *Q, const void *K, const void *V,
  * TTT_F_GATE_SIGMOID the sigmoid. h is the norm of r as stored. Sums in fp32.
  * Squares whose sum leaves fp32 (finite channels of about 1e18 and more) count as
  * an infinite norm: the normed row or head is its beta, no gradient goes through it.
+ * R and Hn overlap no input and not one another, but that R may be X or gate, Hn
+ * gate, and with H = 1 either Z (the same address and size); else TTT_ERR_ARG.
  * Supported: H = 1 with d a multiple of 8, or d in {16, 32, 64, 128, 256}; D <= 4096.
  * flags: TTT_F_Z_BF16, TTT_F_RMS, TTT_F_GATE_SIGMOID.
  */
@@ -587,9 +589,13 @@ TTT_API ttt_status ttt_join_fwd(const void *X, const void *Z, const void *gate, 
  * outputs fp32, overwritten: dX [B][T][D], dZ [B][H][T][d] (as the backwards of
  * the layers take it), dGate [B][T][D] (with gate), and the parameters' [D]
  * gradients, each NULL where it is not wanted. post_beta is read, pre_beta is
- * not needed. dX may be dR.
+ * not needed.
  * workspace: at least ttt_join_bwd_workspace_bytes(...) bytes, 256-byte
  *   aligned, clobbered; calls that share one must not overlap on the GPU.
+ * No output (the workspace is one) may overlap an input or another output, else
+ *   TTT_ERR_ARG; but an output may be, at the same address and size, an input laid
+ *   out as it is: dX R, gate or dR; dGate R, gate, dR or dH; dZ Z; a parameter's
+ *   gradient a parameter; with H = 1 also dX or dGate Z, and dZ any of those.
  * Deterministic. Shapes and flags as ttt_join_fwd.
  */
 TTT_API size_t ttt_join_bwd_workspace_bytes(int B, int H, int T, int d);

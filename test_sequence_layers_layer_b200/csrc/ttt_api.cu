@@ -887,6 +887,14 @@ ttt_status ttt_join_fwd(const void *X, const void *Z, const void *gate, const fl
     if (st != TTT_OK) return st;
     st = check_device_ptrs(ptrs, 10);
     if (st != TTT_OK) return st;
+    const size_t D = (size_t)H * d, n = (size_t)B * T * D, io = n * (dt == TTT_BF16 ? 2 : 4);
+    const Range in[] = {{X, io}, {gate, io}, {Z, n * (flags & TTT_F_Z_BF16 ? 2 : 4)},
+                        {scale, D * 4}, {post_gamma, D * 4}, {post_beta, D * 4},
+                        {pre_gamma, D * 4}, {pre_beta, D * 4}};
+    // a thread reads the places of X and gate that it writes, and with one head those of Z
+    const unsigned z = H == 1 ? 1u << 2 : 0;
+    const OutRange out[] = {{{R, io}, 1u << 0 | 1u << 1 | z}, {{Hn, io}, 1u << 1 | z}};
+    if (outputs_clash(out, in)) return TTT_ERR_ARG;
     const JoinArgs a{X, Z, gate, scale, post_gamma, post_beta, pre_gamma, pre_beta, R, Hn, B, H,
                      T, d, eps, dt == TTT_BF16, (flags & TTT_F_Z_BF16) != 0,
                      (flags & TTT_F_RMS) != 0, !(flags & TTT_F_GATE_SIGMOID)};
@@ -930,6 +938,18 @@ ttt_status ttt_join_bwd(const void *R, const void *Z, const void *gate, const fl
     if (st != TTT_OK) return st;
     st = check_device_ptrs(ptrs, 18);
     if (st != TTT_OK) return st;
+    const size_t D = (size_t)H * d, p = D * 4, n = (size_t)B * T * D, io = n * (dt == TTT_BF16 ? 2 : 4);
+    const Range in[] = {{R, io}, {gate, io}, {dR, n * 4}, {dH, n * 4},
+                        {Z, n * (flags & TTT_F_Z_BF16 ? 2 : 4)},
+                        {scale, p}, {post_gamma, p}, {post_beta, p}, {pre_gamma, p}};
+    // a thread reads the places of the token-major inputs and of Z that it writes (with one
+    // head the two are laid out alike); the parameters are read before their gradients are written
+    const unsigned rows = 0xFu, heads = 1u << 4, params = 0x1E0u, one = H == 1 ? rows | heads : 0;
+    const OutRange out[] = {{{dX, n * 4}, rows | one}, {{dGate, n * 4}, rows | one}, {{dZ, n * 4}, heads | one},
+                            {{dscale, p}, params}, {{dpost_gamma, p}, params}, {{dpost_beta, p}, params},
+                            {{dpre_gamma, p}, params}, {{dpre_beta, p}, params},
+                            {{workspace, ttt_join_bwd_workspace_bytes(B, H, T, d)}, 0}};
+    if (outputs_clash(out, in)) return TTT_ERR_ARG;
     const JoinBwdArgs a{R, Z, gate, scale, post_gamma, post_beta, pre_gamma, dR, dH, dX, dZ,
                         dGate, dscale, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta,
                         static_cast<float *>(workspace), B, H, T, d, eps, dt == TTT_BF16,
