@@ -488,7 +488,8 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  * workspace: device memory of at least ttt_delta_workspace_bytes(...) bytes,
  *   256-byte aligned, owned by the caller, clobbered. Calls that share one must
  *   not overlap on the GPU (two captured graphs that may run at the same time
- *   need one each). n_seq is 0 without seq_start.
+ *   need one each). A size of 0 (T <= 24): the call takes none, NULL will do.
+ *   n_seq is 0 without seq_start.
  * Supported: any T >= 1, dk and dv in {64, 128}, TTT_BF16 or TTT_FP32.
  *   Deterministic. The weight, the sums over tokens and the decays are held
  *   in fp32 (their products on the tensor cores take an fp32 operand as two

@@ -760,6 +760,8 @@ class _On:
     def workspace(self, given, need):
         """A workspace of `need` bytes (a given one is checked): its address and size."""
         if given is None:
+            if need == 0:  # none is used, or the call refuses its shapes
+                return None, 0
             # held to the end of the call: freed before the launch, another
             # thread's allocation on this stream could be put in its place
             self.held = self.empty(max(need, 256), self.torch.uint8)

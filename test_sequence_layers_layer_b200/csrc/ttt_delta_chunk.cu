@@ -1167,19 +1167,22 @@ cudaError_t launch_scan(const DeltaArgs &a, const Images &im, int mode, float *s
 
 using namespace delta;
 
+// Short calls go token by token: one launch instead of two, no chunk to prepare and no
+// workspace. Both sides, us of kernel time (token by token / chunked):
+//   B 1, H 4, d 64, bf16:     T 8: 12 / 24    T 24: 19 / 23     T 32: 23 / 23
+//   B 4, H 8, d 128, fp32:    T 8: 11 / 32    T 24: 19 / 32     T 48: 29 / 32
+//   B 128, H 8, d 128, bf16:  T 8: 69 / 272   T 24: 180 / 276   T 48: 342 / 279
+static bool token_by_token(int T) { return T <= 24; }
+
 size_t delta_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int N, bool packed,
                              bool bf16) {
     (void)dv;
+    if (token_by_token(T)) return 0;
     return make_plan(B, Hk, H, T, dk, N, packed, bf16, false).end;
 }
 
 cudaError_t launch_delta_fwd(const DeltaArgs &a, cudaStream_t s) {
-    // Short calls go token by token: one launch instead of two, and no chunk to
-    // prepare. Both sides, us of kernel time (token by token / chunked):
-    //   B 1, H 4, d 64, bf16:     T 8: 12 / 24    T 24: 19 / 23     T 32: 23 / 23
-    //   B 4, H 8, d 128, fp32:    T 8: 11 / 32    T 24: 19 / 32     T 48: 29 / 32
-    //   B 128, H 8, d 128, bf16:  T 8: 69 / 272   T 24: 180 / 276   T 48: 342 / 279
-    if (a.T <= 24) return launch_delta_recurrent(a, s);
+    if (token_by_token(a.T)) return launch_delta_recurrent(a, s);
     const Plan p = make_plan(a.B, a.Hk, a.H, a.T, a.dk, a.N, a.seq_start != nullptr, a.bf16, false);
     const Images im = images_at(p, a.workspace, false);
     const cudaError_t e = launch_prep(a, p, im, s);
