@@ -493,7 +493,11 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  * Supported: any T >= 1, dk and dv in {64, 128}, TTT_BF16 or TTT_FP32.
  *   Deterministic. The weight, the sums over tokens and the decays are held
  *   in fp32 (their products on the tensor cores take an fp32 operand as two
- *   fp16 terms under a power-of-two scale, 22 significant bits). A bf16 Z is
+ *   fp16 terms under a power-of-two scale: 22 significant bits for what is down
+ *   to 2^-17 of the largest value that shares its scale, one less for each further
+ *   factor of two. A row of Q or K, a column or row of the weight have scales of their own;
+ *   of what the tokens bring (V - k W and the gradients) 16 tokens may share one:
+ *   those at 16 i .. 16 i + 15 of their sequence). A bf16 Z is
  *   the fp32 Z rounded, bit for bit.
  * No output (the workspace is one) may overlap an input or another output, but
  *   that Z may be V and W_out, with TTT_F_W0_PER_SEQ, W0 (the same address and

@@ -456,7 +456,8 @@ struct GradSmem {
     static constexpr int big1 = W + (W > 2 * R ? W : 2 * R), big2 = R + 2 * kImg, big3 = 6 * kImg;
     static constexpr int big = big1 > big2 ? (big1 > big3 ? big1 : big3) : (big2 > big3 ? big2 : big3);
     static constexpr int oBig = 2 * IMG, oR = oBig + big, oF = oR + R;
-    // floats: Gh, Gl, eta, iR, iT (5 x 64), iS (128), iZ or iO (128), sums over warps (128)
+    // floats: Gh, Gl, eta, iR, iT (5 x 64), iS (128), iZ or iO (128), sums over warps (128:
+    // X's maxima 32, <W, Om> 16, 1 / scales of X 4)
     static constexpr int bytes = oF + 4 * (5 * C + 128 + 128 + 128);
 };
 
@@ -509,6 +510,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     // partial sums over the warps, in the place of rho once it is read
     float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 4 * C, *colp = dotp + 4 * C,
           *decp = colp + 4 * C, *diag = decp + 4 * C, *from = diag + C, *upto = from + C;
+    // largest sizes of the rows and columns of phi eta and E, and the three images' row scales
+    float *p_row = upto + C, *p_col = p_row + 4 * C, *e_row = p_col + 4 * C, *e_col = e_row + 4 * C, *isc = e_col + 4 * C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const int mt = warp & 3, hf = warp >> 2;
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -554,45 +557,47 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             iTs[tid] = vec[kVit * C + tid];
             eta[tid] = tid < len ? a.eta[hrow + tid] : 0.f;
         }
-        // X under one scale, and T
+        // X, 16 tokens under one scale, and T
         {
             constexpr int U = C * DV / 8 / kGradThreads;
+            constexpr int RW = 256 / DV, GW = 16 / RW;  // rows of a warp's units, warps of 16 rows
             const float *gx = a.saveX + hslot * C * DV;
-            float x[U][8], m = 0.f;
+            float x[U][8];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 get8(x[i], gx + (size_t)(tid + kGradThreads * i) * 8);
-                m = fmaxf(m, max8(x[i]));
-            }
+                float m = max8(x[i]);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) red[warp] = m;
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (lane == 0) red[16 * i + warp] = m;
+            }
             for (int u = tid; u < 2 * kImg / 16; u += kGradThreads)
                 reinterpret_cast<uint4 *>(big + SM::R)[u] =
                     reinterpret_cast<const uint4 *>(a.im.T + hslot * 2 * kImg)[u];
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < 16; ++w) m = fmaxf(m, red[w]);
-            float s, is;
-            pow2_scale(m, s, is);
-#pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int u = tid + kGradThreads * i, rw = u / (DV / 8), col = (u % (DV / 8)) * 8;
+                float m = 0.f, s, is;
+#pragma unroll
+                for (int w = 0; w < GW; ++w) m = fmaxf(m, red[16 * i + (warp & ~(GW - 1)) + w]);
+                pow2_scale(m, s, is);
                 char *d = big + img_off(rw, col);
                 put8(x[i], s, d, d + C * DV * 2);
+                if (lane == 0 && (warp & (GW - 1)) == 0) red[48 + (rw >> 4)] = is;
             }
-            if (tid == 0) red[16] = is;
         }
         __syncthreads();
         constexpr int LPR = DV / 8, RPP = kGradThreads / LPR;
         const int srow = tid / LPR, scol = (tid % LPR) * 8;
         // rho = T X: 16 tokens, a quarter of DV
         {
-            float rho[NV][4] = {}, small[NV][4] = {};
+            float rho[NV][4] = {};
             const uint32_t uT = uB + SM::R;
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 if (jj > mt) break;
+                float acc[NV][4] = {}, small[NV][4] = {};
                 uint32_t th[4], tl[4];
                 ldsm_x4(th, step16(uT + oA, jj));
                 ldsm_x4(tl, step16(uT + oA, jj) + kImg);
@@ -603,18 +608,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     ldsm_x4_t(xl, step16(uB + oX, np) + 2048 * jj + C * DV * 2);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        mma_f16(rho[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
+                        mma_f16(acc[2 * np + x], th, xh[2 * x], xh[2 * x + 1]);
                         mma_f16(small[2 * np + x], tl, xh[2 * x], xh[2 * x + 1]);
                         mma_f16(small[2 * np + x], th, xl[2 * x], xl[2 * x + 1]);
                     }
                 }
+                const float is = red[48 + jj];
+#pragma unroll
+                for (int nt = 0; nt < NV; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) rho[nt][e] = fmaf(is, acc[nt][e] + small[nt][e], rho[nt][e]);
             }
             float m[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < NV; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    rho[nt][e] = (rho[nt][e] + small[nt][e]) * (iTs[row[e >> 1]] * red[16]);
+                    rho[nt][e] *= iTs[row[e >> 1]];
                     m[e >> 1] = fmaxf(m[e >> 1], fabsf(rho[nt][e]));
                 }
 #pragma unroll
@@ -849,10 +859,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 for (int e = 0; e < 4; ++e) kk2[x][e] += ks[x][e], qk2[x][e] += qs[x][e];
         }
         __syncthreads();  // rho, W and Om are read
-        float rs[2] = {0.f, 0.f}, mx[3] = {0.f, 0.f, 0.f};
+        float rs[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f}, em[2] = {0.f, 0.f};
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-            float cs[2] = {0.f, 0.f};
+            float cs[2] = {0.f, 0.f}, qm[2] = {0.f, 0.f}, fm[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = row[e >> 1], j = 16 * hf + 8 * nt + 2 * q4 + (e & 1);
@@ -871,9 +881,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     p *= eta[j];
                     q *= eta[j];
                     // as operands: the rows of K and Q they meet carry their scales
-                    mx[0] = fmaxf(mx[0], fabsf(p * ikj));
-                    mx[1] = fmaxf(mx[1], fabsf(p * iqi));
-                    mx[2] = fmaxf(mx[2], fabsf(q) * fmaxf(ikj, iki));
+                    pm[e >> 1] = fmaxf(pm[e >> 1], fabsf(p * ikj));
+                    qm[e & 1] = fmaxf(qm[e & 1], fabsf(p * iqi));
+                    em[e >> 1] = fmaxf(em[e >> 1], fabsf(q * ikj));
+                    fm[e & 1] = fmaxf(fm[e & 1], fabsf(q * iki));
                 }
                 phi[nt][e] = p;
                 eps[nt][e] = q;
@@ -881,8 +892,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
-                if (gq == 0) colp[mt * C + 16 * hf + 8 * nt + 2 * q4 + x] = cs[x];
+                for (int o = 4; o <= 16; o <<= 1) {
+                    cs[x] += __shfl_xor_sync(0xffffffffu, cs[x], o);
+                    qm[x] = fmaxf(qm[x], __shfl_xor_sync(0xffffffffu, qm[x], o));
+                    fm[x] = fmaxf(fm[x], __shfl_xor_sync(0xffffffffu, fm[x], o));
+                }
+                const int at = mt * C + 16 * hf + 8 * nt + 2 * q4 + x;
+                if (gq == 0) colp[at] = cs[x], p_col[at] = qm[x], e_col[at] = fm[x];
             }
         }
 #pragma unroll
@@ -894,29 +910,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 w += __shfl_xor_sync(0xffffffffu, w, o);
                 k2 += __shfl_xor_sync(0xffffffffu, k2, o);
             }
-            if (q4 == 0)
-                decp[hf * C + row[x]] = d, rowp[hf * C + row[x]] = w, dotp[hf * C + row[x]] = k2;
-        }
-#pragma unroll
-        for (int y = 0; y < 3; ++y) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
-            if (lane == 0) red[48 + 16 * y + warp] = mx[y];
+            pm[x] = quad_max(pm[x]), em[x] = quad_max(em[x]);
+            const int at = hf * C + row[x];
+            if (q4 == 0) decp[at] = d, rowp[at] = w, dotp[at] = k2, p_row[at] = pm[x], e_row[at] = em[x];
         }
         __syncthreads();  // sums and maxima are there
-        float sx[3], ix[3];
-#pragma unroll
-        for (int y = 0; y < 3; ++y) {
-            float m = 0.f;
-#pragma unroll
-            for (int w = 0; w < 16; ++w) m = fmaxf(m, red[48 + 16 * y + w]);
-            pow2_scale(m, sx[y], ix[y]);
+        // a scale a row of what is multiplied: of phi eta, of its transpose, of E + E^T
+        if (tid < 3 * C) {
+            const int y = tid >> 6, i = tid & 63;
+            auto max4 = [&](const float *v) { return fmaxf(fmaxf(v[i], v[C + i]), fmaxf(v[2 * C + i], v[3 * C + i])); };
+            float s, is;
+            pow2_scale(y == 0 ? max4(p_row) : y == 1 ? max4(p_col) : fmaxf(max4(e_row), max4(e_col)), s, is);
+            isc[tid] = s;
         }
+        __syncthreads();
         char *i1 = big, *i2 = big + 2 * kImg, *i3 = big + 4 * kImg;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
             const int j0 = 16 * hf + 8 * nt + 2 * q4;
             const float k0 = iKs[j0], k1 = iKs[j0 + 1];
+            const float q0 = isc[C + j0], q1 = isc[C + j0 + 1], f0 = isc[2 * C + j0], f1 = isc[2 * C + j0 + 1];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int i = row[x];
@@ -925,16 +938,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 const float e0 = eps[nt][2 * x], e1 = eps[nt][2 * x + 1];
                 const uint32_t o = img_off(i, 16 * hf + 8 * nt) + 4 * q4;
                 uint32_t hi, lo;
-                split_f16(p0 * k0 * sx[0], p1 * k1 * sx[0], hi, lo);
+                split_f16(p0 * k0 * isc[i], p1 * k1 * isc[i], hi, lo);
                 *reinterpret_cast<uint32_t *>(i1 + o) = hi;
                 *reinterpret_cast<uint32_t *>(i1 + kImg + o) = lo;
-                split_f16(p0 * qi * sx[1], p1 * qi * sx[1], hi, lo);
+                split_f16(p0 * qi * q0, p1 * qi * q1, hi, lo);
                 *reinterpret_cast<uint32_t *>(i2 + o) = hi;
                 *reinterpret_cast<uint32_t *>(i2 + kImg + o) = lo;
                 // E + E^T: the element below the diagonal, and its mirror
                 uint32_t uh, ul;
-                split_f16(e0 * k0 * sx[2], e1 * k1 * sx[2], hi, lo);
-                split_f16(e0 * ki * sx[2], e1 * ki * sx[2], uh, ul);
+                split_f16(e0 * k0 * isc[2 * C + i], e1 * k1 * isc[2 * C + i], hi, lo);
+                split_f16(e0 * ki * f0, e1 * ki * f1, uh, ul);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int j = j0 + y;
@@ -981,6 +994,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 a.dg[hrow + 2 * lane + 1] = (float)(a1 + (lane < 31 ? later : 0.0) + (c0 + b0) + wo);
         }
         // dQ += (phi eta) K, dK += (phi eta)^T Q + (E + E^T) K
+        float ix[3][2];
+#pragma unroll
+        for (int y = 0; y < 3; ++y)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ix[y][x] = inv_pow2(isc[y * C + row[x]]);
         const uint32_t u1 = smem_u32(i1), u2 = smem_u32(i2), u3 = smem_u32(i3);
         const uint32_t oAt = img_off(rB, 16 * mt + cB);  // A read across
 #pragma unroll
@@ -1021,8 +1039,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    dQ[2 * np + x][y] = fmaf(ix[0], q[x][y], dQ[2 * np + x][y]);
-                    dK[2 * np + x][y] += fmaf(ix[1], k[x][y], ix[2] * e[x][y]);
+                    dQ[2 * np + x][y] = fmaf(ix[0][y >> 1], q[x][y], dQ[2 * np + x][y]);
+                    dK[2 * np + x][y] += fmaf(ix[1][y >> 1], k[x][y], ix[2][y >> 1] * e[x][y]);
                 }
         }
     }

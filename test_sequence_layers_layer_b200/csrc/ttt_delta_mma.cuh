@@ -68,6 +68,11 @@ __device__ __forceinline__ void pow2_scale(float amax, float &s, float &inv) {
     inv = __int_as_float((254 - f) << 23);
 }
 
+// 1 / s of a scale that pow2_scale gave.
+__device__ __forceinline__ float inv_pow2(float s) {
+    return __int_as_float((254 << 23) - __float_as_int(s));
+}
+
 __device__ __forceinline__ uint32_t h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
