@@ -497,8 +497,8 @@ TTT_API ttt_status ttt_affine_prefix(const float *M, const float *N, const float
  *   to 2^-17 of the largest value that shares its scale, one less for each further
  *   factor of two. A row of Q or K, a column or row of the weight have scales of their own;
  *   of what the tokens bring (V - k W and the gradients) 16 tokens may share one:
- *   those at 16 i .. 16 i + 15 of their sequence). A bf16 Z is
- *   the fp32 Z rounded, bit for bit.
+ *   those at 16 i .. 16 i + 15 of their sequence). Calls of at most 24 tokens, and
+ *   decode, multiply in fp32 throughout. A bf16 Z is the fp32 Z rounded, bit for bit.
  * No output (the workspace is one) may overlap an input or another output, but
  *   that Z may be V and W_out, with TTT_F_W0_PER_SEQ, W0 (the same address and
  *   size); else TTT_ERR_ARG.

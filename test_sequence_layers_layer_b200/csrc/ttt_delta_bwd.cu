@@ -13,10 +13,11 @@
 //   dg_t = sum_{i >= t} (q_i.(c D_i W dZ_i) - k_i.(D_i W dX_i))
 //          + sum_{j < t <= i} eta_j (phi_ij q_i.k_j + eps_ij k_i.k_j)
 //          + sum_{j < t} eta_j exp(G_C - G_j) k_j.(Om rho_j) + exp(G_C) <W, Om>:
-// what g_t scales, and nothing that would have to cancel (the sums of dL/dG_i from t on
-// hold every pair j, i >= t twice with opposite signs). The pairs across t come one
-// token after the other: t + 1 gains those of column t below the diagonal and loses
-// those of row t left of it.
+// what g_t scales, no sums of dL/dG_i from t on (those hold every pair j, i >= t twice with
+// opposite signs). The pairs across t come one token after the other: t + 1 gains those
+// of column t below the diagonal and loses those of row t left of it, in double, so that
+// a pair that has left leaves nothing: in fp32 the decays of tokens behind a forgetting were off
+// by 2^-24 of the largest pair in front of it.
 // The forward scan runs again first and keeps W at the start of each chunk and
 // X; the reverse scan keeps Om at its end. Everything is fp32, its products two
 // fp16 terms an operand (ttt_delta_mma.cuh). No atomics: every sum has one order.
@@ -508,10 +509,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     float *Gh = reinterpret_cast<float *>(gsm + SM::oF), *Gl = Gh + C, *eta = Gl + C, *iR = eta + C,
           *iTs = iR + C, *iS = iTs + C, *iZ = iS + 128, *iO = iZ, *rmax = iS, *red = iZ + 128;
     // partial sums over the warps, in the place of rho once it is read
-    float *rowp = reinterpret_cast<float *>(sR), *dotp = rowp + 4 * C, *colp = dotp + 4 * C,
-          *decp = colp + 4 * C, *diag = decp + 4 * C, *from = diag + C, *upto = from + C;
+    double *rowp = reinterpret_cast<double *>(sR), *colp = rowp + 4 * C, *upto = colp + 4 * C;
+    float *dotp = reinterpret_cast<float *>(upto + C), *decp = dotp + 4 * C, *diag = decp + 4 * C, *from = diag + C;
     // largest sizes of the rows and columns of phi eta and E, and the three images' row scales
-    float *p_row = upto + C, *p_col = p_row + 4 * C, *e_row = p_col + 4 * C, *e_col = e_row + 4 * C, *isc = e_col + 4 * C;
+    float *p_row = from + C, *p_col = p_row + 4 * C, *e_row = p_col + 4 * C, *e_col = e_row + 4 * C, *isc = e_col + 4 * C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const int mt = warp & 3, hf = warp >> 2;
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -859,10 +860,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                 for (int e = 0; e < 4; ++e) kk2[x][e] += ks[x][e], qk2[x][e] += qs[x][e];
         }
         __syncthreads();  // rho, W and Om are read
-        float rs[2] = {0.f, 0.f}, pm[2] = {0.f, 0.f}, em[2] = {0.f, 0.f};
+        // The sums over pairs in double: a pair comes into the running sum of dg with its
+        // column and leaves it with its row, and what stays may be 2^30 smaller (behind a
+        // forgetting). eta_j times the pair is exact in 48 bits.
+        double rs[2] = {0.0, 0.0};
+        float pm[2] = {0.f, 0.f}, em[2] = {0.f, 0.f};
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-            float cs[2] = {0.f, 0.f}, qm[2] = {0.f, 0.f}, fm[2] = {0.f, 0.f};
+            double cs[2] = {0.0, 0.0};
+            float qm[2] = {0.f, 0.f}, fm[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = row[e >> 1], j = 16 * hf + 8 * nt + 2 * q4 + (e & 1);
@@ -875,7 +881,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
                     const float w = ikj * (p * qk2[nt][e] * iqi + q * kk2[nt][e] * iki);
                     if (j < i) {
                         cs[e & 1] += w;
-                        rs[e >> 1] = fmaf(eta[j], w, rs[e >> 1]);
+                        rs[e >> 1] = fma((double)eta[j], (double)w, rs[e >> 1]);
                     } else
                         diag[i] = w;
                     p *= eta[j];
@@ -903,7 +909,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float d = dot[x], w = rs[x], k2 = ktp[x];
+            float d = dot[x], k2 = ktp[x];
+            double w = rs[x];
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
                 d += __shfl_xor_sync(0xffffffffu, d, o);
@@ -963,11 +970,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
             }
         }
         if (tid < C) {
-            auto sum4 = [&](const float *v) {
+            auto sum4 = [&](const auto *v) {
                 return (v[tid] + v[C + tid]) + (v[2 * C + tid] + v[3 * C + tid]);
             };
-            const float cs = sum4(colp), k2 = sum4(dotp);
-            if (tid < len) a.deta[hrow + tid] = (cs + diag[tid]) + k2;
+            const double cs = sum4(colp);
+            const float k2 = sum4(dotp);
+            if (tid < len) a.deta[hrow + tid] = ((float)cs + diag[tid]) + k2;
             from[tid] = sum4(decp);
             upto[tid] = eta[tid] * (cs + k2) - sum4(rowp);
         }

@@ -73,3 +73,17 @@ def test_read_out_behind_a_forgetting(dt, dk, dv, at, big, outlier):
     Z, W = ttt.delta_fwd(**x, w0_per_seq=True)
     Zr, Wr = od.delta_f64(**x, w0_per_seq=True)
     assert off(Z, Zr, at) <= 1.6e-4
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("at,big,outlier", PLACES)
+def test_gradient_of_the_decays_behind_a_forgetting(dt, dk, dv, at, big, outlier):
+    """A pair of tokens on one side of t counts nothing for g_t: it has left the running sum to the
+    last bit of 53, however large it was. At the forgetting itself nothing passes (exp(-300) of it)."""
+    x, dZ = case(dt, dk, dv, at, big, outlier)
+    args = [x[n] for n in ("Q", "K", "V", "eta", "g", "W0")]
+    got = ttt.delta_bwd(*args, dZ, None, w0_per_seq=True)["g"]
+    ref = od.delta_grads(*args, dZ, None, w0_per_seq=True)["g"]
+    assert off(got, ref, at + 1) <= 4e-4
+    assert float(got[:, :, at].abs().max()) <= 1e-12 * float(got.abs().max())
