@@ -1117,17 +1117,21 @@ cudaError_t scan_run(ScanArgs r, int N, cudaStream_t s) {
 
 template <int DK, bool BF16, int MODE>
 cudaError_t scan_inst(const ScanArgs &r, int N, cudaStream_t s) {
-    // 16 columns a block, or 32 where that saves rounds over the SMs. A chunk of 32
-    // takes 1.6 - 1.8 times one of 16 (the fragments of K and H are loaded once for
-    // both, but the chain's warps are latency-bound and have twice the work), so 32
-    // pay from a ratio of rounds of 9 : 5 on. T 2048, bf16, us with 16 / 32 columns:
-    //   d 64:   64 heads (2 rounds / 1) 74 / 63    96 (3 / 2) 108 / 117   148 (4 / 2) 143 / 119
-    //   d 128:  24 heads (2 rounds / 1) 92 / 86    48 (3 / 2) 139 / 165   148 (8 / 4) 362 / 328
+    // 16 columns a block, or 32 where that saves rounds over the SMs: the fragments of K
+    // and H are loaded once for both, but the chain's and Z's warps have twice the work. A
+    // chunk of 32 takes 1.6 - 1.8 times one of 16 at d_k = 64, so 32 pay from a ratio of
+    // rounds of 9 : 5 on, and 1.95 times at 128, where they pay if they halve the rounds.
+    // T 2048, bf16 in and out, us with 16 / 32 columns:
+    //   d 64:   64 heads (2 rounds / 1) 87 / 71   96 (3 / 2) 127 / 133   148 (4 / 2) 169 / 135
+    //           400 (11 / 6) 445 / 387
+    //   d 128:  24 heads (2 rounds / 1) 102 / 97  48 (3 / 2) 149 / 194   148 (8 / 4) 391 / 385
+    //           200 (11 / 6) 527 / 567
     // The saving scan, whose stores of W bound it, takes 16 (16 heads of 128, T 8192: 159 / 389).
     if constexpr (MODE != kSave && scan_fits<DK, BF16, MODE, 2>()) {
         const long long blocks = (long long)N * r.H * (r.dv / 16);
         const long long rounds16 = (blocks + 147) / 148, rounds32 = (blocks / 2 + 147) / 148;
-        if (9 * rounds32 < 5 * rounds16) return scan_run<DK, BF16, MODE, 2>(r, N, s);
+        if (DK == 128 ? 2 * rounds32 <= rounds16 : 9 * rounds32 < 5 * rounds16)
+            return scan_run<DK, BF16, MODE, 2>(r, N, s);
     }
     return scan_run<DK, BF16, MODE, 1>(r, N, s);
 }
