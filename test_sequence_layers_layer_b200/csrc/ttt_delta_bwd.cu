@@ -66,7 +66,7 @@ constexpr int rev_area_bytes() {
 // each), up to two chunks ahead. Two more warps fill the rings of stages, and one, the
 // gate, does the chain's waiting. Bound by the chain's latency as the forward's scan is:
 // 2 x 8192 x 8 heads of 128 in 250 us, 1.95 us a chunk (337 with dZ's parts on the
-// chain); shared memory busy 57 %, the tensor pipe 29 %, DRAM 18 %.
+// chain); shared memory busy 57 %, the tensor pipe 28 %, DRAM 17 %.
 template <int DK, bool BF16>
 __global__ void __launch_bounds__(352, 1) delta_rev_kernel(RevArgs a) {
     extern __shared__ __align__(128) char ssm[];
@@ -490,9 +490,10 @@ __device__ __forceinline__ float2 h2f(uint32_t u) {
 // holds the rows of tokens 16 mt .. 16 mt + 15 and a quarter of the columns.
 // Reads 272 KB and writes 64 KB a chunk at 128 x 128 (bf16), more than a block's
 // shared memory, so one block an SM, whose loads and products take turns. 2048 chunks of
-// 128 x 128 take 434 us (31 us a block; 107 us at the copy rate): issue slots used to
-// 30 %, shared memory 57 %, tensor pipe 26 %, DRAM 19 %; the stalls are waits for loads,
-// shared memory and barriers. Eight warps of 255 registers instead of sixteen of 128, with
+// 128 x 128 take 448 us (32 us a block; 107 us at the copy rate): issue slots used to
+// 34 %, shared memory 57 %, tensor pipe 27 %, DRAM 18 %; the stalls are waits for loads,
+// shared memory and barriers. One scale for X of a chunk and one an image of phi and E
+// took 435: tokens behind a forgetting lost their bits to those in front of it. Eight warps of 255 registers instead of sixteen of 128, with
 // dZ and dX as fragments from global memory, took 17 % longer, W asked for before rho is
 // formed 3 %. The low terms' products in the same sums as the high ones' would take 8 %
 // less, and double the gradients' errors (8e-7 of a gradient's norm instead of 4.5e-7): the
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
     float *dotp = reinterpret_cast<float *>(upto + C), *decp = dotp + 4 * C, *diag = decp + 4 * C, *from = diag + C;
     // largest sizes of the rows and columns of phi eta and E, and the three images' row scales
     float *p_row = from + C, *p_col = p_row + 4 * C, *e_row = p_col + 4 * C, *e_col = e_row + 4 * C, *isc = e_col + 4 * C;
+    static_assert((9 * 8 + 29 * 4) * C <= SM::R, "partial sums");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
     const int mt = warp & 3, hf = warp >> 2;
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) delta_grad_kernel(GradArgs a)
 #pragma unroll
             for (int np = 0; np < NK / 2; ++np) {
                 float N[2][4] = {}, Ns[2][4] = {};
-#pragma unroll 4  // all eight: more loads ahead than registers (297 bytes spilled, 36 us)
+#pragma unroll 4  // DV 128, all eight: more loads ahead than registers (297 bytes spilled, 36 us)
                 for (int kk = 0; kk < KV; ++kk) {
                     uint32_t hi[4], lo[4], wh[4], wl[4];
                     ldsm_x4(hi, step16(uZ + oA, kk));

@@ -18,12 +18,12 @@
 // inverse) and the chain has T / C steps, each of which costs latency more than
 // products; 64 is also the largest whose images, twice over, fit beside one another in
 // shared memory at dk = 128. The products are warp-level MMAs: tiles of 16 x 64 x 32
-// that follow one another through registers, of which the tensor pipe is busy 12 - 36 %
+// that follow one another through registers, of which the tensor pipe is busy 12 - 38 %
 // of the time; a tcgen05 instruction costs about 150 cycles of the chain whatever its
 // width, and its accumulators would have to come back from tensor memory at each of the
 // chain's two turns. The forward's bytes (4 dk + 4 dv + 8 a token and head with bf16 in
 // and out) are no bound: 4 x 32768 x 8 heads of 128 need 166 us at the copy rate and
-// take 1970, 730 in the preparation and 1240 in the scan.
+// take 2215, 730 in the preparation and 1485 in the scan.
 #include "../../include/ttt.h"
 #include "ttt_delta_mma.cuh"
 
@@ -638,13 +638,17 @@ constexpr int scan_area_bytes() { return MT * (16 * 1024 + 2 * scan_turn_bytes<D
 // chain's next images need not wait for Z; one thread of a warp of its own fills
 // each ring. The last warp, the gate, does the chain's waiting: a wait on an
 // mbarrier costs a warp about 150 cycles even when nothing is waited for.
-// The chain's latency is the bound: 1.4 us a chunk at dk = 128 and 1.1 us at 64 with 16
-// columns (2.6 and 1.9 with 32), of which the products are a third; shared memory is
-// busy 53 %, the tensor pipe 36 %, DRAM 16 %. 4 x 32768 x 8 heads of 128 (bf16, bf16
-// Z): 1240 us; 8 x 2048 x 12 of 64: 114 us; the saving scan of 2 x 8192 x 8 of 128
-// 159 us. Measured and not taken: two or one warps a group (1516, 2076 us for the first
-// of these, Z on the chain), eight (2142: more exchange than products), two groups of
-// 16 a block (1380), Z's stores on the chain (+ 193 cycles a chunk).
+// Latency is the bound, the chain's and, where Z is formed, that of the four warps behind it:
+// 1.5 us a chunk at dk = 128 and 1.2 us at 64 with 16 columns (2.9 and 2.2 with 32; the
+// saving scan 1.25), of which the products are a third; shared memory is busy 53 %, the
+// tensor pipe 38 %, DRAM 14 %. 4 x 32768 x 8 heads of 128 (bf16, bf16 Z): 1485 us; 8 x
+// 2048 x 12 of 64: 114 us; the saving scan of 2 x 8192 x 8 of 128 160 us. A bf16 Z takes
+// the products of an fp32 one and is rounded once: with one fp16 term an operand the
+// first of these took 1240 us, and Z was off by 2^-11 of its terms' sizes, more than its own
+// rounding where they cancel. Measured and not taken (Z with one term): two or one warps
+// a group (1516, 2076 us for the first of these, Z on the chain), eight (2142: more exchange
+// than products), two groups of 16 a block (1380), Z's stores on the chain (+ 193 cycles
+// a chunk).
 template <int DK, bool BF16, int MODE, int MT>
 __global__ void __launch_bounds__(384, 1) delta_scan_kernel(ScanArgs a) {
     extern __shared__ __align__(128) char ssm[];

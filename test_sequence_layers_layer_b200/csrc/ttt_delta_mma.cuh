@@ -1,7 +1,8 @@
 // ttt_delta_mma.cuh -- the operand form of the chunked gated delta rule.
 //
 // An fp32 operand goes to the tensor cores as two fp16 terms under a
-// power-of-two scale of its row: with the row's largest size brought into
+// power-of-two scale of its row (of what the tokens bring, 16 tokens' values of a column, or of
+// all columns in the gradients' X, may share one): with the row's largest size brought into
 // [2^13, 2^14), x s = hi + lo + e, hi = fp16(x s), lo = fp16(x s - hi) and |e| <= 2^-22
 // of |x s| (2^-25 absolute for the elements more than 2^17 below the largest): the
 // precision of fp32 products, in two or three fp16 products (lo lo is left

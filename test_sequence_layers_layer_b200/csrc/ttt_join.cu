@@ -15,8 +15,8 @@
 // shuffle among its d / 8 threads; the norm of the row a block reduction with one
 // barrier. Sums and statistics are fp32.
 // 32,768 rows of 8 x 128, bf16 with fp32 z, RMS norms: forward 76 us (403 MB at
-// 5.3 TB/s, 0.82 of the copy rate; issue slots used to 62 %), backward 160 us and 8 us
-// for the parameters' sums (940 MB at 5.6 TB/s, 0.86). Without loads ahead, with exact
+// 5.3 TB/s, 0.82 of the copy rate; issue slots used to 65 %), backward 160 us and 7 us
+// for the parameters' sums (940 MB at 5.6 TB/s, 0.87). Without loads ahead, with exact
 // divisions and two-barrier sums they took 170 and 257 us.
 //
 // The backward's parameter gradients are column sums over all rows: each block
@@ -403,12 +403,13 @@ bool join_supported(int H, int d) {
 namespace {
 int join_threads(int H, int d) { return (H * d / V + 31) / 32 * 32; }
 // Blocks of the persistent kernels: as many as are resident at 128 registers a
-// thread (168 in the backward's narrow blocks), at most one per row: 200,000 rows of 64
-// take 88 and 209 us (136 and 279 with eight blocks an SM, 6 heads of 64 and 65,536 rows
-// 149 instead of 205, of which a third had to wait for a second round). The count depends
+// thread (168 in the backward's narrow blocks), at most one per row. Times of the kernels
+// without the parameters' sums: 200,000 rows of 64 take 89 and 212 us (136 and 276 with
+// eight blocks an SM), 6 heads of 64 and 65,536 rows 151 instead of 205, of which a third
+// had to wait for a second round. The count depends
 // on the shape alone, so the order of the parameter sums is the same in every call. Rows
 // of more than 1536 channels leave one block an SM, whose phases overlap with nothing:
-// 8192 rows of 4096, backward, 360 us at a floor of 146.
+// 8192 rows of 4096, backward, 378 us at a floor of 146.
 int join_blocks(long long rows, int nt, bool bwd) {
     const int per_sm = (bwd && nt <= 384 ? 384 : 512) / nt;
     const long long n = 148LL * (per_sm < 1 ? 1 : per_sm);
@@ -456,7 +457,7 @@ cudaError_t launch_join_bwd(const JoinBwdArgs &a, cudaStream_t s) {
     const int nt = join_threads(a.H, a.d), D = a.H * a.d;
     const int grid = join_blocks((long long)a.B * a.T, nt, true);
     // 16,384 rows, us with the instance named and with that of 512 threads: 24 heads of 64
-    // (192) 125 / 293, 16 of 128 (256) 207 / 332, 20 of 128 (384) 282 / 588
+    // (192) 125 / 293, 16 of 128 (256) 200 / 332, 20 of 128 (384) 278 / 588
     if (nt <= kJoinBwdThreads) run_bwd<kJoinBwdThreads>(a, grid, nt, s);
     else if (nt <= 256) run_bwd<256>(a, grid, nt, s);
     else if (nt <= 384) run_bwd<384>(a, grid, nt, s);
